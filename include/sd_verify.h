@@ -399,6 +399,169 @@ sd_status sd_latent_compress(const void *queries, const void *features, int64_t 
 size_t sd_latent_compress_workspace_size(int frames, int N, int Cq, int d);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions
+ *
+ * No counterpart in the method's pages beyond their target models' use of it:
+ * the attention calls above take queries and keys with the rotary embedding
+ * already applied, and these calls apply it.  With R = rot_dim, pair i
+ * (0 <= i < R/2) of a head turns by the angle position * w_i:
+ *   (a, b) -> (a c - b s, b c + a s),  c = m cos(position w_i), s = m sin(position w_i)
+ * where (a, b) are elements (i, i + R/2) of the head (SD_ROPE_HALF) or
+ * (2i, 2i + 1) (SD_ROPE_INTERLEAVED); elements R .. D-1 are copied.
+ *
+ * Frequencies: w_i = theta^(-2i/R), stretched for contexts longer than the
+ * one a model was trained on:
+ *   SD_ROPE_NONE    w_i
+ *   SD_ROPE_LINEAR  w_i / factor
+ *   SD_ROPE_NTK     (theta factor^(R/(R-2)))^(-2i/R); R > 2
+ *   SD_ROPE_PARTS   (1 - g) w_i / factor + g w_i, where g rises linearly from 0
+ *                   to 1 as the pair's turns over the original context,
+ *                   original_max w_i / (2 pi), go from `low` to `high`
+ *   SD_ROPE_YARN    SD_ROPE_PARTS, and the magnitude m = 0.1 ln(factor) + 1
+ *                   ("YaRN: Efficient Context Window Extension of Large
+ *                   Language Models"); m = 1 in every other kind
+ *
+ * sd_rotary_table (host only; no GPU call) writes R/2 words, turns[i] =
+ * round(2^64 frac(w_i / (2 pi))), and the magnitude.  The kernels multiply a
+ * word by the position in 64-bit integers, which drops whole turns exactly:
+ * the angle of any int32 position is right to position * 2^-54 turns plus
+ * 2^-32, whatever its size.
+ * ------------------------------------------------------------------------ */
+typedef enum { SD_ROPE_HALF = 0, SD_ROPE_INTERLEAVED = 1 } sd_rope_layout;
+
+typedef enum {
+    SD_ROPE_NONE = 0, SD_ROPE_LINEAR = 1, SD_ROPE_NTK = 2, SD_ROPE_PARTS = 3, SD_ROPE_YARN = 4
+} sd_rope_scaling;
+
+/*   rot_dim      R, even, in [2, 1024]
+ *   theta        > 0, finite
+ *   factor       >= 1 (not read by SD_ROPE_NONE)
+ *   original_max >= 1, 0 <= low < high (read by SD_ROPE_PARTS and SD_ROPE_YARN)
+ *   turns        host memory, R/2 words; magnitude: host memory, one float */
+sd_status sd_rotary_table(int rot_dim, double theta, sd_rope_scaling scaling, double factor, int original_max,
+                          double low, double high, uint64_t *turns, float *magnitude);
+
+/* y = the rotated x.
+ *   x, y       device [N, H, D]: token n, head h at n * tok + h * head elements
+ *              (D contiguous); y may be x itself (equal pointers and strides),
+ *              else the two must not overlap
+ *   positions  device int32 [N], any value; a negative one turns back, so a
+ *              call on y with the negated positions and magnitude 1/m returns x
+ *              (and is, with magnitude m, the gradient of this call)
+ *   turns      device copy of sd_rotary_table's words, 8-byte aligned
+ *   N >= 0 (0 launches nothing), H >= 1, rot_dim <= D <= 1024
+ * 16-byte vectors are used where bases and strides allow it. */
+sd_status sd_rotary(const void *x, int64_t x_tok, int64_t x_head, void *y, int64_t y_tok, int64_t y_head,
+                    const int32_t *positions, const uint64_t *turns, float magnitude, int N, int H, int D,
+                    int rot_dim, sd_rope_layout layout, sd_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged K/V cache
+ *
+ * A pool of pages shared by all sequences instead of one block of slots per
+ * sequence: cache position i of sequence b is slot i % page_size of page
+ * table[b * table_stride + i / page_size].
+ *
+ *   k, v        device [n_pages, page_size, Hkv, D], element strides
+ *               (b: page, s: slot, h: head), D contiguous
+ *   table       device int32, row b at b * table_stride, table_cols entries
+ *               used per row; only the entries that the call's lengths reach
+ *               are read
+ * The new tokens of all sequences are packed: rows cu_q[b] .. cu_q[b+1] of a
+ * [N, ...] tensor are sequence b's (cu_q[0] = 0, non-decreasing; a sequence
+ * may have none).  kv_len[b] counts the cache positions of sequence b, the new
+ * ones among them, so new token i of q_len sits at position
+ * kv_len[b] - q_len + i.  (With ctx_len as sd_verify_attention counts it, a
+ * block of T slots is q_len = T and kv_len = ctx_len + T - 1.)
+ *
+ * Guards never trap: a cu_q entry outside [0, N] or a decreasing one, more
+ * new tokens than max_q, or a kv_len outside [0, min(max_kv, table_cols *
+ * page_size)] is clamped and sets bit 7 of the fault word; a page index
+ * outside [0, n_pages) sets bit 8 (its keys and values read as zeros, and
+ * nothing is written there).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void *k, *v;
+    sd_strides strides;
+    const int32_t *table;
+    int64_t table_stride;
+    int table_cols, n_pages, page_size;
+} sd_paged_cache;
+
+/* Rotary positions and the cache write of the new tokens in one launch: q is
+ * rotated into q_out, k is rotated into the cache, v is copied into it.
+ *   q          device [N, Hq, D], strides (q_tok, q_head); with q_out, may be
+ *              NULL (then only the cache is written)
+ *   q_out      device [N, Hq, D] contiguous (q itself when q is contiguous)
+ *   k, v       device [N, Hkv, D], strides (kv_tok, kv_head)
+ *   positions  device int32 [N], or NULL: each token's cache position
+ *   tokens of one call must not share a cache position (two sequences that
+ *   share a page share only what was written before)
+ * Rows from cu_q[B] on and all other slots are left as they were.  A token
+ * whose position is negative (kv_len < q_len) is not written and sets bit 7. */
+sd_status sd_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, const void *k, const void *v,
+                                 int64_t kv_tok, int64_t kv_head, void *q_out, const int32_t *positions,
+                                 const uint64_t *turns, float magnitude, int rot_dim, sd_rope_layout layout,
+                                 const int32_t *cu_q, const int32_t *kv_len, const sd_paged_cache *cache, int N,
+                                 int B, int Hq, int Hkv, int D, sd_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of new tokens over a paged cache
+ *
+ * sd_verify_attention with its fixed block and contiguous cache replaced by
+ * any number of new tokens per sequence (one while decoding, a block while
+ * verifying, thousands while a prompt is read in chunks, none while idle)
+ * over paged K/V that already hold them:
+ *   row i of sequence b sees cache positions [0, kv_len[b] - q_len + i]
+ *   (causal != 0) or all of [0, kv_len[b]) (causal == 0: the drafter's block);
+ *   out = sum softmax(scale q.k) v; a row that sees nothing gives zeros.
+ *
+ *   q     device [N, Hq, D], element strides (q_tok, q_head), multiples of 16 bytes
+ *   out   device [N, Hq, D] contiguous, of the inputs' dtype (fp32 sums and
+ *         softmax, one rounding at the end); rows from cu_q[B] on are left as
+ *         they were
+ *   max_q, max_kv  host upper bounds of the sequences' new tokens and kv_len
+ *   query head h reads kv head h / (Hq / Hkv); Hq / Hkv <= 64; D in {64, 128}
+ *   scale > 0, finite; B in [1, 65535]; all bases 16-byte aligned, all strides
+ *   multiples of 16 bytes
+ * Slots at and past kv_len[b] may hold anything.  Values inside a sequence are
+ * taken to be finite: bf16 weights are 0 for masked positions, and 0 times a
+ * non-finite value of a later position of the same tile is not 0.
+ * bf16 pages of a multiple of 8 slots run on the tensor cores (the softmax
+ * weights are rounded to bf16 for the second product); fp32, and other page
+ * sizes, on CUDA cores.  One launch.
+ *
+ * workspace: at least the size below, zero-filled before the first call on it;
+ * every call leaves its counters zero again (a call whose bounded wait gave up
+ * included: fault bit 3).  The size holds for every call whose N, B, max_q and
+ * max_kv are at most those given.
+ * ------------------------------------------------------------------------ */
+sd_status sd_paged_attention(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,
+                             const int32_t *cu_q, const int32_t *kv_len, int max_q, int max_kv, void *out, int N,
+                             int B, int Hq, int Hkv, int D, sd_dtype dtype, float scale, int causal,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+size_t sd_paged_attention_workspace_size(int N, int B, int max_q, int Hq, int Hkv, int D, int max_kv,
+                                         sd_dtype dtype);
+
+/* ------------------------------------------------------------------------
+ * Attention over whole prompts
+ *
+ * The same over the prompts' own keys and values, packed as the queries are
+ * (no cache): rows cu[b] .. cu[b+1] of q, k, v are sequence b's.
+ *   causal != 0: row i sees rows 0 .. i of its sequence; == 0: all of them
+ *   q     device [N, Hq, D], strides (q_tok, q_head)
+ *   k, v  device [N, Hkv, D], strides (kv_tok, kv_head)
+ *   max_len  host upper bound of the sequences' lengths
+ * Everything else as for sd_paged_attention, whose workspace of
+ * max_q = max_kv = max_len serves.
+ * ------------------------------------------------------------------------ */
+sd_status sd_prompt_attention(const void *q, int64_t q_tok, int64_t q_head, const void *k, const void *v,
+                              int64_t kv_tok, int64_t kv_head, const int32_t *cu, int max_len, void *out, int N,
+                              int B, int Hq, int Hkv, int D, sd_dtype dtype, float scale, int causal,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Greedy acceptance without a caller workspace
  *
  * No counterpart in the method's pages: this is a convenience of the library.
@@ -441,7 +604,9 @@ int sd_version(void);                   /* 100 * major + minor */
  * current device; `clear` resets it to 0.  Bits: 0 ctx_len outside
  * [1, max_ctx]; 1 a draft id outside [0, V); 2 a logits row with no ordered
  * value (NaN); 3 a bounded wait gave up; 4 tensor-memory allocation failed;
- * 5 a tree parent outside [0, node); 6 a commit out of range (skipped). */
+ * 5 a tree parent outside [0, node); 6 a commit out of range (skipped);
+ * 7 a packed offset or cache length out of range (clamped); 8 a page index
+ * outside the pool. */
 sd_status sd_fault_word(uint32_t *out, int clear);
 
 /* Attention kernel selection, process-wide, for tests and measurement:

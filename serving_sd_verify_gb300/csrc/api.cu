@@ -3,6 +3,7 @@
 // call follows are in include/sd_verify.h.
 #include <cuda_runtime.h>
 
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -843,6 +844,306 @@ sd_status sd_latent_compress(const void *queries, const void *features, int64_t 
     cudaError_t e = launch_latent(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "latent compressor launch");
     return SD_OK;
+}
+
+// ----------------------------------------------------------------------------
+// rotary positions, paged cache, packed attention
+// ----------------------------------------------------------------------------
+sd_status sd_rotary_table(int rot_dim, double theta, sd_rope_scaling scaling, double factor, int original_max,
+                          double low, double high, uint64_t *turns, float *magnitude) {
+    if (!turns || !magnitude) return fail(SD_ERR_INVALID_ARG, "null table pointer");
+    if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2)
+        return fail(SD_ERR_INVALID_ARG, "rot_dim must be even and in [2, 1024]");
+    if (!(theta > 0.0) || !isfinite(theta)) return fail(SD_ERR_INVALID_ARG, "theta must be positive and finite");
+    if (scaling < SD_ROPE_NONE || scaling > SD_ROPE_YARN) return fail(SD_ERR_INVALID_ARG, "unknown rotary scaling");
+    if (scaling != SD_ROPE_NONE && (!(factor >= 1.0) || !isfinite(factor)))
+        return fail(SD_ERR_INVALID_ARG, "the scaling factor must be >= 1 and finite");
+    if (scaling == SD_ROPE_NTK && rot_dim == 2) return fail(SD_ERR_INVALID_ARG, "SD_ROPE_NTK needs rot_dim > 2");
+    const bool parts = scaling == SD_ROPE_PARTS || scaling == SD_ROPE_YARN;
+    if (parts && (original_max < 1 || !(low >= 0.0) || !(high > low) || !isfinite(high)))
+        return fail(SD_ERR_INVALID_ARG, "need original_max >= 1 and 0 <= low < high");
+    const double two_pi = 6.283185307179586476925286766559;
+    if (scaling == SD_ROPE_NTK) theta *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double w = pow(theta, -2.0 * i / rot_dim);
+        if (scaling == SD_ROPE_LINEAR) w /= factor;
+        if (parts) {
+            const double n = original_max * w / two_pi;    // turns over the original context
+            const double g = std::min(1.0, std::max(0.0, (n - low) / (high - low)));
+            w = (1.0 - g) * w / factor + g * w;
+        }
+        const double t = w / two_pi, f = t - floor(t);
+        // f <= 1 - 2^-53, so the product stays below 2^64
+        turns[i] = (uint64_t)ldexp(f, 64);
+    }
+    *magnitude = scaling == SD_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+    return SD_OK;
+}
+
+namespace {
+
+bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+sd_status check_rope(const RopeParams &p, sd_rope_layout layout) {
+    if (p.dt != SD_BF16 && p.dt != SD_FP32) return fail(SD_ERR_INVALID_ARG, "unknown dtype");
+    if (layout != SD_ROPE_HALF && layout != SD_ROPE_INTERLEAVED)
+        return fail(SD_ERR_INVALID_ARG, "unknown rotary layout");
+    if (p.N < 0) return fail(SD_ERR_INVALID_ARG, "N must be >= 0");
+    if (p.D < 1 || p.D > 1024 || p.rot < 2 || p.rot > p.D || p.rot % 2)
+        return fail(SD_ERR_INVALID_ARG, "need D <= 1024 and an even rot_dim in [2, D]");
+    if (p.Hq > 4096 || p.Hk > 4096) return fail(SD_ERR_UNSUPPORTED, "more than 4096 heads");
+    if (!(p.magnitude == p.magnitude)) return fail(SD_ERR_INVALID_ARG, "magnitude is NaN");
+    if (!p.turns || !aligned_to(p.turns, 8))
+        return fail(SD_ERR_INVALID_ARG, "the turns table must be a device pointer aligned to 8 bytes");
+    return SD_OK;
+}
+
+// strides of [n, h, D] rows: with one row (or head) the stride is not used
+bool fix_strides(int n, int h, int D, long &tok, long &head) {
+    if (h == 1) head = D;
+    if (n == 1) tok = (long)h * D;
+    return tok >= D && head >= D;
+}
+
+sd_status check_cache(const sd_paged_cache *c, int B, const int32_t *cu, const int32_t *kv_len, int Hkv, int D,
+                      size_t es, size_t align, sd_strides *st) {
+    if (!c || !c->k || !c->v || !c->table || !cu || !kv_len) return fail(SD_ERR_INVALID_ARG, "null cache pointer");
+    if (B < 1 || B > 65535) return fail(SD_ERR_INVALID_ARG, "B must be in [1, 65535]");
+    if (c->n_pages < 1 || c->page_size < 1 || c->table_cols < 1)
+        return fail(SD_ERR_INVALID_ARG, "a cache needs at least one page, slot and table column");
+    if ((long)c->page_size * c->table_cols > (1L << 40)) return fail(SD_ERR_INVALID_ARG, "the page table is too wide");
+    if (B > 1 && c->table_stride < 1) return fail(SD_ERR_INVALID_ARG, "table_stride must be >= 1");
+    *st = c->strides;
+    if (Hkv == 1) st->h = D;
+    if (c->page_size == 1) st->s = (int64_t)Hkv * D;
+    if (c->n_pages == 1) st->b = (int64_t)c->page_size * Hkv * D;
+    if (st->h < D || st->s < D || st->b < D)
+        return fail(SD_ERR_INVALID_ARG, "page strides must not overlap the D axis");
+    if (!aligned_to(c->k, align) || !aligned_to(c->v, align) || (st->h * es) % align || (st->s * es) % align ||
+        (st->b * es) % align)
+        return fail(SD_ERR_INVALID_ARG, "page bases and strides must be multiples of %zu bytes", align);
+    if (!aligned_to(c->table, 4) || !aligned_to(cu, 4) || !aligned_to(kv_len, 4))
+        return fail(SD_ERR_INVALID_ARG, "index arrays must be aligned to 4 bytes");
+    return SD_OK;
+}
+
+// ---- packed attention: units, grid and workspace
+void varlen_units(VarlenParams &p, int path) {
+    const int G = p.Hq / p.Hkv;
+    p.rows = path >= 2 ? kVarlenTcRows : varlen_generic_rows(p);
+    p.tb = path >= 2 ? 2 * (128 / G) : p.rows / G;
+    if (p.tb < 1) p.tb = 1;      // 64 rows, a group of at most 64
+    p.tile = path >= 2 ? kVarlenTcTile : kVarlenGenTile;
+}
+
+// at most `cap` CTAs, and no more than the work line of the largest batch
+// within the bounds has shares
+int varlen_grid(const VarlenParams &p, int cap) {
+    const long units = (long)p.Hkv * ((long)p.N / p.tb + p.B);
+    const long line = units * ((long)p.max_kv + kVarlenFixed);
+    return (int)std::max(1L, std::min((long)cap, line / kVarlenMinShare));
+}
+
+struct VarlenLayout {
+    size_t ctr, o, ml, total;
+};
+VarlenLayout varlen_layout(int grid, int rows, int D) {
+    VarlenLayout l;
+    l.ctr = kHeader;
+    l.o = l.ctr + align_up((size_t)grid * 4, 256);
+    l.ml = l.o + align_up((size_t)2 * grid * rows * D * 4, 256);
+    l.total = l.ml + align_up((size_t)2 * grid * rows * 8, 256);
+    return l;
+}
+
+sd_status check_varlen(const VarlenParams &p) {
+    if (p.dt != SD_BF16 && p.dt != SD_FP32) return fail(SD_ERR_INVALID_ARG, "unknown dtype");
+    if (p.N < 0 || p.B < 1 || p.B > 65535) return fail(SD_ERR_INVALID_ARG, "need N >= 0 and B in [1, 65535]");
+    if (p.Hq < 1 || p.Hkv < 1 || p.Hq % p.Hkv) return fail(SD_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
+    if (p.Hq > 4096) return fail(SD_ERR_UNSUPPORTED, "Hq must be <= 4096");
+    if (p.Hq / p.Hkv > kVarlenMaxGroup) return fail(SD_ERR_UNSUPPORTED, "Hq / Hkv must be <= %d", kVarlenMaxGroup);
+    if (p.D != 64 && p.D != 128) return fail(SD_ERR_UNSUPPORTED, "D must be 64 or 128");
+    if (p.max_q < 0 || p.max_kv < 0 || p.max_kv > (1 << 30) || p.N > (1 << 30))
+        return fail(SD_ERR_INVALID_ARG, "N, max_q and max_kv must be in [0, 2^30]");
+    if (!(p.scale > 0.f) || !isfinite(p.scale)) return fail(SD_ERR_INVALID_ARG, "scale must be positive and finite");
+    return SD_OK;
+}
+
+sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st) {
+    sd_status v = check_varlen(p);
+    if (v != SD_OK) return v;
+    if (p.N == 0) return SD_OK;
+    if (!p.q || !p.k || !p.v || !p.cu || !p.out) return fail(SD_ERR_INVALID_ARG, "null tensor pointer");
+    const size_t es = esize(p.dt);
+    if (!fix_strides(p.N, p.Hq, p.D, p.q_tok, p.q_head))
+        return fail(SD_ERR_INVALID_ARG, "query strides must not overlap the D axis");
+    if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out))
+        return fail(SD_ERR_INVALID_ARG, "tensor base addresses must be 16-byte aligned");
+    if ((p.q_tok * es) % 16 || (p.q_head * es) % 16 || (p.kv.s * es) % 16 || (p.kv.h * es) % 16)
+        return fail(SD_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
+    if (!aligned_to(p.cu, 4)) return fail(SD_ERR_INVALID_ARG, "index arrays must be aligned to 4 bytes");
+    p.max_q = std::min(p.max_q, p.N);
+    const int force = g_force_path.load();
+    int path = 1;
+    if (force != 1) {
+        if (varlen_tc_supported(p)) path = 2;
+        else if (force >= 2) return fail(SD_ERR_UNSUPPORTED, "tensor-core attention does not cover this call");
+    }
+    p.fault = fault_ptr();
+    if (!p.fault) return fail(SD_ERR_CUDA, "no CUDA device / fault word unavailable");
+    varlen_units(p, path);
+    const int cap = varlen_max_grid(path, p);
+    if (cap < 1) return fail(SD_ERR_CUDA, "the attention kernel's occupancy is unavailable");
+    int grid = varlen_grid(p, cap);
+    const VarlenLayout l = varlen_layout(grid, p.rows, p.D);
+    if (!ws || ws_bytes < l.total)
+        return fail(SD_ERR_WORKSPACE, "attention workspace too small: need %zu bytes, got %zu", l.total, ws_bytes);
+    if (!aligned16(ws)) return fail(SD_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    char *w = static_cast<char *>(ws);
+    p.ctr = reinterpret_cast<unsigned int *>(w + l.ctr);
+    p.o_part = reinterpret_cast<float *>(w + l.o);
+    p.ml_part = reinterpret_cast<float2 *>(w + l.ml);
+    p.wt = wait_test();
+    for (;;) {
+        const cudaError_t e = path == 2 ? launch_varlen_tc(p, grid, st) : launch_varlen_generic(p, grid, st);
+        if (e == cudaErrorCooperativeLaunchTooLarge && grid > 1) {
+            // a device that cannot hold that many CTAs at once (a partitioned one): any number serves
+            (void)cudaGetLastError();
+            grid = grid / 2;
+            continue;
+        }
+        if (e != cudaSuccess) return cuda_fail(e, "packed attention launch");
+        break;
+    }
+    g_last_path = path;
+    g_last_splits = grid;
+    g_last_launches = 1;
+    return SD_OK;
+}
+
+}  // namespace
+
+sd_status sd_rotary(const void *x, int64_t x_tok, int64_t x_head, void *y, int64_t y_tok, int64_t y_head,
+                    const int32_t *positions, const uint64_t *turns, float magnitude, int N, int H, int D,
+                    int rot_dim, sd_rope_layout layout, sd_dtype dtype, void *stream) {
+    RopeParams p = {};
+    p.x = x; p.y = y;
+    p.x_tok = (long)x_tok; p.x_head = (long)x_head; p.y_tok = (long)y_tok; p.y_head = (long)y_head;
+    p.positions = positions; p.turns = turns; p.magnitude = magnitude;
+    p.N = N; p.Hq = H; p.D = D; p.rot = rot_dim; p.interleaved = layout == SD_ROPE_INTERLEAVED; p.dt = dtype;
+    if (H < 1) return fail(SD_ERR_INVALID_ARG, "H must be >= 1");
+    sd_status s = check_rope(p, layout);
+    if (s != SD_OK) return s;
+    if (N == 0) return SD_OK;
+    if (!x || !y || !positions) return fail(SD_ERR_INVALID_ARG, "null tensor pointer");
+    if (!fix_strides(N, H, D, p.x_tok, p.x_head) || !fix_strides(N, H, D, p.y_tok, p.y_head))
+        return fail(SD_ERR_INVALID_ARG, "strides must not overlap the D axis");
+    if (!aligned_to(x, esize(dtype)) || !aligned_to(y, esize(dtype)) || !aligned_to(positions, 4))
+        return fail(SD_ERR_INVALID_ARG, "tensor base addresses must be aligned to their elements");
+    if (x == y && (p.x_tok != p.y_tok || p.x_head != p.y_head))
+        return fail(SD_ERR_INVALID_ARG, "in place, x and y must share strides");
+    p.copy_rest = x != y && rot_dim < D;
+    p.fault = fault_ptr();
+    if (!p.fault) return fail(SD_ERR_CUDA, "no CUDA device / fault word unavailable");
+    const cudaError_t e = launch_rope(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
+    return SD_OK;
+}
+
+sd_status sd_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, const void *k, const void *v,
+                                 int64_t kv_tok, int64_t kv_head, void *q_out, const int32_t *positions,
+                                 const uint64_t *turns, float magnitude, int rot_dim, sd_rope_layout layout,
+                                 const int32_t *cu_q, const int32_t *kv_len, const sd_paged_cache *cache, int N,
+                                 int B, int Hq, int Hkv, int D, sd_dtype dtype, void *stream) {
+    RopeParams p = {};
+    p.x = q; p.y = q_out; p.k = k; p.v = v;
+    p.x_tok = (long)q_tok; p.x_head = (long)q_head; p.y_tok = (long)Hq * D; p.y_head = D;
+    p.kv_tok = (long)kv_tok; p.kv_head = (long)kv_head;
+    p.positions = positions; p.turns = turns; p.magnitude = magnitude;
+    p.N = N; p.Hq = q ? Hq : 0; p.Hk = Hkv; p.D = D; p.rot = rot_dim;
+    p.interleaved = layout == SD_ROPE_INTERLEAVED; p.dt = dtype;
+    if ((q == nullptr) != (q_out == nullptr)) return fail(SD_ERR_INVALID_ARG, "q and q_out go together");
+    if ((q && Hq < 1) || Hkv < 1) return fail(SD_ERR_INVALID_ARG, "Hq and Hkv must be >= 1");
+    sd_status s = check_rope(p, layout);
+    if (s != SD_OK) return s;
+    const size_t es = esize(dtype);
+    s = check_cache(cache, B, cu_q, kv_len, Hkv, D, es, es, &p.pages);
+    if (s != SD_OK) return s;
+    if (N == 0) return SD_OK;
+    if (!k || !v) return fail(SD_ERR_INVALID_ARG, "null tensor pointer");
+    if (q && !fix_strides(N, Hq, D, p.x_tok, p.x_head))
+        return fail(SD_ERR_INVALID_ARG, "query strides must not overlap the D axis");
+    if (!fix_strides(N, Hkv, D, p.kv_tok, p.kv_head))
+        return fail(SD_ERR_INVALID_ARG, "key and value strides must not overlap the D axis");
+    if (q == q_out && q && ((N > 1 && p.x_tok != p.y_tok) || (Hq > 1 && p.x_head != p.y_head)))
+        return fail(SD_ERR_INVALID_ARG, "in place, q must be contiguous");
+    if ((q && (!aligned_to(q, es) || !aligned_to(q_out, es))) || !aligned_to(k, es) || !aligned_to(v, es) ||
+        !aligned_to(positions, 4))
+        return fail(SD_ERR_INVALID_ARG, "tensor base addresses must be aligned to their elements");
+    p.copy_rest = rot_dim < D;
+    p.cu = cu_q; p.kv_len = kv_len; p.B = B;
+    p.table = cache->table; p.table_stride = (long)cache->table_stride; p.table_cols = cache->table_cols;
+    p.n_pages = cache->n_pages; p.page_size = cache->page_size;
+    p.k_pages = cache->k; p.v_pages = cache->v;
+    p.fault = fault_ptr();
+    if (!p.fault) return fail(SD_ERR_CUDA, "no CUDA device / fault word unavailable");
+    const cudaError_t e = launch_rope(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rotary append launch");
+    return SD_OK;
+}
+
+sd_status sd_paged_attention(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,
+                             const int32_t *cu_q, const int32_t *kv_len, int max_q, int max_kv, void *out, int N,
+                             int B, int Hq, int Hkv, int D, sd_dtype dtype, float scale, int causal,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+    VarlenParams p = {};
+    p.q = q; p.q_tok = (long)q_tok; p.q_head = (long)q_head;
+    p.cu = cu_q; p.kv_len = kv_len; p.out = out;
+    p.N = N; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.D = D;
+    p.max_q = max_q; p.max_kv = max_kv; p.causal = causal != 0; p.scale = scale; p.dt = dtype;
+    sd_status s = check_varlen(p);
+    if (s != SD_OK) return s;
+    s = check_cache(cache, B, cu_q, kv_len, Hkv, D, esize(dtype), 16, &p.kv);
+    if (s != SD_OK) return s;
+    p.k = cache->k; p.v = cache->v;
+    p.table = cache->table; p.table_stride = (long)cache->table_stride; p.table_cols = cache->table_cols;
+    p.n_pages = cache->n_pages; p.page_size = cache->page_size;
+    return run_varlen(p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+sd_status sd_prompt_attention(const void *q, int64_t q_tok, int64_t q_head, const void *k, const void *v,
+                              int64_t kv_tok, int64_t kv_head, const int32_t *cu, int max_len, void *out, int N,
+                              int B, int Hq, int Hkv, int D, sd_dtype dtype, float scale, int causal,
+                              void *workspace, size_t workspace_bytes, void *stream) {
+    VarlenParams p = {};
+    p.q = q; p.q_tok = (long)q_tok; p.q_head = (long)q_head;
+    p.k = k; p.v = v;
+    long tok = (long)kv_tok, head = (long)kv_head;
+    p.cu = cu; p.out = out;
+    p.N = N; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.D = D;
+    p.max_q = p.max_kv = max_len; p.causal = causal != 0; p.scale = scale; p.dt = dtype;
+    sd_status s = check_varlen(p);
+    if (s != SD_OK) return s;
+    if (!fix_strides(N, Hkv, D, tok, head) && N > 0)
+        return fail(SD_ERR_INVALID_ARG, "key and value strides must not overlap the D axis");
+    p.kv.s = tok; p.kv.h = head;
+    return run_varlen(p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t sd_paged_attention_workspace_size(int N, int B, int max_q, int Hq, int Hkv, int D, int max_kv,
+                                         sd_dtype dtype) {
+    VarlenParams p = {};
+    p.N = N; p.B = B; p.max_q = max_q; p.Hq = Hq; p.Hkv = Hkv; p.D = D; p.max_kv = max_kv; p.dt = dtype;
+    p.scale = 1.f;
+    if (check_varlen(p) != SD_OK) return 0;
+    p.max_q = std::min(p.max_q, p.N);
+    // the largest of what the kernels take (which one runs also depends on the
+    // page size and a forced path): tensor cores one CTA per SM and 256 rows,
+    // CUDA cores kVarlenGenPerSm CTAs per SM of 64 rows
+    p.tb = 1;
+    const int sms = device_sm_count();
+    const int g2 = varlen_grid(p, sms), g1 = varlen_grid(p, kVarlenGenPerSm * sms);
+    return std::max(varlen_layout(g2, kVarlenTcRows, D).total, varlen_layout(g1, 64, D).total);
 }
 
 int sd_set_projector_path(int path) {

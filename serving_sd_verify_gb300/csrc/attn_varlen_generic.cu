@@ -1,0 +1,299 @@
+// Attention of packed new tokens on CUDA cores: fp32 or bf16 storage, any page
+// size, fp32 arithmetic throughout.  The tensor-core kernel takes the bf16
+// calls it can (attn_varlen_tc.cu); this one takes the rest.
+//
+// A unit is R query rows (64, or 16 where no sequence has more rows per kv
+// head than that) and its keys come in tiles of 64; units and tiles are dealt
+// out as in varlen.cuh.  256 threads as 16 x 16: thread (ty, tx) computes
+// R / 16 rows x 4 keys of S = Q K^T from transposed tiles in shared memory,
+// the 16 threads of a row find its maximum and sum by shuffles, and the same
+// thread adds P V for its rows and D / 16 of the columns, O in registers.
+// Every number of S and P V costs R / 16 x 4 multiply-adds per pair of 16-byte
+// shared loads: with 64 rows the FMA pipe is the bound (half its rate), with
+// 16 the shared-memory reads of K and V, at about the rate HBM delivers them.
+#include "varlen.cuh"
+
+#include <math.h>
+#include <atomic>
+
+namespace sdv {
+
+namespace {
+
+constexpr int kGThreads = 256;
+constexpr int kGTile = kVarlenGenTile;      // 64 keys
+constexpr float kGLog2e = 1.4426950408889634f;
+
+template <int D, int R> struct GLay {
+    static constexpr int kQs = R + 4;               // transposed rows, padded: 16-byte aligned, bank-shifted
+    static constexpr int kKs = kGTile + 4;
+    static constexpr int kQ = D * kQs;              // floats
+    static constexpr int kK = D * kKs;              // P overlays K: [kGTile][kQs]
+    static constexpr int kV = kGTile * D;
+    static constexpr int kSmem = (kQ + kK + kV) * 4;
+    static_assert(kGTile * kQs <= kK, "P fits over K");
+};
+
+// first element of key `key`'s row of the unit's kv head, or null for a bad page
+template <typename T>
+__device__ __forceinline__ const T *key_row(const VarlenParams &p, const VlUnit &u, const void *base, int key) {
+    const T *t = static_cast<const T *>(base);
+    if (!p.table) return t + (long)(u.row0 - u.tok0 + key) * p.kv.s + (long)u.g * p.kv.h;
+    const int pg = __ldg(p.table + (long)u.b * p.table_stride + key / p.page_size);
+    if (pg < 0 || pg >= p.n_pages) { set_fault(p.fault, FAULT_BAD_PAGE); return nullptr; }
+    return t + (long)pg * p.kv.b + (long)(key % p.page_size) * p.kv.s + (long)u.g * p.kv.h;
+}
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kGThreads, 2)
+attn_varlen_generic_kernel(const VarlenParams p) {
+    using L = GLay<D, R>;
+    constexpr int TM = R / 16, TN = D / 16;          // rows and output columns of a thread
+    constexpr int VP = Elem<T>::kPerVec, VPR = D / VP;
+    extern __shared__ float4 smem4[];
+    float *Qs = reinterpret_cast<float *>(smem4);    // [D][R + 4]
+    float *Ks = Qs + L::kQ;                          // [D][64 + 4]
+    float *Ps = Ks;                                  // [64][R + 4]
+    float *Vs = Ks + L::kK;                          // [64][D]
+    __shared__ VlPlan pl;
+    __shared__ VlEnds ends;
+    __shared__ int join_flag;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int cta = (int)blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid < 32) {
+        const VlPlan q = vl_plan(p, cta, (int)gridDim.x);
+        if (tid == 0) pl = q;
+    }
+    __syncthreads();
+    if (pl.idle) return;
+    const int G = p.Hq / p.Hkv;
+    const float qk = p.scale * kGLog2e;
+
+    VlWalk walk(pl);
+    VlUnit u;
+    while (walk.next(p, pl, u)) {
+        const int rows = u.ntok * G;
+        __syncthreads();
+        for (int i = tid; i < R * VPR; i += kGThreads) {       // Q, scaled, transposed
+            const int r = i % R, v = i / R;
+            float f[VP];
+            if (r < rows) {
+                const T *src = static_cast<const T *>(p.q) + (long)(u.row0 + r / G) * p.q_tok +
+                               (long)(u.g * G + r % G) * p.q_head + v * VP;
+                Elem<T>::load_vec(src, f);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VP; ++e) f[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < VP; ++e) Qs[(v * VP + e) * L::kQs + r] = f[e] * qk;
+        }
+        float o[TM][TN], m[TM], l[TM];
+        int lim[TM];
+#pragma unroll
+        for (int a = 0; a < TM; ++a) {
+            const int r = ty * TM + a;
+            lim[a] = r < rows ? vl_limit(p, u, u.tok0 + r / G) : 0;
+            m[a] = -INFINITY;
+            l[a] = 0.f;
+#pragma unroll
+            for (int e = 0; e < TN; ++e) o[a][e] = 0.f;
+        }
+        for (int t = u.t0; t < u.t1; ++t) {
+            const int key0 = t * kGTile;
+            __syncthreads();
+            for (int i = tid; i < kGTile * VPR; i += kGThreads) {
+                const int kk = i / VPR, v = i % VPR;
+                float kf[VP], vf[VP];
+                const T *kp = nullptr, *vp = nullptr;
+                if (key0 + kk < u.kv) {
+                    kp = key_row<T>(p, u, p.k, key0 + kk);
+                    vp = key_row<T>(p, u, p.v, key0 + kk);
+                }
+                if (kp) {
+                    Elem<T>::load_vec(kp + v * VP, kf);
+                    Elem<T>::load_vec(vp + v * VP, vf);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) { kf[e] = 0.f; vf[e] = 0.f; }
+                }
+#pragma unroll
+                for (int e = 0; e < VP; ++e) {
+                    Ks[(v * VP + e) * L::kKs + kk] = kf[e];
+                    Vs[kk * D + v * VP + e] = vf[e];
+                }
+            }
+            __syncthreads();
+            float s[TM][4];
+#pragma unroll
+            for (int a = 0; a < TM; ++a)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[a][c] = 0.f;
+#pragma unroll 8
+            for (int d = 0; d < D; ++d) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(Ks + d * L::kKs + 4 * tx);
+                float q[TM];
+                if constexpr (TM == 4) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(Qs + d * L::kQs + 4 * ty);
+                    q[0] = q4.x; q[1] = q4.y; q[2] = q4.z; q[3] = q4.w;
+                } else {
+                    q[0] = Qs[d * L::kQs + ty];
+                }
+#pragma unroll
+                for (int a = 0; a < TM; ++a) {
+                    s[a][0] = fmaf(q[a], k4.x, s[a][0]); s[a][1] = fmaf(q[a], k4.y, s[a][1]);
+                    s[a][2] = fmaf(q[a], k4.z, s[a][2]); s[a][3] = fmaf(q[a], k4.w, s[a][3]);
+                }
+            }
+            __syncthreads();       // K has been read; P goes over it
+#pragma unroll
+            for (int a = 0; a < TM; ++a) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (key0 + 4 * tx + c >= lim[a]) s[a][c] = -INFINITY;
+                    mx = fmaxf(mx, s[a][c]);
+                }
+#pragma unroll
+                for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                const float m_new = fmaxf(m[a], mx);
+                const float ref = m_new == -INFINITY ? 0.f : m_new;
+                const float alpha = exp2f(m[a] - ref);         // 0 while nothing is held
+                m[a] = m_new;
+                float sum = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float pv = exp2f(s[a][c] - ref);
+                    sum += pv;
+                    Ps[(4 * tx + c) * L::kQs + ty * TM + a] = pv;
+                }
+#pragma unroll
+                for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                l[a] = fmaf(l[a], alpha, sum);
+#pragma unroll
+                for (int e = 0; e < TN; ++e) o[a][e] *= alpha;
+            }
+            __syncthreads();
+#pragma unroll 4
+            for (int kk = 0; kk < kGTile; ++kk) {
+                float q[TM];
+                if constexpr (TM == 4) {
+                    const float4 q4 = *reinterpret_cast<const float4 *>(Ps + kk * L::kQs + 4 * ty);
+                    q[0] = q4.x; q[1] = q4.y; q[2] = q4.z; q[3] = q4.w;
+                } else {
+                    q[0] = Ps[kk * L::kQs + ty];
+                }
+#pragma unroll
+                for (int c = 0; c < TN; c += 4) {              // columns 64 (c / 4) + 4 tx ..: neighbours read 16 bytes each
+                    const float4 v4 = *reinterpret_cast<const float4 *>(Vs + kk * D + 16 * c + 4 * tx);
+#pragma unroll
+                    for (int a = 0; a < TM; ++a) {
+                        o[a][c] = fmaf(q[a], v4.x, o[a][c]); o[a][c + 1] = fmaf(q[a], v4.y, o[a][c + 1]);
+                        o[a][c + 2] = fmaf(q[a], v4.z, o[a][c + 2]); o[a][c + 3] = fmaf(q[a], v4.w, o[a][c + 3]);
+                    }
+                }
+            }
+        }
+        const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+        const long slot = u.t0 == 0 ? 2L * cta + 1 : 2L * cta;
+#pragma unroll
+        for (int a = 0; a < TM; ++a) {
+            const int r = ty * TM + a;
+            if (r >= rows) continue;
+            const float inv = l[a] > 0.f ? 1.f / l[a] : 0.f;
+#pragma unroll
+            for (int c = 0; c < TN; c += 4) {
+                const float4 v = make_float4(o[a][c], o[a][c + 1], o[a][c + 2], o[a][c + 3]);
+                const int c4 = 4 * c + tx;
+                if (whole)
+                    vl_store4(p, (long)(u.row0 + r / G) * p.Hq + u.g * G + r % G, c4,
+                              make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                else
+                    __stcg(reinterpret_cast<float4 *>(p.o_part) + (slot * (D / 4) + c4) * p.rows + r, v);
+            }
+            if (!whole && tx == 0) __stcg(p.ml_part + slot * p.rows + r, make_float2(m[a], l[a]));
+        }
+    }
+    if (tid < 32) {
+        const VlEnds e = vl_ends(p, pl, cta);
+        if (tid == 0) ends = e;
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid < ends.n) vl_arrive(p, ends.u[tid]);
+    for (int i = 0; i < ends.n; ++i) vl_join(p, ends.u[i], p.tb, 0, &join_flag);
+}
+
+template <typename T, int D, int R>
+int grid_of() {
+    using L = GLay<D, R>;
+    static std::atomic<int> per_sm[kMaxDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < kMaxDevices) n = per_sm[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        if (cudaFuncSetAttribute(attn_varlen_generic_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 L::kSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_varlen_generic_kernel<T, D, R>, kGThreads,
+                                                          L::kSmem) != cudaSuccess)
+            return 0;
+        n = n < kVarlenGenPerSm ? n : kVarlenGenPerSm;
+        if (dev >= 0 && dev < kMaxDevices) per_sm[dev].store(n, std::memory_order_release);
+    }
+    return n * device_sm_count();
+}
+
+template <typename T, int D, int R>
+cudaError_t launch_gen(const VarlenParams &p, int grid, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kGThreads);
+    cfg.dynamicSmemBytes = GLay<D, R>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;     // the CTAs of a shared unit wait for one another
+    attr[1].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, attn_varlen_generic_kernel<T, D, R>, p);
+}
+
+template <typename F> auto dispatch(const VarlenParams &p, F f) {
+    const bool big = varlen_generic_rows(p) == 64;
+    using bf = __nv_bfloat16;
+    if (p.dt == SD_BF16) {
+        if (p.D == 128) return big ? f.template run<bf, 128, 64>() : f.template run<bf, 128, 16>();
+        return big ? f.template run<bf, 64, 64>() : f.template run<bf, 64, 16>();
+    }
+    if (p.D == 128) return big ? f.template run<float, 128, 64>() : f.template run<float, 128, 16>();
+    return big ? f.template run<float, 64, 64>() : f.template run<float, 64, 16>();
+}
+
+struct GridOf {
+    template <typename T, int D, int R> int run() const { return grid_of<T, D, R>(); }
+};
+struct Launch {
+    const VarlenParams &p;
+    int grid;
+    cudaStream_t st;
+    template <typename T, int D, int R> cudaError_t run() const { return launch_gen<T, D, R>(p, grid, st); }
+};
+
+}  // namespace
+
+// 16 rows where they hold every sequence's rows of a kv head: nothing is then
+// computed for absent rows
+int varlen_generic_rows(const VarlenParams &p) { return (long)p.max_q * (p.Hq / p.Hkv) <= 16 ? 16 : 64; }
+
+int varlen_max_grid(int path, const VarlenParams &p) {
+    return path >= 2 ? device_sm_count() : dispatch(p, GridOf{});
+}
+
+cudaError_t launch_varlen_generic(const VarlenParams &p, int grid, cudaStream_t st) {
+    return dispatch(p, Launch{p, grid, st});
+}
+
+}  // namespace sdv

@@ -1,0 +1,753 @@
+// Attention of packed new tokens on the tensor cores, for sm_103a: bf16, over
+// the prompts' own keys or a paged cache whose pages are a multiple of 8 slots.
+//
+// For a unit (up to 256 query rows: 2 tiles of 128, each of 128 / G whole
+// tokens with their G query heads) and key tile t of 128 keys:
+//   S_t = Q K_t^T,  m = max(m, max S_t),  P_t = exp2((S_t - m) scale log2 e)
+//   O = O + P_t V_t,  l = l + sum P_t,  out = O / l
+// one pass over the keys, S and P in tensor memory, P rounded to bf16 for the
+// second product (the running sum takes P before that rounding).  The heads of
+// a group share a tile, so K and V are read once per 256 rows whatever G is,
+// and a causal edge is 128 / G tokens wide instead of 128.
+//
+// Persistent, one CTA per SM; the units' tiles are dealt out evenly (varlen.cuh).
+// Warp roles (384 threads):
+//   warp 0            TMA: Q, and K and V tiles in the order of their use through
+//                     a ring of 32 KB slots (a page at a time for a paged cache)
+//   warp 1            issues the MMAs; warp 2 allocates tensor memory; warp 3 works
+//                     out which units the CTA shares
+//   warps 4-7, 8-11   softmax, thread = row: warpgroup i owns S_i and O_i
+// The two warpgroups are two streams that alternate on the tensor pipe: while
+// one does its softmax, the other's products run.  In a unit of more than 128
+// rows stream i is row tile i and both read every K/V tile; in a smaller one
+// (decoding, block verification) the streams take the even and the odd key
+// tiles of the one row tile, and are joined at its end.
+// O is rescaled only where the running max grows by more than 2^8 (exact
+// either way: P and l use the same reference).
+// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [384,384+D);
+// P_i overlays the first 64 columns of S_i.
+// Every wait is bounded; one that gives up sets the fault word, and the CTA
+// drains its copies and MMAs before it returns.
+#include "tcgen05.cuh"
+#include "varlen.cuh"
+
+#include <math.h>
+#include <atomic>
+
+namespace sdv {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;   // 216 * 256 + 72 * 128 = 168 * 384
+constexpr int kLaunchRegs = 168;
+static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads, "register shares within the launch's");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescale = 8.0f;            // log2 units
+
+template <int D> struct Lay {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = kHalves * 128 * 128;      // Q, K or V tile: 64-column blocks of [128 rows x 128 B]
+    static constexpr int kSlots = D == 128 ? 5 : 9;
+    static constexpr int kOffQ = 0;                        // two row tiles
+    static constexpr int kOffRing = 2 * kTile;
+    static constexpr int kOffBar = kOffRing + kSlots * kTile;
+    // full[slots] empty[slots] qfull qempty sfull[2] pfull[2][2] ofull[2] ofree[2]
+    static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 2 + 2;
+    static constexpr int kOffMl = kOffBar + 8 * kBars + 8; // [2][128] max and sum of stream 1
+    static constexpr int kOffMisc = kOffMl + 2 * 128 * 4;
+    static constexpr int kSmem = kOffMisc + 256 + 1024;    // + alignment slack
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+struct Misc {
+    uint32_t tmem;
+    int abort_flag;
+    int join_flag;
+    int pad;
+    VlPlan plan;
+    VlEnds ends;
+};
+static_assert(sizeof(Misc) <= 256, "the misc area");
+
+struct RingPos {        // slot and phase of the next tile in a ring
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int n) { if (++slot == n) { slot = 0; phase ^= 1u; } }
+};
+
+// mbar_wait, inlined: a call cannot be made where the warps' register counts differ
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned int *fault) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (abort_flag && *abort_flag) return false;
+            if (global_timer() - t0 > kWaitLimitNs) {
+                if (abort_flag) *abort_flag = 1;
+                set_fault(fault, FAULT_WAIT_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const VarlenParams p, const int tpt, const int box) {
+    using L = Lay<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t base = (raw_u32 + 1023u) & ~1023u;
+    uint8_t *sbase = smem_raw + (base - raw_u32);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = (int)blockIdx.x;
+
+    const uint32_t sQ = base + L::kOffQ, sRing = base + L::kOffRing, bar0 = base + L::kOffBar;
+    auto full_bar = [&](int i) { return bar0 + 8u * i; };
+    auto empty_bar = [&](int i) { return bar0 + 8u * (L::kSlots + i); };
+    const uint32_t bar1 = bar0 + 8u * (2 * L::kSlots);
+    const uint32_t qfull_bar = bar1, qempty_bar = bar1 + 8u;
+    auto sfull_bar = [&](int i) { return bar1 + 8u * (2 + i); };             // S_i computed
+    auto pfull_bar = [&](int i, int h) { return bar1 + 8u * (4 + 2 * i + h); };   // half h of P_i written (4 warps)
+    auto ofull_bar = [&](int i) { return bar1 + 8u * (8 + i); };             // O_i complete for the unit
+    auto ofree_bar = [&](int i) { return bar1 + 8u * (10 + i); };            // O_i read out (4 warps)
+    float *ml1 = reinterpret_cast<float *>(sbase + L::kOffMl);
+    Misc *misc = reinterpret_cast<Misc *>(sbase + L::kOffMisc);
+    volatile int *abort_flag = &misc->abort_flag;
+
+    if (tid == 0) {
+        for (int i = 0; i < L::kSlots; ++i) { mbar_init(full_bar(i), 1); mbar_init(empty_bar(i), 1); }
+        mbar_init(qfull_bar, 1);
+        mbar_init(qempty_bar, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull_bar(i), 1);
+            mbar_init(pfull_bar(i, 0), 4);
+            mbar_init(pfull_bar(i, 1), 4);
+            mbar_init(ofull_bar(i), 1);
+            mbar_init(ofree_bar(i), 4);
+        }
+        misc->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&misc->tmem)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) {
+        const VlPlan q = vl_plan(p, cta, (int)gridDim.x);
+        if (lane == 0) misc->plan = q;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem;
+    const VlPlan &pl = misc->plan;
+    const int G = p.Hq / p.Hkv;
+
+    if (!pl.idle) {
+        if (warp < 4) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+            if (warp == 0) {
+                // ---------------------------------------------------------- TMA producer
+                // the whole warp: the lanes share a tile's page look-ups and copies
+                VlWalk walk(pl);
+                VlUnit u;
+                RingPos rp;
+                uint32_t qphase = 0;
+                long loads = 0, units = 0;
+                bool ok = true;
+                const int per_half = 128 / box;        // copies per 64-column block of a tile
+                while (ok && walk.next(p, pl, u)) {
+                    const int n = u.t1 - u.t0;
+                    if (n <= 0) continue;
+                    const int la = u.ntok <= tpt ? 2 : 1;
+                    const int32_t *trow = kPaged ? p.table + (long)u.b * p.table_stride : nullptr;
+                    // the lane's page of tile t
+                    auto page_of = [&](int t) {
+                        if (!kPaged) return 0;
+                        const int key = t * 128 + (lane % per_half) * box;
+                        int pg = -1;
+                        if (key < u.kv) {
+                            pg = __ldg(trow + key / p.page_size);
+                            if (pg < 0 || pg >= p.n_pages) { set_fault(p.fault, FAULT_BAD_PAGE); pg = p.n_pages; }
+                        }
+                        return pg;
+                    };
+                    auto load_tile = [&](bool is_v, int t, int pg) {
+                        if (ok && loads >= L::kSlots)
+                            ok = wait_bar(empty_bar(rp.slot), rp.phase ^ 1u, abort_flag, p.fault);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) return;
+                        const uint32_t dst = sRing + rp.slot * L::kTile, bar = full_bar(rp.slot);
+                        const CUtensorMap *map = is_v ? &tmap_v : &tmap_k;
+                        if (!kPaged) {
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
+                                tma_load_4d(dst, map, bar, 0, u.row0 - u.tok0 + t * 128, 0, u.g);
+                            }
+                        } else {
+                            const int boxes = min(per_half, (u.kv - t * 128 + box - 1) / box);
+                            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * L::kHalves));
+                            __syncwarp();
+                            const int i = lane % per_half, h = lane / per_half;
+                            if (i < boxes && h < L::kHalves)
+                                tma_load_5d(dst + h * (128 * 128) + i * box * 128, map, bar, 0,
+                                            (t * 128 + i * box) % p.page_size, h, u.g, pg);
+                        }
+                        rp.step(L::kSlots);
+                        ++loads;
+                    };
+                    int pk = page_of(u.t0), pv = pk;      // pages of the next K tile, of the V tile behind it
+                    int pk2 = 0;
+                    load_tile(false, u.t0, pk);
+                    if (n > 1) pk = page_of(u.t0 + 1);
+                    // Q once the last unit's S products have read the old one
+                    if (ok && units > 0) ok = wait_bar(qempty_bar, qphase ^ 1u, abort_flag, p.fault);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const int nq = u.ntok <= tpt ? 1 : 2;
+                        mbar_arrive_expect_tx(qfull_bar, (uint32_t)(nq * L::kHalves * 128 * G * tpt));
+                        for (int i = 0; i < nq; ++i)
+                            for (int h = 0; h < L::kHalves; ++h)
+                                tma_load_3d(sQ + i * L::kTile + h * (128 * 128), &tmap_q, qfull_bar, 64 * h, u.g * G,
+                                            u.row0 + i * tpt);
+                    }
+                    __syncwarp();
+                    qphase ^= 1u;
+                    ++units;
+                    // V of tile j and K of tile j + la, in the order of use
+                    if (la == 2 && n > 1) {
+                        load_tile(false, u.t0 + 1, pk);
+                        pk2 = pk;
+                        if (n > 2) pk = page_of(u.t0 + 2);
+                    }
+                    for (int j = 0; ok && j < n; ++j) {
+                        load_tile(true, u.t0 + j, pv);
+                        if (la == 2) {
+                            pv = pk2;
+                            if (j + 2 < n) {
+                                load_tile(false, u.t0 + j + 2, pk);
+                                pk2 = pk;
+                                if (j + 3 < n) pk = page_of(u.t0 + j + 3);
+                            }
+                        } else if (j + 1 < n) {
+                            load_tile(false, u.t0 + j + 1, pk);
+                            pv = pk;
+                            if (j + 2 < n) pk = page_of(u.t0 + j + 2);
+                        }
+                    }
+                }
+                // the copies still in flight land before the CTA's shared memory goes
+                if (*abort_flag) {
+                    const int m = (int)(loads < L::kSlots ? loads : (long)L::kSlots);
+                    RingPos a = rp;
+                    for (int i = 0; i < m; ++i) {
+                        if (a.slot == 0) { a.slot = L::kSlots - 1; a.phase ^= 1u; } else --a.slot;
+                        wait_bar(full_bar(a.slot), a.phase, nullptr, p.fault);
+                    }
+                    if (units > 0) wait_bar(qfull_bar, qphase ^ 1u, nullptr, p.fault);
+                }
+            } else if (warp == 1) {
+                // ---------------------------------------------------------- MMA issuer
+                if (lane == 0) {
+                    VlWalk walk(pl);
+                    VlUnit u;
+                    RingPos rp;
+                    uint32_t qphase = 0, pphase[2] = {0, 0}, fphase[2] = {0, 0};
+                    bool used[2] = {false, false};
+                    bool ok = true;
+                    const uint32_t idS = idesc_bf16(128, 128, false), idO = idesc_bf16(128, D, true);
+                    auto wait_tile = [&]() {
+                        ok = ok && wait_bar(full_bar(rp.slot), rp.phase, abort_flag, p.fault);
+                        tc_fence_after();
+                    };
+                    auto issue_s = [&](int i, int qt, uint32_t kb) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+                            umma_ss(tmem + 128u * i, sw128_desc(sQ + qt * L::kTile + off, 16, 1024),
+                                    sw128_desc(kb + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                        }
+                        umma_commit(sfull_bar(i));
+                    };
+                    auto issue_pv = [&](int i, uint32_t vb, bool first) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && wait_bar(pfull_bar(i, h), pphase[i], abort_flag, p.fault);
+                            if (!ok) return;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                                umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
+                                        sw128_desc(vb + kk * 16 * 128, 128 * 128, 1024), idO,
+                                        (!first || kk > 0) ? 1u : 0u);
+                        }
+                        pphase[i] ^= 1u;
+                    };
+                    // O_i free for a new unit
+                    auto claim = [&](int i) {
+                        if (used[i]) {
+                            ok = ok && wait_bar(ofree_bar(i), fphase[i], abort_flag, p.fault);
+                            tc_fence_after();
+                            fphase[i] ^= 1u;
+                        }
+                        used[i] = true;
+                    };
+                    while (ok && walk.next(p, pl, u)) {
+                        const int n = u.t1 - u.t0;
+                        if (n <= 0) continue;
+                        const bool pair = u.ntok > tpt;
+                        ok = wait_bar(qfull_bar, qphase, abort_flag, p.fault);
+                        if (!ok) break;
+                        qphase ^= 1u;
+                        wait_tile();
+                        if (!ok) break;
+                        uint32_t tile = sRing + rp.slot * L::kTile;
+                        issue_s(0, 0, tile);
+                        if (pair) issue_s(1, 1, tile);
+                        umma_commit(empty_bar(rp.slot));
+                        rp.step(L::kSlots);
+                        if (pair) {
+                            if (n == 1) umma_commit(qempty_bar);
+                            for (int j = 0; ok && j < n; ++j) {
+                                wait_tile();
+                                if (!ok) break;
+                                const RingPos vp = rp;
+                                const uint32_t vt = sRing + vp.slot * L::kTile;
+                                rp.step(L::kSlots);
+                                if (j == 0) claim(0);
+                                issue_pv(0, vt, j == 0);
+                                if (!ok) break;
+                                if (j + 1 < n) {
+                                    wait_tile();
+                                    if (!ok) break;
+                                    tile = sRing + rp.slot * L::kTile;
+                                    issue_s(0, 0, tile);
+                                } else {
+                                    umma_commit(ofull_bar(0));
+                                }
+                                if (j == 0) claim(1);
+                                issue_pv(1, vt, j == 0);
+                                if (!ok) break;
+                                umma_commit(empty_bar(vp.slot));
+                                if (j + 1 < n) {
+                                    issue_s(1, 1, tile);
+                                    umma_commit(empty_bar(rp.slot));
+                                    rp.step(L::kSlots);
+                                    if (j + 2 == n) umma_commit(qempty_bar);
+                                } else {
+                                    umma_commit(ofull_bar(1));
+                                }
+                            }
+                        } else {
+                            if (n > 1) {
+                                wait_tile();
+                                if (!ok) break;
+                                issue_s(1, 0, sRing + rp.slot * L::kTile);
+                                umma_commit(empty_bar(rp.slot));
+                                rp.step(L::kSlots);
+                            }
+                            if (n <= 2) umma_commit(qempty_bar);
+                            for (int j = 0; ok && j < n; ++j) {
+                                const int i = j & 1;
+                                wait_tile();
+                                if (!ok) break;
+                                if (j < 2) claim(i);
+                                issue_pv(i, sRing + rp.slot * L::kTile, j < 2);
+                                if (!ok) break;
+                                umma_commit(empty_bar(rp.slot));
+                                rp.step(L::kSlots);
+                                if (j + 2 < n) {
+                                    wait_tile();
+                                    if (!ok) break;
+                                    issue_s(i, 0, sRing + rp.slot * L::kTile);
+                                    umma_commit(empty_bar(rp.slot));
+                                    rp.step(L::kSlots);
+                                    if (j + 3 == n) umma_commit(qempty_bar);
+                                } else {
+                                    umma_commit(ofull_bar(i));
+                                }
+                            }
+                        }
+                    }
+                    if (!ok) *abort_flag = 1;
+                }
+                __syncwarp();
+            } else if (warp == 3) {
+                const VlEnds e = vl_ends(p, pl, cta);
+                if (lane == 0) misc->ends = e;
+            }
+        } else {
+            // -------------------------------------------------------------- softmax
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+            const int w = (warp - 4) >> 2;             // stream
+            const int r = (tid - 128) & 127;           // row of the tile = tensor-memory lane
+            const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t s_col = tmem + lane_off + 128u * w, o_col = tmem + lane_off + 256u + 128u * w;
+            const float qk = p.scale * kLog2e;
+            const int tr = r / G;                      // token of the row within its tile
+            VlWalk walk(pl);
+            VlUnit u;
+            uint32_t sphase = 0, ophase = 0, ophase1 = 0;
+            long ring = 0;                             // tiles that went through the ring before this unit
+            bool ok = true;
+            while (walk.next(p, pl, u)) {
+                const int n = u.t1 - u.t0;
+                const bool pair = u.ntok > tpt;
+                const int tl = tr + (pair && w ? tpt : 0);             // token within the unit
+                const bool row_ok = tr < tpt && tl < u.ntok;
+                const int lim = row_ok ? vl_limit(p, u, u.tok0 + tl) : 0;
+                // rows this warp has to do anything for
+                const bool warp_live = __any_sync(0xffffffffu, row_ok);
+                float m_used = -INFINITY, l = 0.f;
+                const int step = pair ? 1 : 2, la = pair ? 1 : 2;
+                const int j0 = pair ? 0 : w;
+                for (int j = j0; j < n; j += step) {
+                    const int key0 = (u.t0 + j) * 128;
+                    ok = __all_sync(0xffffffffu, wait_bar(sfull_bar(w), sphase, abort_flag, p.fault)) && ok;
+                    sphase ^= 1u;
+                    tc_fence_after();
+                    if (warp_live && key0 + 128 > u.kv && (!pair || w == 0)) {
+                        // slots past the sequence may hold anything, and 0 times that is not 0:
+                        // one stream clears those rows of the last V tile before its product
+                        const int nk = min(la, n);
+                        const long idx = ring + nk + j + min(j, n - nk);
+                        const int slot = (int)(idx % L::kSlots);
+                        ok = __all_sync(0xffffffffu, wait_bar(full_bar(slot), (uint32_t)(idx / L::kSlots) & 1u,
+                                                               abort_flag, p.fault)) && ok;
+                        uint8_t *vt = sbase + L::kOffRing + slot * L::kTile;
+                        const int v0 = u.kv - key0;
+                        // the live warps share the rows
+                        const int live = min(4, ((pair ? tpt : min(u.ntok, tpt)) * G + 31) / 32);
+                        for (int i = r; i < (128 - v0) * 8 * L::kHalves; i += 32 * live) {
+                            const int row = v0 + i / (8 * L::kHalves), ch = i % (8 * L::kHalves);
+                            *reinterpret_cast<uint4 *>(vt + (ch >> 3) * (128 * 128) + sw128_off(row, ch & 7)) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        // every live warp's rows, before any arrival lets the product start
+                        named_sync(3 + w, 32 * live);
+                    }
+                    if (warp_live) {
+                        uint32_t s[4][32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32_async(s_col + 32u * c, s[c]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld_bind(s[c]);
+                        const int vis = lim - key0;                     // this row sees keys [0, vis) of the tile
+                        if (!__all_sync(0xffffffffu, vis >= 128 || !row_ok)) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (32 * c + e >= vis) s[c][e] = 0xff800000u;
+                        }
+                        float mx[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t *src = s[i >> 1] + 16 * (i & 1);
+                            float m8 = __uint_as_float(src[0]);
+#pragma unroll
+                            for (int e = 1; e < 16; ++e) m8 = fmaxf(m8, __uint_as_float(src[e]));
+                            mx[i] = m8;
+                        }
+                        const float tmax = qk * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                                      fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                        const bool need = tmax > m_used + kRescale;     // true at first while m_used = -inf
+                        float alpha = 1.f;
+                        if (need) {
+                            alpha = ex2(m_used - tmax);                 // 0 while nothing is held
+                            m_used = tmax;
+                        }
+                        if (j > j0 && __any_sync(0xffffffffu, need)) {
+                            // S_j is complete, hence every earlier product of this stream too
+                            // (they were issued before it and complete in order)
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32_async(o_col + 32u * c, o);
+                                tmem_ld_wait();
+                                tmem_ld_bind(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st32(o_col + 32u * c, o);
+                            }
+                        }
+                        l *= alpha;
+                        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                        const float2 qk2 = make_float2(qk, qk), nm2 = make_float2(neg_m, neg_m);
+                        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int q = 2 * h; q < 2 * h + 2; ++q) {     // 32 keys at a time
+                                uint32_t pk[16];
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[q][2 * c]),
+                                                                            __uint_as_float(s[q][2 * c + 1])), qk2, nm2);
+                                    const float p0 = ex2(x.x), p1 = ex2(x.y);
+                                    ls[c & 1] = __fadd2_rn(ls[c & 1], make_float2(p0, p1));
+                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+                                    pk[c] = *reinterpret_cast<const uint32_t *>(&b2);
+                                }
+                                tmem_st16(s_col + 16u * q, pk);
+                            }
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(pfull_bar(w, h));
+                        }
+                        l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
+                    } else {
+                        tc_fence_before();
+                        if (lane == 0) { mbar_arrive(pfull_bar(w, 0)); mbar_arrive(pfull_bar(w, 1)); }
+                    }
+                }
+                // ---- end of the unit: this CTA's rows, normalised, or its part of them
+                const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+                const long slot = u.t0 == 0 ? 2L * cta + 1 : 2L * cta;
+                const bool had0 = n > 0, had1 = pair ? n > 0 : n > 1;     // streams that hold anything
+                ring += 2 * n;
+                float a0 = 1.f, a1 = 0.f;
+                if (!pair) {
+                    // join the two streams of the one row tile: stream 1 leaves its max and sum
+                    if (w == 1) {
+                        ml1[r] = m_used;
+                        ml1[128 + r] = l;
+                    }
+                    named_sync(1, 256);
+                    if (w == 0) {
+                        const float m1 = ml1[r], l1 = ml1[128 + r];
+                        const float m = fmaxf(m_used, m1);
+                        a0 = m_used == -INFINITY ? 0.f : ex2(m_used - m);
+                        a1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+                        l = a0 * l + a1 * l1;
+                        m_used = m;
+                    }
+                }
+                if (pair ? (w == 0 ? had0 : had1) : (w == 0 && had0)) {
+                    ok = __all_sync(0xffffffffu, wait_bar(ofull_bar(w), ophase, abort_flag, p.fault)) && ok;
+                    ophase ^= 1u;
+                }
+                if (!pair && had1) {
+                    // both warpgroups follow stream 1's barrier, so that its phase stays known to each
+                    if (w == 0) ok = __all_sync(0xffffffffu, wait_bar(ofull_bar(1), ophase1, abort_flag, p.fault)) && ok;
+                    else ophase ^= 1u;
+                }
+                if (had1) ophase1 ^= 1u;
+                tc_fence_after();
+                if ((pair || w == 0) && warp_live) {
+                    const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                    const long orow = (long)(u.row0 + tl) * p.Hq + u.g * G + (r - tr * G);
+                    const bool dead = n <= 0;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        if (!dead) {
+                            tmem_ld32_async(o_col + 32u * c, o);
+                            tmem_ld_wait();
+                            tmem_ld_bind(o);
+                        }
+                        float f[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = dead ? 0.f : __uint_as_float(o[e]) * (a0 * inv);
+                        if (!pair && had1) {
+                            tmem_ld32_async(o_col + 128u + 32u * c, o);
+                            tmem_ld_wait();
+                            tmem_ld_bind(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), a1 * inv, f[e]);
+                        }
+                        if (row_ok && ok) {
+                            if (whole) {
+                                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + orow * D + 32 * c;
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8) {
+                                    uint4 v;
+                                    uint32_t *vw = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) {
+                                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[e + 2 * q], f[e + 2 * q + 1]);
+                                        vw[q] = *reinterpret_cast<const uint32_t *>(&b2);
+                                    }
+                                    *reinterpret_cast<uint4 *>(dst + e) = v;
+                                }
+                            } else {
+                                float4 *dst = reinterpret_cast<float4 *>(p.o_part) +
+                                              (slot * (D / 4) + 8 * c) * kVarlenTcRows + 128 * (pair ? w : 0) + r;
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    __stcg(dst + (e / 4) * kVarlenTcRows, make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
+                            }
+                        }
+                    }
+                    if (row_ok && !whole)
+                        __stcg(p.ml_part + slot * kVarlenTcRows + 128 * (pair ? w : 0) + r,
+                               make_float2(ok ? m_used : -INFINITY, ok ? l : 0.f));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && n > 0) {
+                    if (pair) {
+                        mbar_arrive(ofree_bar(w));
+                    } else if (w == 0) {
+                        mbar_arrive(ofree_bar(0));
+                        if (had1) mbar_arrive(ofree_bar(1));
+                    }
+                }
+                if (!pair) named_sync(2, 256);     // stream 1's max and sum have been read
+            }
+        }
+    }
+
+    // every product has been waited for by a softmax warp (or the CTA aborted:
+    // then drain the pipe): free tensor memory, join the shared units
+    __syncthreads();
+    if (warp == 1 && lane == 0 && *abort_flag) {
+        // the barrier's phase may be anything: re-initialise one that nobody uses any more
+        mbar_init(qempty_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        umma_commit(qempty_bar);
+        wait_bar(qempty_bar, 0, nullptr, p.fault);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+    if (!pl.idle) {
+        const VlEnds &ends = misc->ends;
+        if (tid < ends.n) vl_arrive(p, ends.u[tid]);
+        for (int i = 0; i < ends.n; ++i) vl_join(p, ends.u[i], tpt, 128, &misc->join_flag);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn_vl() {
+    // looked up once; the initialisation of a function-local static is thread-safe
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess && q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+        return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+    }();
+    return fn;
+}
+
+bool encode_vl(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+               const cuuint32_t *box) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn_vl();
+    if (!fn) return false;
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int page_box(int page_size) {       // slots per copy: the largest power of two that divides the page, up to 128
+    int b = 128;
+    while (page_size % b) b >>= 1;
+    return b;
+}
+
+template <int D, bool kPaged>
+cudaError_t configure() {
+    // the shared-memory limit, and the registers that the warps share out
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, attn_varlen_tc_kernel<D, kPaged>);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;   // setmaxnreg would wait for registers that are not there
+    e = cudaFuncSetAttribute(attn_varlen_tc_kernel<D, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Lay<D>::kSmem);
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+template <int D, bool kPaged>
+cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
+    const int G = p.Hq / p.Hkv, tpt = 128 / G;
+    alignas(64) CUtensorMap mq, mk, mv;
+    {   // (d, head, token): box 64 d x G heads x tpt tokens = rows token * G + head of 128 bytes
+        const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.N};
+        const cuuint64_t strides[2] = {(cuuint64_t)p.q_head * 2, (cuuint64_t)p.q_tok * 2};
+        const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tpt};
+        if (!encode_vl(&mq, p.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    int box_rows = 128;
+    for (int i = 0; i < 2; ++i) {
+        const void *t = i ? p.v : p.k;
+        CUtensorMap *m = i ? &mv : &mk;
+        if (kPaged) {   // (d % 64, slot, d / 64, kv head, page): a copy per page and 64-column block
+            box_rows = page_box(p.page_size);
+            const cuuint64_t dims[5] = {64, (cuuint64_t)p.page_size, (cuuint64_t)(D / 64), (cuuint64_t)p.Hkv,
+                                        (cuuint64_t)p.n_pages};
+            const cuuint64_t strides[4] = {(cuuint64_t)p.kv.s * 2, 128, (cuuint64_t)p.kv.h * 2, (cuuint64_t)p.kv.b * 2};
+            const cuuint32_t box[5] = {64, (cuuint32_t)box_rows, 1, 1, 1};
+            if (!encode_vl(m, t, 5, dims, strides, box)) return cudaErrorInvalidValue;
+        } else {        // (d % 64, token, d / 64, kv head): one copy per tile
+            const cuuint64_t dims[4] = {64, (cuuint64_t)p.N, (cuuint64_t)(D / 64), (cuuint64_t)p.Hkv};
+            const cuuint64_t strides[3] = {(cuuint64_t)p.kv.s * 2, 128, (cuuint64_t)p.kv.h * 2};
+            const cuuint32_t box[4] = {64, 128, (cuuint32_t)(D / 64), 1};
+            if (!encode_vl(m, t, 4, dims, strides, box)) return cudaErrorInvalidValue;
+        }
+    }
+    cudaError_t e = configure<D, kPaged>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Lay<D>::kSmem;
+    cfg.stream = st;
+    // the CTAs of a shared unit wait for one another: a cooperative launch makes
+    // them resident together
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kPaged>, mq, mk, mv, p, tpt, box_rows);
+}
+
+}  // namespace
+
+bool varlen_tc_supported(const VarlenParams &p) {
+    if (p.dt != SD_BF16 || (p.D != 64 && p.D != 128) || p.Hq / p.Hkv > kVarlenMaxGroup) return false;
+    if (p.table && p.page_size % 8) return false;      // a copy's rows start on the swizzle's 8-row period
+    if (!encode_fn_vl()) return false;
+    int dev = 0, optin = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return false;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    return optin >= Lay<128>::kSmem && optin >= Lay<64>::kSmem && major == 10 && minor == 3;
+}
+
+cudaError_t launch_varlen_tc(const VarlenParams &p, int grid, cudaStream_t st) {
+    if (p.table) return p.D == 128 ? launch_tc<128, true>(p, grid, st) : launch_tc<64, true>(p, grid, st);
+    return p.D == 128 ? launch_tc<128, false>(p, grid, st) : launch_tc<64, false>(p, grid, st);
+}
+
+}  // namespace sdv

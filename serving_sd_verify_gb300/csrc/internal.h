@@ -20,6 +20,8 @@ enum FaultBits : unsigned int {
     FAULT_TMEM_ALLOC = 1u << 4,     // tensor-memory allocation returned out of range
     FAULT_BAD_TREE = 1u << 5,       // a tree node's parent outside [0, node)
     FAULT_BAD_COMMIT = 1u << 6,     // a commit with n_acc / path / lengths out of range (skipped)
+    FAULT_BAD_LENGTH = 1u << 7,     // a packed offset or cache length out of range (clamped)
+    FAULT_BAD_PAGE = 1u << 8,       // a page index outside the pool
 };
 
 constexpr int kMaxT = 16;           // block rows (anchor + 15 proposals)
@@ -79,6 +81,70 @@ struct AttnParams {
     WaitTest wt;
     unsigned int *fault;
 };
+
+// Attention of packed new tokens over their own rows (prompt) or a paged
+// cache.  A unit is `tb` consecutive tokens of a sequence for one kv head, all
+// G query heads of them; the CTAs share the units' key tiles evenly (varlen.cuh).
+struct VarlenParams {
+    const void *q;                  // [N, Hq, D], strides q_tok, q_head (elements)
+    long q_tok, q_head;
+    const void *k, *v;              // prompt: [N, Hkv, D]; paged: [n_pages, page_size, Hkv, D]
+    sd_strides kv;                  // (b: page, s: token or slot, h: head)
+    const int32_t *cu;              // [B + 1]
+    const int32_t *kv_len;          // [B] (paged), null for prompts
+    const int32_t *table;           // [B] rows of table_stride (paged)
+    long table_stride;
+    int table_cols, n_pages, page_size;
+    void *out;                      // [N, Hq, D], contiguous
+    int N, B, Hq, Hkv, D;
+    int max_q, max_kv, causal;
+    float scale;
+    sd_dtype dt;
+    int tb;                         // tokens per unit
+    int tile;                       // keys per tile
+    int rows;                       // rows of a partial slot
+    float *o_part;                  // [2 * grid][D / 4][rows] float4, weighted sums of a CTA's first and last unit
+    float2 *ml_part;                // [2 * grid][rows] (running max in log2 units, running sum)
+    unsigned int *ctr;              // [grid] arrivals of the unit that CTA c opens and others finish
+    WaitTest wt;
+    unsigned int *fault;
+};
+constexpr int kVarlenMaxGroup = 64;     // Hq / Hkv
+constexpr int kVarlenTcRows = 256;      // rows of a unit, tensor cores: two tiles of 128
+constexpr int kVarlenTcTile = 128;      // its keys per tile
+constexpr int kVarlenGenTile = 64;      // keys per tile of the CUDA-core kernel
+constexpr int kVarlenGenPerSm = 4;      // and its CTAs per SM at most
+constexpr int kVarlenFixed = 128;       // a unit's fixed cost, in keys (its queries, its epilogue)
+constexpr int kVarlenMinShare = 256 + kVarlenFixed;   // smallest share of a CTA, in the same keys
+bool varlen_tc_supported(const VarlenParams &p);
+int varlen_generic_rows(const VarlenParams &p);        // rows per unit of the CUDA-core kernel
+int varlen_max_grid(int path, const VarlenParams &p);  // its CTAs that are resident at once (0: none)
+// grid <= varlen_max_grid(): the CTAs of a shared unit wait for one another
+cudaError_t launch_varlen_tc(const VarlenParams &p, int grid, cudaStream_t st);
+cudaError_t launch_varlen_generic(const VarlenParams &p, int grid, cudaStream_t st);
+
+// Rotary positions, and with them the write of new keys and values to a paged
+// cache.  Heads 0 .. Hq-1 are x's (rotated into y); then Hk heads of k (rotated)
+// and Hk heads of v (copied) into the pages.
+struct RopeParams {
+    const void *x, *k, *v;
+    void *y;
+    long x_tok, x_head, y_tok, y_head, kv_tok, kv_head;   // elements
+    const int32_t *positions;       // null: the token's cache position (append only)
+    const uint64_t *turns;          // [rot / 2]
+    float magnitude;
+    int N, Hq, Hk, D, rot, interleaved;
+    int copy_rest;                  // elements rot .. D-1 of x are copied to y (not in place)
+    sd_dtype dt;
+    const int32_t *cu, *kv_len, *table;
+    int B;
+    long table_stride;
+    int table_cols, n_pages, page_size;
+    void *k_pages, *v_pages;
+    sd_strides pages;
+    unsigned int *fault;
+};
+cudaError_t launch_rope(const RopeParams &p, cudaStream_t st);
 
 // kernel launchers: return the launch error (cudaSuccess when enqueued)
 cudaError_t launch_attn_generic(const AttnParams &p, cudaStream_t st);

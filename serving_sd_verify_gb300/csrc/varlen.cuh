@@ -1,0 +1,424 @@
+// What the two kernels of packed (varlen) attention share: how the work of a
+// ragged batch is divided, and how partial results are joined.
+//
+// Work.  Unit (b, g, r) is tokens [r tb, (r + 1) tb) of sequence b's new tokens
+// for kv head g, with every query head that reads it; its keys are those its
+// last token sees.  Units in the order (b, g, r) form one line whose length is
+// counted in keys (a unit's visible keys plus a fixed cost); CTA c of n takes
+// the c-th n-th of it, cut at whole key tiles.  So every CTA has the same load
+// whatever the lengths are -- one token over a long cache, a causal prompt, a
+// mixture -- and at most its first and its last unit are shared with its
+// neighbours.  Lengths are read on the device, so the host needs only bounds;
+// the whole plan costs a warp two passes over the sequences.
+//
+// Join.  A CTA that has only some of a unit's tiles leaves its weighted sums,
+// running max and running sum in a slot of the workspace; when all n CTAs of
+// the unit have arrived, each joins its n-th of the rows.  The order of the
+// sum is the order of the tiles, whoever arrives when.
+#pragma once
+
+#include "common.cuh"
+
+namespace sdv {
+namespace {
+
+struct VlSeq {
+    int c0, q, kv;      // first packed row, new tokens, keys
+    int off;            // causal: row i sees off + i + 1 keys
+    int nr;             // units per kv head
+};
+
+__device__ __forceinline__ VlSeq vl_seq(const VarlenParams &p, int b, bool report) {
+    VlSeq s;
+    const int a = p.cu[b], e = p.cu[b + 1];
+    const int len = p.kv_len ? p.kv_len[b] : 0;
+    s.c0 = max(0, min(a, p.N));
+    const int c1 = max(s.c0, min(e, p.N));
+    s.q = min(c1 - s.c0, p.max_q);
+    bool bad = a != s.c0 || e != s.c0 + s.q;
+    if (p.kv_len) {
+        const long slots = (long)p.table_cols * p.page_size;
+        s.kv = max(0, (int)min((long)len, min((long)p.max_kv, slots)));
+        bad = bad || s.kv != len;
+    } else {
+        s.kv = s.q;
+    }
+    if (bad && report) set_fault(p.fault, FAULT_BAD_LENGTH);
+    s.off = s.kv - s.q;
+    s.nr = (s.q + p.tb - 1) / p.tb;
+    return s;
+}
+
+// keys the last token of unit r sees
+__device__ __forceinline__ int vl_keys(const VarlenParams &p, const VlSeq &s, int r) {
+    if (!p.causal) return s.kv;
+    return max(0, s.off + min(s.q, (r + 1) * p.tb));
+}
+
+// length of units [0, r) of one kv head on the work line, r <= nr
+__device__ __forceinline__ long vl_before(const VarlenParams &p, const VlSeq &s, int r) {
+    if (r == 0) return 0;
+    if (!p.causal) return (long)r * (s.kv + kVarlenFixed);
+    const long off = max(0, s.off);
+    const long r1 = r < s.nr ? r : r - 1;      // units of full tb tokens among them
+    long w = r1 * (off + kVarlenFixed) + (long)p.tb * (r1 * (r1 + 1) / 2);
+    if (r == s.nr) w += off + s.q + kVarlenFixed;
+    return w;
+}
+
+struct VlPos {          // a place on the work line: tile t of unit (b, g, r)
+    int b, g, r, t;
+};
+
+struct VlUnit {
+    int b, g, r;
+    int row0, ntok;     // first packed row, tokens
+    int tok0;           // the first one's number within the sequence
+    int off, kv;
+    int t0, t1, tiles;  // this CTA's tiles of all
+};
+
+// a unit shared by several CTAs, of which this one is `s` of `n`, the first `c0`
+struct VlShared {
+    int c0, n, s, slot;
+    int g, row0, ntok;
+};
+
+struct VlPlan {
+    int idle;
+    VlPos begin, end;
+    long W;             // length of the line
+    int C;              // CTAs that share it
+};
+
+// cut of a unit of length len and `tiles` tiles at `off` (0 <= off <= len): whole tiles before it
+__device__ __forceinline__ int vl_cut(long off, long len, int tiles, bool splittable) {
+    if (!splittable) return 2 * off >= len ? tiles : 0;
+    return (int)((off * tiles + len / 2) / len);
+}
+__device__ __forceinline__ bool vl_splittable(const VarlenParams &p, const VlSeq &s) {
+    return !p.causal || s.off >= 0;
+}
+
+__device__ __forceinline__ long vl_boundary(long W, int C, int c) { return (long)((unsigned __int128)W * c / C); }
+
+// the place of boundary x on the line, within sequence b whose part begins at `seq_x`
+__device__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, long seq_x, long x) {
+    const long head = vl_before(p, s, s.nr);
+    long o = x - seq_x;
+    const int g = min((int)(o / head), p.Hkv - 1);
+    o -= (long)g * head;
+    int lo = 0, hi = s.nr - 1;                  // the last unit that begins at or before o
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (vl_before(p, s, mid) <= o) lo = mid;
+        else hi = mid - 1;
+    }
+    const long u0 = vl_before(p, s, lo), len = vl_before(p, s, lo + 1) - u0;
+    const int tiles = (vl_keys(p, s, lo) + p.tile - 1) / p.tile;
+    const int t = vl_cut(o - u0, len, tiles, vl_splittable(p, s));
+    VlPos r = {b, g, lo, t};
+    if (t >= tiles && (tiles > 0 || 2 * (o - u0) >= len)) {      // at its end: the next unit's beginning
+        r.t = 0;
+        if (++r.r == s.nr) { r.r = 0; ++r.g; }
+        if (r.g == p.Hkv) { r.g = 0; ++r.b; }
+    }
+    return r;
+}
+
+// The share of CTA `c` of `grid` (one full warp).
+__device__ VlPlan vl_plan(const VarlenParams &p, int c, int grid) {
+    const int lane = threadIdx.x & 31;
+    VlPlan pl = {};
+    long tot = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        if (b < p.B) {
+            const VlSeq s = vl_seq(p, b, c == 0);
+            tot += (long)p.Hkv * vl_before(p, s, s.nr);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    pl.W = tot;
+    pl.C = (int)max(1L, min((long)grid, tot / kVarlenMinShare));
+    pl.idle = tot == 0 || c >= pl.C;
+    if (pl.idle) return pl;
+    const long x0 = vl_boundary(tot, pl.C, c), x1 = vl_boundary(tot, pl.C, c + 1);
+    pl.begin = {0, 0, 0, 0};
+    pl.end = {p.B, 0, 0, 0};
+    long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        VlSeq s = {};
+        long w = 0;
+        if (b < p.B) {
+            s = vl_seq(p, b, false);
+            w = (long)p.Hkv * vl_before(p, s, s.nr);
+        }
+        long incl = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const long a = base + incl - w, e = base + incl;
+        VlPos ps = {}, pe = {};
+        const bool hs = w > 0 && x0 >= a && x0 < e, he = w > 0 && x1 >= a && x1 < e;
+        if (hs) ps = vl_locate(p, b, s, a, x0);
+        if (he) pe = vl_locate(p, b, s, a, x1);
+        const unsigned ms = __ballot_sync(0xffffffffu, hs), me = __ballot_sync(0xffffffffu, he);
+        if (ms) {
+            const int src = __ffs((int)ms) - 1;
+            pl.begin = {__shfl_sync(0xffffffffu, ps.b, src), __shfl_sync(0xffffffffu, ps.g, src),
+                        __shfl_sync(0xffffffffu, ps.r, src), __shfl_sync(0xffffffffu, ps.t, src)};
+        }
+        if (me) {
+            const int src = __ffs((int)me) - 1;
+            pl.end = {__shfl_sync(0xffffffffu, pe.b, src), __shfl_sync(0xffffffffu, pe.g, src),
+                      __shfl_sync(0xffffffffu, pe.r, src), __shfl_sync(0xffffffffu, pe.t, src)};
+            break;
+        }
+        base = base + __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return pl;
+}
+
+// Walks a CTA's units in order; every warp role runs its own copy.
+struct VlWalk {
+    VlPos at;
+    VlSeq s;
+    bool fresh;         // s is that of at.b
+
+    __device__ __forceinline__ explicit VlWalk(const VlPlan &pl) : at(pl.begin), fresh(false) {}
+
+    __device__ __forceinline__ bool next(const VarlenParams &p, const VlPlan &pl, VlUnit &u) {
+        for (;;) {
+            if (at.b >= p.B) return false;
+            if (at.b == pl.end.b && at.g == pl.end.g && at.r == pl.end.r && at.t >= pl.end.t) return false;
+            if (at.b > pl.end.b) return false;
+            if (!fresh) { s = vl_seq(p, at.b, false); fresh = true; }
+            if (s.nr == 0) {
+                ++at.b; at.g = at.r = at.t = 0; fresh = false;
+                continue;
+            }
+            u.b = at.b; u.g = at.g; u.r = at.r;
+            u.tok0 = at.r * p.tb;
+            u.row0 = s.c0 + u.tok0;
+            u.ntok = min(p.tb, s.q - u.tok0);
+            u.off = s.off;
+            u.kv = s.kv;
+            u.tiles = (vl_keys(p, s, at.r) + p.tile - 1) / p.tile;
+            u.t0 = at.t;
+            const bool last = at.b == pl.end.b && at.g == pl.end.g && at.r == pl.end.r;
+            u.t1 = last ? pl.end.t : u.tiles;
+            if (last) {
+                at.t = pl.end.t;                 // next() ends here
+            } else {
+                at.t = 0;
+                if (++at.r == s.nr) { at.r = 0; ++at.g; }
+                if (at.g == p.Hkv) { at.g = 0; ++at.b; fresh = false; }
+            }
+            return true;
+        }
+    }
+};
+
+// keys that token i (within the sequence) of the unit sees
+__device__ __forceinline__ int vl_limit(const VarlenParams &p, const VlUnit &u, int i) {
+    return p.causal ? max(0, min(u.kv, u.off + i + 1)) : u.kv;
+}
+
+// The CTAs of a unit that CTA c shares: `opens` when its part begins at tile 0.
+// seq_x: where the unit's sequence begins on the line.
+__device__ VlShared vl_shared(const VarlenParams &p, const VlPlan &pl, int c, const VlUnit &u, long seq_x) {
+    const VlSeq s = vl_seq(p, u.b, false);
+    const long X = seq_x + (long)u.g * vl_before(p, s, s.nr) + vl_before(p, s, u.r);
+    const long len = vl_before(p, s, u.r + 1) - vl_before(p, s, u.r);
+    const bool sp = vl_splittable(p, s);
+    // the first boundary that cuts after at least one tile, and the last that cuts before the last
+    int lo = (int)((unsigned __int128)X * pl.C / pl.W);
+    while (lo < pl.C && (vl_boundary(pl.W, pl.C, lo) < X ||
+                         vl_cut(vl_boundary(pl.W, pl.C, lo) - X, len, u.tiles, sp) < 1)) ++lo;
+    int hi = min(pl.C, (int)((unsigned __int128)(X + len) * pl.C / pl.W) + 1);
+    while (hi > lo && (vl_boundary(pl.W, pl.C, hi) > X + len ||
+                       vl_cut(vl_boundary(pl.W, pl.C, hi) - X, len, u.tiles, sp) >= u.tiles)) --hi;
+    VlShared r;
+    r.c0 = lo - 1;
+    r.n = hi - lo + 2;
+    r.s = c - r.c0;
+    r.slot = u.t0 == 0 ? 2 * c + 1 : 2 * c;
+    r.g = u.g;
+    r.row0 = u.row0;
+    r.ntok = u.ntok;
+    return r;
+}
+
+// where sequence b begins on the work line (one full warp)
+__device__ long vl_seq_start(const VarlenParams &p, int b_end) {
+    const int lane = threadIdx.x & 31;
+    long tot = 0;
+    for (int b = lane; b < b_end; b += 32) {
+        const VlSeq s = vl_seq(p, b, false);
+        tot += (long)p.Hkv * vl_before(p, s, s.nr);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    return tot;
+}
+
+// the units that CTA c shares with others (one full warp): the one its share
+// begins in the middle of, and the one it opens and leaves unfinished
+struct VlEnds {
+    int n;              // 0 to 2
+    VlShared u[2];
+};
+__device__ VlEnds vl_ends(const VarlenParams &p, const VlPlan &pl, int c) {
+    VlEnds e = {};
+    auto unit_at = [&](const VlPos &at, int t0) {
+        const VlSeq s = vl_seq(p, at.b, false);
+        VlUnit u = {};
+        u.b = at.b; u.g = at.g; u.r = at.r;
+        u.row0 = s.c0 + at.r * p.tb;
+        u.ntok = min(p.tb, s.q - at.r * p.tb);
+        u.tiles = (vl_keys(p, s, at.r) + p.tile - 1) / p.tile;
+        u.t0 = t0;
+        return u;
+    };
+    const bool same = pl.begin.b == pl.end.b && pl.begin.g == pl.end.g && pl.begin.r == pl.end.r;
+    if (pl.begin.t > 0) {
+        const long x = vl_seq_start(p, pl.begin.b);
+        e.u[e.n++] = vl_shared(p, pl, c, unit_at(pl.begin, pl.begin.t), x);
+    }
+    if (pl.end.t > 0 && !(same && pl.begin.t > 0)) {
+        const long x = vl_seq_start(p, pl.end.b);
+        e.u[e.n++] = vl_shared(p, pl, c, unit_at(pl.end, 0), x);
+    }
+    return e;
+}
+
+// Bounded wait until the counter reaches `target`.
+__device__ __noinline__ bool vl_wait(const unsigned int *ctr, unsigned int target, unsigned long long limit_ns) {
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (uint32_t it = 0;; ++it) {
+        unsigned int v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ctr) : "memory");
+        if (v >= target) return true;
+        if ((it & 15u) == 15u) {
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+            if (t - t0 > limit_ns) return false;
+        }
+        __nanosleep(32);
+    }
+}
+
+// Four output values of one row, in the output's type.
+__device__ __forceinline__ void vl_store4(const VarlenParams &p, long row, int c4, float4 o) {
+    if (p.dt == SD_BF16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+        uint2 w;
+        w.x = *reinterpret_cast<const uint32_t *>(&a);
+        w.y = *reinterpret_cast<const uint32_t *>(&b);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.D + 4 * c4) = w;
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * p.D + 4 * c4) = o;
+    }
+}
+
+// Joins this CTA's n-th of a shared unit's rows (the whole CTA).  Row k of the
+// unit is query head k % G of token k / G; in a slot the tokens lie `tpt` to a
+// tile of `trows` rows.  Where a CTA has fewer (row, 4 columns) items than
+// threads, `lanes` threads share an item's parts, each taking every lanes-th,
+// and combine by shuffles: always in the same order.
+__device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int trows, int *flag) {
+    const int nt = blockDim.x, tid = threadIdx.x;
+    unsigned int *ctr = p.ctr + sh.c0;
+    unsigned int ticket = 0;
+    if (tid == 0) {
+        const bool ok = vl_wait(ctr, (unsigned)sh.n + p.wt.extra, p.wt.limit_ns);
+        if (!ok) set_fault(p.fault, FAULT_WAIT_TIMEOUT);
+        *flag = ok;
+        // second ticket, whether or not the wait succeeded: the CTA with the last
+        // of the 2 n increments returns the counter to zero (nobody reads it then)
+        ticket = atomicAdd(ctr, 1u);
+    }
+    __syncthreads();
+    if (*flag) {
+        const int G = p.Hq / p.Hkv, D4 = p.D / 4;
+        const int items = sh.ntok * G * D4;
+        const int ia = (int)((long)sh.s * items / sh.n), ie = (int)((long)(sh.s + 1) * items / sh.n);
+        int lanes = 1;
+        while (lanes < 32 && 2 * lanes <= sh.n && (ie - ia) * lanes * 2 <= nt) lanes *= 2;
+        const int sub = tid & (lanes - 1);
+        // the loop runs the same number of times in every thread, so that whole
+        // warps meet at the shuffles
+        for (int i0 = ia; i0 < ie; i0 += nt / lanes) {
+            const int i = i0 + tid / lanes;
+            const bool live_i = i < ie;
+            // items in the order (row, column): row fastest within a block of
+            // the CTA's items would break up short ranges, columns fastest keeps
+            // the output stores together
+            const int k = live_i ? i / D4 : 0, c4 = live_i ? i - k * D4 : 0;
+            const int tok = k / G, h = k - tok * G;
+            const int row = (tok / tpt) * trows + (tok % tpt) * G + h;
+            float M = -INFINITY, l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int e0 = sub; e0 < sh.n; e0 += 4 * lanes) {
+                float4 v[4];
+                float2 ml[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int e = e0 + q * lanes;
+                    const bool live = live_i && e < sh.n;
+                    const long slot = e == 0 ? 2L * sh.c0 + 1 : 2L * (sh.c0 + e);
+                    v[q] = live ? __ldcg(reinterpret_cast<const float4 *>(p.o_part) + (slot * D4 + c4) * p.rows + row)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                    ml[q] = live ? __ldcg(p.ml_part + slot * p.rows + row) : make_float2(-INFINITY, 0.f);
+                }
+                const float bm = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+                if (bm == -INFINITY) continue;
+                const float f = exp2f(M - bm);                // 0 while nothing is held
+                M = bm;
+                l *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float w = exp2f(ml[q].x - M);      // 0 for a part that saw nothing
+                    l = fmaf(w, ml[q].y, l);
+                    acc.x = fmaf(w, v[q].x, acc.x); acc.y = fmaf(w, v[q].y, acc.y);
+                    acc.z = fmaf(w, v[q].z, acc.z); acc.w = fmaf(w, v[q].w, acc.w);
+                }
+            }
+            for (int o = 1; o < lanes; o <<= 1) {
+                const float M2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+                const float4 a2 = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o),
+                                              __shfl_xor_sync(0xffffffffu, acc.y, o),
+                                              __shfl_xor_sync(0xffffffffu, acc.z, o),
+                                              __shfl_xor_sync(0xffffffffu, acc.w, o));
+                const float m = fmaxf(M, M2);
+                const float f1 = m == -INFINITY ? 0.f : exp2f(M - m), f2 = m == -INFINITY ? 0.f : exp2f(M2 - m);
+                l = f1 * l + f2 * l2;
+                acc = make_float4(f1 * acc.x + f2 * a2.x, f1 * acc.y + f2 * a2.y, f1 * acc.z + f2 * a2.z,
+                                  f1 * acc.w + f2 * a2.w);
+                M = m;
+            }
+            if (live_i && sub == 0) {
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                vl_store4(p, (long)(sh.row0 + tok) * p.Hq + sh.g * G + h, c4,
+                          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+            }
+        }
+    }
+    if (tid == 0 && ticket == 2u * (unsigned)sh.n - 1u) atomicExch(ctr, 0u);
+    __syncthreads();
+}
+
+// announces this CTA's part of a shared unit (one thread, after a barrier that
+// follows every thread's writes of it)
+__device__ __forceinline__ void vl_arrive(const VarlenParams &p, const VlShared &sh) {
+    __threadfence();
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.ctr + sh.c0) : "memory");
+}
+
+}  // namespace
+}  // namespace sdv

@@ -33,7 +33,12 @@ SYMBOLS = [
     "sd_set_sample_path", "sd_last_sample_path", "sd_set_wait_test",
     "sd_commit_tokens", "sd_compact_tree_kv", "sd_store_to_host", "sd_project_kv_commit",
     "sd_latent_compress", "sd_latent_compress_workspace_size",
+    "sd_rotary_table", "sd_rotary", "sd_rotary_append_paged", "sd_paged_attention",
+    "sd_paged_attention_workspace_size", "sd_prompt_attention",
 ]
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
 
 
 class SdError(RuntimeError):
@@ -44,6 +49,12 @@ class SdError(RuntimeError):
 
 class Strides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("s", ctypes.c_int64), ("h", ctypes.c_int64)]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("strides", Strides), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("table_cols", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int)]
 
 
 _lib = None
@@ -121,6 +132,23 @@ def load():
     lib.sd_latent_compress.restype = _i
     lib.sd_latent_compress_workspace_size.argtypes = [_i] * 4
     lib.sd_latent_compress_workspace_size.restype = _sz
+    lib.sd_rotary_table.argtypes = [_i, ctypes.c_double, _i, ctypes.c_double, _i, ctypes.c_double, ctypes.c_double,
+                                    _vp, ctypes.POINTER(_f)]
+    lib.sd_rotary_table.restype = _i
+    lib.sd_rotary.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _f, _i, _i, _i, _i, _i, _i, _vp]
+    lib.sd_rotary.restype = _i
+    _cache = ctypes.POINTER(PagedCache)
+    lib.sd_rotary_append_paged.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _f, _i, _i, _vp, _vp,
+                                           _cache, _i, _i, _i, _i, _i, _i, _vp]
+    lib.sd_rotary_append_paged.restype = _i
+    lib.sd_paged_attention.argtypes = [_vp, _i64, _i64, _cache, _vp, _vp, _i, _i, _vp, _i, _i, _i, _i, _i, _i, _f, _i,
+                                       _vp, _sz, _vp]
+    lib.sd_paged_attention.restype = _i
+    lib.sd_paged_attention_workspace_size.argtypes = [_i] * 8
+    lib.sd_paged_attention_workspace_size.restype = _sz
+    lib.sd_prompt_attention.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f,
+                                        _i, _vp, _sz, _vp]
+    lib.sd_prompt_attention.restype = _i
     lib.sd_set_projector_path.argtypes = [_i]
     lib.sd_set_projector_path.restype = _i
     lib.sd_set_wait_test.argtypes = [ctypes.c_uint32, ctypes.c_uint64]
@@ -414,6 +442,143 @@ def sd_latent_compress(queries, features, out, ws, stream=None):
     _check(load().sd_latent_compress(_p(queries), _p(features), features.stride(1), features.stride(0), F, N, Cq, d,
                                      _p(out), out.stride(1), out.stride(0), _dt(features), _p(ws),
                                      ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# rotary positions, paged cache, packed attention
+# --------------------------------------------------------------------------
+
+def _on_current_device(*ts):
+    """Every tensor (None left out) on the current CUDA device: the calls use
+    its stream and its fault word."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError("all tensors must be CUDA tensors on the current device")
+
+
+def _table(t, name):
+    if t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} is int32 [B, columns] with contiguous rows")
+
+
+def _paged_cache(k_pages, v_pages, page_table) -> PagedCache:
+    _table(page_table, "page_table")
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages are [pages, page_size, Hkv, D] of equal shape and strides")
+    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), _kv_strides(k_pages), page_table.data_ptr(),
+                      page_table.stride(0), page_table.shape[1], k_pages.shape[0], k_pages.shape[1])
+
+
+def sd_rotary_table(rot_dim, theta, scaling="none", factor=1.0, original_max=0, low=1.0, high=32.0):
+    """(turns, magnitude): turns is a CPU int64 tensor [rot_dim / 2] of 64-bit
+    words, to be moved to the device once; scaling is one of ROPE_SCALINGS."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling is one of {sorted(ROPE_SCALINGS)}")
+    turns = torch.zeros(max(int(rot_dim), 2) // 2, dtype=torch.int64)
+    m = ctypes.c_float(0.0)
+    _check(load().sd_rotary_table(int(rot_dim), float(theta), ROPE_SCALINGS[scaling], float(factor), int(original_max),
+                                  float(low), float(high), turns.data_ptr(), ctypes.byref(m)))
+    return turns, m.value
+
+
+def _rope_args(turns, positions, N, layout):
+    if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError("turns is the int64 [rot_dim / 2] table of sd_rotary_table, on the device")
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (N,) or
+                                  not positions.is_contiguous()):
+        raise ValueError("positions is contiguous int32 [N]")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout is one of {sorted(ROPE_LAYOUTS)}")
+    return ROPE_LAYOUTS[layout]
+
+
+def sd_rotary(x, y, positions, turns, magnitude=1.0, layout="half", stream=None):
+    """x, y [N, H, D] (D contiguous; y may be x); positions int32 [N]."""
+    _on_current_device(x, y, positions, turns)
+    N, H, D = x.shape
+    lay = _rope_args(turns, positions, N, layout)
+    if y.shape != x.shape or y.dtype != x.dtype or x.stride(2) != 1 or y.stride(2) != 1:
+        raise ValueError("x and y are [N, H, D] of one dtype with contiguous last axes")
+    _check(load().sd_rotary(x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), y.stride(0), y.stride(1),
+                            positions.data_ptr(), turns.data_ptr(), float(magnitude), N, H, D, 2 * turns.shape[0], lay,
+                            _dt(x), _stream(stream)))
+
+
+def sd_rotary_append_paged(q, k, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages,
+                           magnitude=1.0, layout="half", stream=None):
+    """q [N, Hq, D] with q_out contiguous (or both None); k, v [N, Hkv, D] with
+    equal strides; positions int32 [N] or None; cu_q int32 [B + 1]; kv_len
+    int32 [B]; page_table int32 [B, columns]; k_pages, v_pages [pages,
+    page_size, Hkv, D]."""
+    _on_current_device(q, k, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages)
+    N, Hkv, D = k.shape
+    lay = _rope_args(turns, positions, N, layout)
+    _i32_cuda(cu_q, kv_len)
+    cache = _paged_cache(k_pages, v_pages, page_table)
+    B = kv_len.shape[0]
+    if cu_q.shape != (B + 1,) or page_table.shape[0] != B:
+        raise ValueError("cu_q is [B + 1] and page_table has B rows")
+    if k.shape != v.shape or k.stride() != v.stride() or k.stride(2) != 1:
+        raise ValueError("k and v are [N, Hkv, D] with equal strides and contiguous last axes")
+    if k_pages.shape[2:] != k.shape[1:] or not (k.dtype == v.dtype == k_pages.dtype == v_pages.dtype):
+        raise ValueError("pages and new rows share heads, head dimension and dtype")
+    Hq = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        Hq = q.shape[1]
+        if q.shape != (N, Hq, D) or q_out.shape != q.shape or q.stride(2) != 1 or not q_out.is_contiguous() or \
+                q.dtype != k.dtype or q_out.dtype != k.dtype:
+            raise ValueError("q and q_out are [N, Hq, D] of the pages' dtype; q_out contiguous")
+    _check(load().sd_rotary_append_paged(
+        _p(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1), k.data_ptr(), v.data_ptr(),
+        k.stride(0), k.stride(1), _p(q_out), _p(positions), turns.data_ptr(), float(magnitude), 2 * turns.shape[0],
+        lay, cu_q.data_ptr(), kv_len.data_ptr(), cache, N, B, Hq, Hkv, D, _dt(k), _stream(stream)))
+
+
+def sd_paged_attention_workspace_size(N, B, max_q, Hq, Hkv, D, max_kv, dtype=SD_BF16) -> int:
+    return int(load().sd_paged_attention_workspace_size(N, B, max_q, Hq, Hkv, D, max_kv, dtype))
+
+
+def sd_paged_attention(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q, max_kv, out, scale, ws, causal=True,
+                       stream=None):
+    """q [N, Hq, D] (D contiguous); k_pages, v_pages [pages, page_size, Hkv, D];
+    page_table int32 [B, columns]; cu_q int32 [B + 1]; kv_len int32 [B]; out
+    [N, Hq, D] contiguous, of q's dtype."""
+    _on_current_device(q, k_pages, v_pages, page_table, cu_q, kv_len, out, ws)
+    N, Hq, D = q.shape
+    _i32_cuda(cu_q, kv_len)
+    cache = _paged_cache(k_pages, v_pages, page_table)
+    B = kv_len.shape[0]
+    if cu_q.shape != (B + 1,) or page_table.shape[0] != B:
+        raise ValueError("cu_q is [B + 1] and page_table has B rows")
+    if out.shape != q.shape or not out.is_contiguous() or q.stride(2) != 1 or k_pages.shape[3] != D or \
+            not (q.dtype == out.dtype == k_pages.dtype == v_pages.dtype):
+        raise ValueError("q, out and pages share D and dtype; out is contiguous [N, Hq, D]")
+    _check(load().sd_paged_attention(q.data_ptr(), q.stride(0), q.stride(1), cache, cu_q.data_ptr(),
+                                     kv_len.data_ptr(), int(max_q), int(max_kv), out.data_ptr(), N, B, Hq,
+                                     k_pages.shape[2], D, _dt(q), float(scale), 1 if causal else 0, ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def sd_prompt_attention(q, k, v, cu_seqlens, max_len, out, scale, ws, causal=True, stream=None):
+    """q [N, Hq, D]; k, v [N, Hkv, D] with equal strides; cu_seqlens int32
+    [B + 1]; out [N, Hq, D] contiguous, of q's dtype; ws of
+    sd_paged_attention_workspace_size(N, B, max_len, Hq, Hkv, D, max_len)."""
+    _on_current_device(q, k, v, cu_seqlens, out, ws)
+    N, Hq, D = q.shape
+    _i32_cuda(cu_seqlens)
+    if k.dim() != 3 or k.shape != v.shape or k.stride() != v.stride() or k.shape[0] != N or k.shape[2] != D:
+        raise ValueError("k and v are [N, Hkv, D] of equal shape and strides")
+    if out.shape != q.shape or not out.is_contiguous() or q.stride(2) != 1 or k.stride(2) != 1 or \
+            not (q.dtype == out.dtype == k.dtype == v.dtype):
+        raise ValueError("q, k, v, out share dtype and contiguous last axes; out is contiguous [N, Hq, D]")
+    _check(load().sd_prompt_attention(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(),
+                                      k.stride(0), k.stride(1), cu_seqlens.data_ptr(), int(max_len), out.data_ptr(),
+                                      N, cu_seqlens.shape[0] - 1, Hq, k.shape[1], D, _dt(q), float(scale),
+                                      1 if causal else 0, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                      _stream(stream)))
 
 
 def sd_set_projector_path(path: int) -> int:
