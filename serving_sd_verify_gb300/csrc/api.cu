@@ -933,7 +933,7 @@ void varlen_units(VarlenParams &p, int path) {
     p.rows = path >= 2 ? kVarlenTcRows : varlen_generic_rows(p);
     p.tb = path >= 2 ? 2 * (128 / G) : p.rows / G;
     if (p.tb < 1) p.tb = 1;      // 64 rows, a group of at most 64
-    p.tile = path >= 2 ? kVarlenTcTile : kVarlenGenTile;
+    p.tile_log2 = path >= 2 ? kVarlenTcTileLog2 : kVarlenGenTileLog2;
 }
 
 // at most `cap` CTAs, and no more than the work line of the largest batch
@@ -963,8 +963,8 @@ sd_status check_varlen(const VarlenParams &p) {
     if (p.Hq > 4096) return fail(SD_ERR_UNSUPPORTED, "Hq must be <= 4096");
     if (p.Hq / p.Hkv > kVarlenMaxGroup) return fail(SD_ERR_UNSUPPORTED, "Hq / Hkv must be <= %d", kVarlenMaxGroup);
     if (p.D != 64 && p.D != 128) return fail(SD_ERR_UNSUPPORTED, "D must be 64 or 128");
-    if (p.max_q < 0 || p.max_kv < 0 || p.max_kv > (1 << 30) || p.N > (1 << 30))
-        return fail(SD_ERR_INVALID_ARG, "N, max_q and max_kv must be in [0, 2^30]");
+    if (p.max_q < 0 || p.max_kv < 0 || p.max_kv > kVarlenMaxKv || p.N > kVarlenMaxKv)
+        return fail(SD_ERR_INVALID_ARG, "N, max_q and max_kv must be in [0, 2^26]");
     if (!(p.scale > 0.f) || !isfinite(p.scale)) return fail(SD_ERR_INVALID_ARG, "scale must be positive and finite");
     return SD_OK;
 }

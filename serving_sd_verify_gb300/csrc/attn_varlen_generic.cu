@@ -21,7 +21,7 @@ namespace sdv {
 namespace {
 
 constexpr int kGThreads = 256;
-constexpr int kGTile = kVarlenGenTile;      // 64 keys
+constexpr int kGTile = 1 << kVarlenGenTileLog2;      // 64 keys
 constexpr float kGLog2e = 1.4426950408889634f;
 
 template <int D, int R> struct GLay {

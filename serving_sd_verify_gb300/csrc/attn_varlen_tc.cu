@@ -93,6 +93,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// true in one lane of a converged warp, the same one each time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -144,11 +151,15 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     if (warp == 0) {
         const VlPlan q = vl_plan(p, cta, (int)gridDim.x);
         if (lane == 0) misc->plan = q;
+        __syncwarp();
+        // the producer goes straight on to its copies (it set up the barriers itself); the others wait for the plan
+        asm volatile("bar.arrive 15, %0;" ::"n"(kThreads) : "memory");
+    } else {
+        tc_fence_before();
+        named_sync(15, kThreads);
+        tc_fence_after();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = misc->tmem;
+    const uint32_t tmem = warp == 0 ? 0u : misc->tmem;
     const VlPlan &pl = misc->plan;
     const int G = p.Hq / p.Hkv;
 
@@ -258,7 +269,12 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 }
             } else if (warp == 1) {
                 // ---------------------------------------------------------- MMA issuer
-                if (lane == 0) {
+                // the whole warp runs the loop and one elected lane issues: the descriptors are then the
+                // same in every lane for the compiler too and stay in uniform registers (issued from inside
+                // a one-lane branch, the products took twice as long: 4.49 ms against 3.10 for the
+                // 25,119-token prompt)
+                {
+                    const bool el = elect_one();
                     VlWalk walk(pl);
                     VlUnit u;
                     RingPos rp;
@@ -270,16 +286,21 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         ok = ok && wait_bar(full_bar(rp.slot), rp.phase, abort_flag, p.fault);
                         tc_fence_after();
                     };
-                    auto issue_s = [&](int i, int qt, uint32_t kb) {
+                    // descriptors by their first tile's, moved on by whole 16-byte units
+                    const uint64_t qd0 = sw128_desc(sQ, 16, 1024), kd0 = sw128_desc(sRing, 16, 1024),
+                                   vd0 = sw128_desc(sRing, 128 * 128, 1024);
+                    auto issue_s = [&](int i, int qt, int slot) {
+                        const uint64_t qd = qd0 + (uint64_t)(qt * (L::kTile / 16)),
+                                       kd = kd0 + (uint64_t)(slot * (L::kTile / 16));
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-                            umma_ss(tmem + 128u * i, sw128_desc(sQ + qt * L::kTile + off, 16, 1024),
-                                    sw128_desc(kb + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                            const uint64_t off = (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2;
+                            if (el) umma_ss(tmem + 128u * i, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
                         }
-                        umma_commit(sfull_bar(i));
+                        if (el) umma_commit(sfull_bar(i));
                     };
-                    auto issue_pv = [&](int i, uint32_t vb, bool first) {
+                    auto issue_pv = [&](int i, int slot, bool first) {
+                        const uint64_t vd = vd0 + (uint64_t)(slot * (L::kTile / 16));
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             ok = ok && wait_bar(pfull_bar(i, h), pphase[i], abort_flag, p.fault);
@@ -287,8 +308,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             tc_fence_after();
 #pragma unroll
                             for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                                umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
-                                        sw128_desc(vb + kk * 16 * 128, 128 * 128, 1024), idO,
+                                if (el) umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + kk * (16 * 128 / 16), idO,
                                         (!first || kk > 0) ? 1u : 0u);
                         }
                         pphase[i] ^= 1u;
@@ -311,70 +331,67 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         qphase ^= 1u;
                         wait_tile();
                         if (!ok) break;
-                        uint32_t tile = sRing + rp.slot * L::kTile;
-                        issue_s(0, 0, tile);
-                        if (pair) issue_s(1, 1, tile);
-                        umma_commit(empty_bar(rp.slot));
+                        issue_s(0, 0, rp.slot);
+                        if (pair) issue_s(1, 1, rp.slot);
+                        if (el) umma_commit(empty_bar(rp.slot));
                         rp.step(L::kSlots);
                         if (pair) {
-                            if (n == 1) umma_commit(qempty_bar);
+                            if (n == 1) if (el) umma_commit(qempty_bar);
                             for (int j = 0; ok && j < n; ++j) {
                                 wait_tile();
                                 if (!ok) break;
                                 const RingPos vp = rp;
-                                const uint32_t vt = sRing + vp.slot * L::kTile;
                                 rp.step(L::kSlots);
                                 if (j == 0) claim(0);
-                                issue_pv(0, vt, j == 0);
+                                issue_pv(0, vp.slot, j == 0);
                                 if (!ok) break;
                                 if (j + 1 < n) {
                                     wait_tile();
                                     if (!ok) break;
-                                    tile = sRing + rp.slot * L::kTile;
-                                    issue_s(0, 0, tile);
+                                    issue_s(0, 0, rp.slot);
                                 } else {
-                                    umma_commit(ofull_bar(0));
+                                    if (el) umma_commit(ofull_bar(0));
                                 }
                                 if (j == 0) claim(1);
-                                issue_pv(1, vt, j == 0);
+                                issue_pv(1, vp.slot, j == 0);
                                 if (!ok) break;
-                                umma_commit(empty_bar(vp.slot));
+                                if (el) umma_commit(empty_bar(vp.slot));
                                 if (j + 1 < n) {
-                                    issue_s(1, 1, tile);
-                                    umma_commit(empty_bar(rp.slot));
+                                    issue_s(1, 1, rp.slot);
+                                    if (el) umma_commit(empty_bar(rp.slot));
                                     rp.step(L::kSlots);
-                                    if (j + 2 == n) umma_commit(qempty_bar);
+                                    if (j + 2 == n) if (el) umma_commit(qempty_bar);
                                 } else {
-                                    umma_commit(ofull_bar(1));
+                                    if (el) umma_commit(ofull_bar(1));
                                 }
                             }
                         } else {
                             if (n > 1) {
                                 wait_tile();
                                 if (!ok) break;
-                                issue_s(1, 0, sRing + rp.slot * L::kTile);
-                                umma_commit(empty_bar(rp.slot));
+                                issue_s(1, 0, rp.slot);
+                                if (el) umma_commit(empty_bar(rp.slot));
                                 rp.step(L::kSlots);
                             }
-                            if (n <= 2) umma_commit(qempty_bar);
+                            if (n <= 2) if (el) umma_commit(qempty_bar);
                             for (int j = 0; ok && j < n; ++j) {
                                 const int i = j & 1;
                                 wait_tile();
                                 if (!ok) break;
                                 if (j < 2) claim(i);
-                                issue_pv(i, sRing + rp.slot * L::kTile, j < 2);
+                                issue_pv(i, rp.slot, j < 2);
                                 if (!ok) break;
-                                umma_commit(empty_bar(rp.slot));
+                                if (el) umma_commit(empty_bar(rp.slot));
                                 rp.step(L::kSlots);
                                 if (j + 2 < n) {
                                     wait_tile();
                                     if (!ok) break;
-                                    issue_s(i, 0, sRing + rp.slot * L::kTile);
-                                    umma_commit(empty_bar(rp.slot));
+                                    issue_s(i, 0, rp.slot);
+                                    if (el) umma_commit(empty_bar(rp.slot));
                                     rp.step(L::kSlots);
-                                    if (j + 3 == n) umma_commit(qempty_bar);
+                                    if (j + 3 == n) if (el) umma_commit(qempty_bar);
                                 } else {
-                                    umma_commit(ofull_bar(i));
+                                    if (el) umma_commit(ofull_bar(i));
                                 }
                             }
                         }

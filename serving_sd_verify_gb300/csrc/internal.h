@@ -101,7 +101,7 @@ struct VarlenParams {
     float scale;
     sd_dtype dt;
     int tb;                         // tokens per unit
-    int tile;                       // keys per tile
+    int tile_log2;                  // keys per tile: a power of two
     int rows;                       // rows of a partial slot
     float *o_part;                  // [2 * grid][D / 4][rows] float4, weighted sums of a CTA's first and last unit
     float2 *ml_part;                // [2 * grid][rows] (running max in log2 units, running sum)
@@ -111,11 +111,14 @@ struct VarlenParams {
 };
 constexpr int kVarlenMaxGroup = 64;     // Hq / Hkv
 constexpr int kVarlenTcRows = 256;      // rows of a unit, tensor cores: two tiles of 128
-constexpr int kVarlenTcTile = 128;      // its keys per tile
-constexpr int kVarlenGenTile = 64;      // keys per tile of the CUDA-core kernel
+constexpr int kVarlenTcTileLog2 = 7;    // its keys per tile: 128
+constexpr int kVarlenGenTileLog2 = 6;   // keys per tile of the CUDA-core kernel: 64
 constexpr int kVarlenGenPerSm = 4;      // and its CTAs per SM at most
-constexpr int kVarlenFixed = 128;       // a unit's fixed cost, in keys (its queries, its epilogue)
-constexpr int kVarlenMinShare = 256 + kVarlenFixed;   // smallest share of a CTA, in the same keys
+constexpr int kVarlenFixed = 768;       // a unit's fixed cost, in keys (its queries, filling the pipeline, its epilogue)
+constexpr int kVarlenMinShare = 768;    // smallest share of a CTA, in the same keys: one unit of a tile
+constexpr int kVarlenGroup = 2;         // a unit is cut at multiples of this many tiles
+constexpr int kVarlenMaxKv = 1 << 26;   // keys of a sequence
+static_assert(2 * 128 + kVarlenFixed / 2 < kVarlenMinShare, "a share is longer than a group of any unit");
 bool varlen_tc_supported(const VarlenParams &p);
 int varlen_generic_rows(const VarlenParams &p);        // rows per unit of the CUDA-core kernel
 int varlen_max_grid(int path, const VarlenParams &p);  // its CTAs that are resident at once (0: none)

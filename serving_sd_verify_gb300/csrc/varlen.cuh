@@ -45,7 +45,7 @@ __device__ __forceinline__ VlSeq vl_seq(const VarlenParams &p, int b, bool repor
     }
     if (bad && report) set_fault(p.fault, FAULT_BAD_LENGTH);
     s.off = s.kv - s.q;
-    s.nr = (s.q + p.tb - 1) / p.tb;
+    s.nr = s.q <= p.tb ? (s.q > 0 ? 1 : 0) : (s.q + p.tb - 1) / p.tb;
     return s;
 }
 
@@ -87,27 +87,42 @@ struct VlShared {
 struct VlPlan {
     int idle;
     VlPos begin, end;
-    long W;             // length of the line
-    int C;              // CTAs that share it
+    long share;         // the line's length W = share * C + rest
+    int C, rest;        // CTAs that share it
 };
 
-// cut of a unit of length len and `tiles` tiles at `off` (0 <= off <= len): whole tiles before it
+__device__ __forceinline__ int vl_tiles(const VarlenParams &p, int keys) {
+    return (keys + (1 << p.tile_log2) - 1) >> p.tile_log2;
+}
+
+// cut of a unit of length len and `tiles` tiles at `off` (0 <= off <= len): the
+// tiles before it, in whole groups of kVarlenGroup.  Non-decreasing in off, and
+// two boundaries at least kVarlenMinShare apart never give the same cut inside
+// a unit of several groups (a group is at most 2 * 128 + kVarlenFixed / 2 long;
+// fp32 holds the quotient to 2^-4 of a group up to kVarlenMaxKv keys).
 __device__ __forceinline__ int vl_cut(long off, long len, int tiles, bool splittable) {
-    if (!splittable) return 2 * off >= len ? tiles : 0;
-    return (int)((off * tiles + len / 2) / len);
+    const int groups = (tiles + kVarlenGroup - 1) / kVarlenGroup;
+    if (!splittable || groups < 2) return 2 * off >= len ? tiles : 0;
+    const int g = (int)fmaf((float)off, (float)groups / (float)len, 0.5f);
+    return min(tiles, g * kVarlenGroup);
 }
 __device__ __forceinline__ bool vl_splittable(const VarlenParams &p, const VlSeq &s) {
     return !p.causal || s.off >= 0;
 }
 
-__device__ __forceinline__ long vl_boundary(long W, int C, int c) { return (long)((unsigned __int128)W * c / C); }
+// floor(W c / C): both products of the remainder are below 2^31
+__device__ __forceinline__ long vl_boundary(const VlPlan &pl, int c) {
+    return pl.share * c + (int)((unsigned)(pl.rest * c) / (unsigned)pl.C);
+}
 
 // the place of boundary x on the line, within sequence b whose part begins at `seq_x`
 __device__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, long seq_x, long x) {
     const long head = vl_before(p, s, s.nr);
     long o = x - seq_x;
-    const int g = min((int)(o / head), p.Hkv - 1);
+    int g = min((int)((float)o / (float)head), p.Hkv - 1);     // at most 4096 heads: one off at most
     o -= (long)g * head;
+    if (o < 0) { --g; o += head; }
+    else if (o >= head && g < p.Hkv - 1) { ++g; o -= head; }
     int lo = 0, hi = s.nr - 1;                  // the last unit that begins at or before o
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -115,7 +130,7 @@ __device__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, long se
         else hi = mid - 1;
     }
     const long u0 = vl_before(p, s, lo), len = vl_before(p, s, lo + 1) - u0;
-    const int tiles = (vl_keys(p, s, lo) + p.tile - 1) / p.tile;
+    const int tiles = vl_tiles(p, vl_keys(p, s, lo));
     const int t = vl_cut(o - u0, len, tiles, vl_splittable(p, s));
     VlPos r = {b, g, lo, t};
     if (t >= tiles && (tiles > 0 || 2 * (o - u0) >= len)) {      // at its end: the next unit's beginning
@@ -126,41 +141,50 @@ __device__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, long se
     return r;
 }
 
-// The share of CTA `c` of `grid` (one full warp).
+// The share of CTA `c` of `grid` (one full warp).  Up to 32 sequences are read
+// once and kept in the lanes' registers.
 __device__ VlPlan vl_plan(const VarlenParams &p, int c, int grid) {
     const int lane = threadIdx.x & 31;
     VlPlan pl = {};
-    long tot = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        if (b < p.B) {
-            const VlSeq s = vl_seq(p, b, c == 0);
-            tot += (long)p.Hkv * vl_before(p, s, s.nr);
-        }
+    VlSeq s = {};
+    long w = 0, tot = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        s = vl_seq(p, b, c == 0);
+        w = (long)p.Hkv * vl_before(p, s, s.nr);
+        tot += w;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    pl.W = tot;
-    pl.C = (int)max(1L, min((long)grid, tot / kVarlenMinShare));
+    pl.C = tot < (long)grid * kVarlenMinShare ? max(1, (int)((unsigned)tot / (unsigned)kVarlenMinShare)) : grid;
     pl.idle = tot == 0 || c >= pl.C;
     if (pl.idle) return pl;
-    const long x0 = vl_boundary(tot, pl.C, c), x1 = vl_boundary(tot, pl.C, c + 1);
+    if (tot >> 32) {
+        pl.share = tot / pl.C;
+        pl.rest = (int)(tot - pl.share * pl.C);
+    } else {
+        pl.share = (unsigned)tot / (unsigned)pl.C;
+        pl.rest = (int)((unsigned)tot - (unsigned)pl.share * (unsigned)pl.C);
+    }
+    const long x0 = vl_boundary(pl, c), x1 = vl_boundary(pl, c + 1);
     pl.begin = {0, 0, 0, 0};
     pl.end = {p.B, 0, 0, 0};
     long base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        VlSeq s = {};
-        long w = 0;
-        if (b < p.B) {
-            s = vl_seq(p, b, false);
-            w = (long)p.Hkv * vl_before(p, s, s.nr);
+        if (p.B > 32) {
+            w = 0;
+            if (b < p.B) {
+                s = vl_seq(p, b, false);
+                w = (long)p.Hkv * vl_before(p, s, s.nr);
+            }
         }
         long incl = w;
+        if (p.B > 1) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
         }
         const long a = base + incl - w, e = base + incl;
         VlPos ps = {}, pe = {};
@@ -179,6 +203,7 @@ __device__ VlPlan vl_plan(const VarlenParams &p, int c, int grid) {
                       __shfl_sync(0xffffffffu, pe.r, src), __shfl_sync(0xffffffffu, pe.t, src)};
             break;
         }
+        if (ms && x1 >= base + __shfl_sync(0xffffffffu, incl, 31) && c + 1 == pl.C) break;
         base = base + __shfl_sync(0xffffffffu, incl, 31);
     }
     return pl;
@@ -208,7 +233,7 @@ struct VlWalk {
             u.ntok = min(p.tb, s.q - u.tok0);
             u.off = s.off;
             u.kv = s.kv;
-            u.tiles = (vl_keys(p, s, at.r) + p.tile - 1) / p.tile;
+            u.tiles = vl_tiles(p, vl_keys(p, s, at.r));
             u.t0 = at.t;
             const bool last = at.b == pl.end.b && at.g == pl.end.g && at.r == pl.end.r;
             u.t1 = last ? pl.end.t : u.tiles;
@@ -236,13 +261,16 @@ __device__ VlShared vl_shared(const VarlenParams &p, const VlPlan &pl, int c, co
     const long X = seq_x + (long)u.g * vl_before(p, s, s.nr) + vl_before(p, s, u.r);
     const long len = vl_before(p, s, u.r + 1) - vl_before(p, s, u.r);
     const bool sp = vl_splittable(p, s);
-    // the first boundary that cuts after at least one tile, and the last that cuts before the last
-    int lo = (int)((unsigned __int128)X * pl.C / pl.W);
-    while (lo < pl.C && (vl_boundary(pl.W, pl.C, lo) < X ||
-                         vl_cut(vl_boundary(pl.W, pl.C, lo) - X, len, u.tiles, sp) < 1)) ++lo;
-    int hi = min(pl.C, (int)((unsigned __int128)(X + len) * pl.C / pl.W) + 1);
-    while (hi > lo && (vl_boundary(pl.W, pl.C, hi) > X + len ||
-                       vl_cut(vl_boundary(pl.W, pl.C, hi) - X, len, u.tiles, sp) >= u.tiles)) --hi;
+    // the first boundary that cuts after at least one tile, and the last that cuts before the last;
+    // c is within a few of both where the unit has few CTAs, else the estimates start nearby
+    const float inv = 1.0f / ((float)pl.share + (float)pl.rest / (float)pl.C);
+    int lo = max(0, (int)((float)X * inv) - 1);
+    while (lo > 0 && vl_boundary(pl, lo - 1) >= X) --lo;
+    while (lo < pl.C && (vl_boundary(pl, lo) < X || vl_cut(vl_boundary(pl, lo) - X, len, u.tiles, sp) < 1)) ++lo;
+    int hi = min(pl.C, (int)((float)(X + len) * inv) + 1);
+    while (hi < pl.C && vl_boundary(pl, hi + 1) <= X + len) ++hi;
+    while (hi > lo && (vl_boundary(pl, hi) > X + len ||
+                       vl_cut(vl_boundary(pl, hi) - X, len, u.tiles, sp) >= u.tiles)) --hi;
     VlShared r;
     r.c0 = lo - 1;
     r.n = hi - lo + 2;
@@ -281,7 +309,7 @@ __device__ VlEnds vl_ends(const VarlenParams &p, const VlPlan &pl, int c) {
         u.b = at.b; u.g = at.g; u.r = at.r;
         u.row0 = s.c0 + at.r * p.tb;
         u.ntok = min(p.tb, s.q - at.r * p.tb);
-        u.tiles = (vl_keys(p, s, at.r) + p.tile - 1) / p.tile;
+        u.tiles = vl_tiles(p, vl_keys(p, s, at.r));
         u.t0 = t0;
         return u;
     };
@@ -327,9 +355,8 @@ __device__ __forceinline__ void vl_store4(const VarlenParams &p, long row, int c
 }
 
 // Joins this CTA's n-th of a shared unit's rows (the whole CTA).  Row k of the
-// unit is query head k % G of token k / G; in a slot the tokens lie `tpt` to a
-// tile of `trows` rows.  Where a CTA has fewer (row, 4 columns) items than
-// threads, `lanes` threads share an item's parts, each taking every lanes-th,
+// unit is query head k % G of token k / G; in a slot the first `tpt` tokens'
+// rows begin at 0 and the others' at `trows`.  Where a CTA has fewer items than threads, `lanes` threads share an item's parts, each taking every lanes-th,
 // and combine by shuffles: always in the same order.
 __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int trows, int *flag) {
     const int nt = blockDim.x, tid = threadIdx.x;
@@ -345,67 +372,70 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
     }
     __syncthreads();
     if (*flag) {
-        const int G = p.Hq / p.Hkv, D4 = p.D / 4;
-        const int items = sh.ntok * G * D4;
+        // an item: 8 columns of a row; rows fastest, as the slots hold them
+        const int G = p.Hq / p.Hkv, R = sh.ntok * G, items = R * (p.D / 8);
         const int ia = (int)((long)sh.s * items / sh.n), ie = (int)((long)(sh.s + 1) * items / sh.n);
         int lanes = 1;
         while (lanes < 32 && 2 * lanes <= sh.n && (ie - ia) * lanes * 2 <= nt) lanes *= 2;
         const int sub = tid & (lanes - 1);
+        const long cstep = p.rows, sstep = (long)(p.D / 4) * p.rows;
         // the loop runs the same number of times in every thread, so that whole
         // warps meet at the shuffles
         for (int i0 = ia; i0 < ie; i0 += nt / lanes) {
             const int i = i0 + tid / lanes;
             const bool live_i = i < ie;
-            // items in the order (row, column): row fastest within a block of
-            // the CTA's items would break up short ranges, columns fastest keeps
-            // the output stores together
-            const int k = live_i ? i / D4 : 0, c4 = live_i ? i - k * D4 : 0;
-            const int tok = k / G, h = k - tok * G;
-            const int row = (tok / tpt) * trows + (tok % tpt) * G + h;
+            const int c8 = live_i ? i / R : 0, k = live_i ? i - c8 * R : 0;
+            const int row = k < tpt * G ? k : trows + k - tpt * G;
+            const float4 *src = reinterpret_cast<const float4 *>(p.o_part) + 2 * c8 * cstep + row;
+            const float2 *mls = p.ml_part + row;
             float M = -INFINITY, l = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int e0 = sub; e0 < sh.n; e0 += 4 * lanes) {
-                float4 v[4];
-                float2 ml[4];
+            float acc[8];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 8; ++q) acc[q] = 0.f;
+            for (int e0 = sub; e0 < sh.n; e0 += 2 * lanes) {
+                float4 v[2][2];
+                float2 ml[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
                     const int e = e0 + q * lanes;
                     const bool live = live_i && e < sh.n;
                     const long slot = e == 0 ? 2L * sh.c0 + 1 : 2L * (sh.c0 + e);
-                    v[q] = live ? __ldcg(reinterpret_cast<const float4 *>(p.o_part) + (slot * D4 + c4) * p.rows + row)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-                    ml[q] = live ? __ldcg(p.ml_part + slot * p.rows + row) : make_float2(-INFINITY, 0.f);
+                    v[q][0] = live ? __ldcg(src + slot * sstep) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[q][1] = live ? __ldcg(src + slot * sstep + cstep) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    ml[q] = live ? __ldcg(mls + slot * p.rows) : make_float2(-INFINITY, 0.f);
                 }
-                const float bm = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+                const float bm = fmaxf(fmaxf(ml[0].x, ml[1].x), M);
                 if (bm == -INFINITY) continue;
                 const float f = exp2f(M - bm);                // 0 while nothing is held
                 M = bm;
-                l *= f; acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+                l *= f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 8; ++q) acc[q] *= f;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
                     const float w = exp2f(ml[q].x - M);      // 0 for a part that saw nothing
                     l = fmaf(w, ml[q].y, l);
-                    acc.x = fmaf(w, v[q].x, acc.x); acc.y = fmaf(w, v[q].y, acc.y);
-                    acc.z = fmaf(w, v[q].z, acc.z); acc.w = fmaf(w, v[q].w, acc.w);
+                    acc[0] = fmaf(w, v[q][0].x, acc[0]); acc[1] = fmaf(w, v[q][0].y, acc[1]);
+                    acc[2] = fmaf(w, v[q][0].z, acc[2]); acc[3] = fmaf(w, v[q][0].w, acc[3]);
+                    acc[4] = fmaf(w, v[q][1].x, acc[4]); acc[5] = fmaf(w, v[q][1].y, acc[5]);
+                    acc[6] = fmaf(w, v[q][1].z, acc[6]); acc[7] = fmaf(w, v[q][1].w, acc[7]);
                 }
             }
             for (int o = 1; o < lanes; o <<= 1) {
                 const float M2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-                const float4 a2 = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o),
-                                              __shfl_xor_sync(0xffffffffu, acc.y, o),
-                                              __shfl_xor_sync(0xffffffffu, acc.z, o),
-                                              __shfl_xor_sync(0xffffffffu, acc.w, o));
                 const float m = fmaxf(M, M2);
                 const float f1 = m == -INFINITY ? 0.f : exp2f(M - m), f2 = m == -INFINITY ? 0.f : exp2f(M2 - m);
                 l = f1 * l + f2 * l2;
-                acc = make_float4(f1 * acc.x + f2 * a2.x, f1 * acc.y + f2 * a2.y, f1 * acc.z + f2 * a2.z,
-                                  f1 * acc.w + f2 * a2.w);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) acc[q] = f1 * acc[q] + f2 * __shfl_xor_sync(0xffffffffu, acc[q], o);
                 M = m;
             }
             if (live_i && sub == 0) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                vl_store4(p, (long)(sh.row0 + tok) * p.Hq + sh.g * G + h, c4,
-                          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                const int tok = k / G;
+                const long orow = (long)(sh.row0 + tok) * p.Hq + sh.g * G + (k - tok * G);
+                vl_store4(p, orow, 2 * c8, make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv));
+                vl_store4(p, orow, 2 * c8 + 1, make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv));
             }
         }
     }

@@ -102,7 +102,7 @@ def test_paged_attention_refusals(S):
     assert paged(S, kv=None) == bad and paged(S, q=FAKE + 8) == bad and paged(S, out=FAKE + 8) == bad
     assert paged(S, q_tok=28 * 128 + 4) == bad and paged(S, q_head=64) == bad
     assert paged(S, B=0) == bad and paged(S, B=70000) == bad and paged(S, N=-1) == bad
-    assert paged(S, max_kv=-1) == bad and paged(S, max_kv=2 ** 30 + 1) == bad and paged(S, max_q=-1) == bad
+    assert paged(S, max_kv=-1) == bad and paged(S, max_kv=2 ** 26 + 1) == bad and paged(S, max_q=-1) == bad
     assert paged(S, Hq=27) == bad and paged(S, D=96) == uns and paged(S, Hq=65 * 4) == uns and paged(S, dt=7) == bad
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert paged(S, scale=s) == bad
