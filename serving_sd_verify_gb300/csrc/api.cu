@@ -983,6 +983,9 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
         return fail(SD_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
     if (!aligned_to(p.cu, 4)) return fail(SD_ERR_INVALID_ARG, "index arrays must be aligned to 4 bytes");
     p.max_q = std::min(p.max_q, p.N);
+    p.page_log2 = -1;
+    for (int i = 0; i < 31; ++i)
+        if (p.page_size == 1 << i) p.page_log2 = i;
     const int force = g_force_path.load();
     int path = 1;
     if (force != 1) {

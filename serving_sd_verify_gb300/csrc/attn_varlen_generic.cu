@@ -39,9 +39,10 @@ template <typename T>
 __device__ __forceinline__ const T *key_row(const VarlenParams &p, const VlUnit &u, const void *base, int key) {
     const T *t = static_cast<const T *>(base);
     if (!p.table) return t + (long)(u.row0 - u.tok0 + key) * p.kv.s + (long)u.g * p.kv.h;
-    const int pg = __ldg(p.table + (long)u.b * p.table_stride + key / p.page_size);
+    const int pi = p.page_log2 >= 0 ? key >> p.page_log2 : key / p.page_size;
+    const int pg = __ldg(p.table + (long)u.b * p.table_stride + pi);
     if (pg < 0 || pg >= p.n_pages) { set_fault(p.fault, FAULT_BAD_PAGE); return nullptr; }
-    return t + (long)pg * p.kv.b + (long)(key % p.page_size) * p.kv.s + (long)u.g * p.kv.h;
+    return t + (long)pg * p.kv.b + (long)(key - pi * p.page_size) * p.kv.s + (long)u.g * p.kv.h;
 }
 
 template <typename T, int D, int R>
@@ -222,7 +223,7 @@ attn_varlen_generic_kernel(const VarlenParams p) {
     __threadfence();
     __syncthreads();
     if (tid < ends.n) vl_arrive(p, ends.u[tid]);
-    for (int i = 0; i < ends.n; ++i) vl_join(p, ends.u[i], p.tb, 0, &join_flag);
+    for (int i = 0; i < ends.n; ++i) vl_join(p, ends.u[i], p.tb, 0, &join_flag, tid, kGThreads, 0);
 }
 
 template <typename T, int D, int R>

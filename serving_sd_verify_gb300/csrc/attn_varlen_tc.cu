@@ -181,14 +181,13 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     if (n <= 0) continue;
                     const int la = u.ntok <= tpt ? 2 : 1;
                     const int32_t *trow = kPaged ? p.table + (long)u.b * p.table_stride : nullptr;
-                    // the lane's page of tile t
+                    // the lane's page of tile t: looked up a tile ahead, first used (and checked) by its copy
                     auto page_of = [&](int t) {
                         if (!kPaged) return 0;
                         const int key = t * 128 + (lane % per_half) * box;
                         int pg = -1;
                         if (key < u.kv) {
-                            pg = __ldg(trow + key / p.page_size);
-                            if (pg < 0 || pg >= p.n_pages) { set_fault(p.fault, FAULT_BAD_PAGE); pg = p.n_pages; }
+                            pg = __ldg(trow + (p.page_log2 >= 0 ? key >> p.page_log2 : key / p.page_size));
                         }
                         return pg;
                     };
@@ -209,21 +208,29 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * L::kHalves));
                             __syncwarp();
                             const int i = lane % per_half, h = lane / per_half;
-                            if (i < boxes && h < L::kHalves)
+                            if (i < boxes && h < L::kHalves) {
+                                const int key = t * 128 + i * box;
+                                if (pg < 0 || pg >= p.n_pages) {      // read as zeros: the copy's fill
+                                    set_fault(p.fault, FAULT_BAD_PAGE);
+                                    pg = p.n_pages;
+                                }
                                 tma_load_5d(dst + h * (128 * 128) + i * box * 128, map, bar, 0,
-                                            (t * 128 + i * box) % p.page_size, h, u.g, pg);
+                                            p.page_log2 >= 0 ? key & (p.page_size - 1) : key % p.page_size, h, u.g, pg);
+                            }
                         }
                         rp.step(L::kSlots);
                         ++loads;
                     };
                     int pk = page_of(u.t0), pv = pk;      // pages of the next K tile, of the V tile behind it
                     int pk2 = 0;
-                    load_tile(false, u.t0, pk);
-                    if (n > 1) pk = page_of(u.t0 + 1);
-                    // Q once the last unit's S products have read the old one
-                    if (ok && units > 0) ok = wait_bar(qempty_bar, qphase ^ 1u, abort_flag, p.fault);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    // the first unit's Q at once; a later one's behind its first K tile, when the
+                    // last unit's S products have read the old Q
+                    if (units > 0) {
+                        load_tile(false, u.t0, pk);
+                        if (ok) ok = wait_bar(qempty_bar, qphase ^ 1u, abort_flag, p.fault);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
                     if (lane == 0) {
                         const int nq = u.ntok <= tpt ? 1 : 2;
                         mbar_arrive_expect_tx(qfull_bar, (uint32_t)(nq * L::kHalves * 128 * G * tpt));
@@ -233,6 +240,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                             u.row0 + i * tpt);
                     }
                     __syncwarp();
+                    if (units == 0) load_tile(false, u.t0, pk);
+                    if (n > 1) pk = page_of(u.t0 + 1);
                     qphase ^= 1u;
                     ++units;
                     // V of tile j and K of tile j + la, in the order of use
@@ -402,6 +411,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             } else if (warp == 3) {
                 const VlEnds e = vl_ends(p, pl, cta);
                 if (lane == 0) misc->ends = e;
+                asm volatile("bar.arrive 14, 288;" ::: "memory");
             }
         } else {
             // -------------------------------------------------------------- softmax
@@ -625,11 +635,16 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 }
                 if (!pair) named_sync(2, 256);     // stream 1's max and sum have been read
             }
+            // the softmax warps (they hold the registers) join the shared units
+            asm volatile("bar.sync 14, 288;" ::: "memory");     // warp 3's answer; every part of this CTA is written
+            const VlEnds &ends = misc->ends;
+            if (tid - 128 < ends.n) vl_arrive(p, ends.u[tid - 128]);
+            for (int i = 0; i < ends.n; ++i) vl_join(p, ends.u[i], tpt, 128, &misc->join_flag, tid - 128, 256, 1);
         }
     }
 
     // every product has been waited for by a softmax warp (or the CTA aborted:
-    // then drain the pipe): free tensor memory, join the shared units
+    // then drain the pipe): free tensor memory
     __syncthreads();
     if (warp == 1 && lane == 0 && *abort_flag) {
         // the barrier's phase may be anything: re-initialise one that nobody uses any more
@@ -643,11 +658,6 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     if (warp == 2) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
-    }
-    if (!pl.idle) {
-        const VlEnds &ends = misc->ends;
-        if (tid < ends.n) vl_arrive(p, ends.u[tid]);
-        for (int i = 0; i < ends.n; ++i) vl_join(p, ends.u[i], tpt, 128, &misc->join_flag);
     }
 }
 

@@ -95,6 +95,7 @@ struct VarlenParams {
     const int32_t *table;           // [B] rows of table_stride (paged)
     long table_stride;
     int table_cols, n_pages, page_size;
+    int page_log2;                  // of page_size, -1 where it is no power of two
     void *out;                      // [N, Hq, D], contiguous
     int N, B, Hq, Hkv, D;
     int max_q, max_kv, causal;
@@ -115,7 +116,7 @@ constexpr int kVarlenTcTileLog2 = 7;    // its keys per tile: 128
 constexpr int kVarlenGenTileLog2 = 6;   // keys per tile of the CUDA-core kernel: 64
 constexpr int kVarlenGenPerSm = 4;      // and its CTAs per SM at most
 constexpr int kVarlenFixed = 768;       // a unit's fixed cost, in keys (its queries, filling the pipeline, its epilogue)
-constexpr int kVarlenMinShare = 768;    // smallest share of a CTA, in the same keys: one unit of a tile
+constexpr int kVarlenMinShare = 648;    // smallest share of a CTA, in the same keys: less than a unit of one key
 constexpr int kVarlenGroup = 2;         // a unit is cut at multiples of this many tiles
 constexpr int kVarlenMaxKv = 1 << 26;   // keys of a sequence
 static_assert(2 * 128 + kVarlenFixed / 2 < kVarlenMinShare, "a share is longer than a group of any unit");

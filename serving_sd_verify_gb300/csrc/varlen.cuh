@@ -45,7 +45,7 @@ __device__ __forceinline__ VlSeq vl_seq(const VarlenParams &p, int b, bool repor
     }
     if (bad && report) set_fault(p.fault, FAULT_BAD_LENGTH);
     s.off = s.kv - s.q;
-    s.nr = s.q <= p.tb ? (s.q > 0 ? 1 : 0) : (s.q + p.tb - 1) / p.tb;
+    s.nr = s.q <= p.tb ? (s.q > 0 ? 1 : 0) : (int)((unsigned)(s.q + p.tb - 1) / (unsigned)p.tb);
     return s;
 }
 
@@ -58,12 +58,12 @@ __device__ __forceinline__ int vl_keys(const VarlenParams &p, const VlSeq &s, in
 // length of units [0, r) of one kv head on the work line, r <= nr
 __device__ __forceinline__ long vl_before(const VarlenParams &p, const VlSeq &s, int r) {
     if (r == 0) return 0;
-    if (!p.causal) return (long)r * (s.kv + kVarlenFixed);
-    const long off = max(0, s.off);
-    const long r1 = r < s.nr ? r : r - 1;      // units of full tb tokens among them
-    long w = r1 * (off + kVarlenFixed) + (long)p.tb * (r1 * (r1 + 1) / 2);
-    if (r == s.nr) w += off + s.q + kVarlenFixed;
-    return w;
+    const int full = (p.causal ? max(0, s.off) + (r == s.nr ? s.q : 0) : s.kv) + kVarlenFixed;   // the last unit's
+    if (r == 1 && r == s.nr) return full;
+    if (!p.causal) return (long)r * full;
+    const int r1 = r == s.nr ? r - 1 : r;      // units of tb tokens among them
+    const long w = (long)r1 * (max(0, s.off) + kVarlenFixed) + (long)p.tb * ((long)r1 * (r1 + 1) / 2);
+    return r == s.nr ? w + full : w;
 }
 
 struct VlPos {          // a place on the work line: tile t of unit (b, g, r)
@@ -166,15 +166,16 @@ __device__ VlPlan vl_plan(const VarlenParams &p, int c, int grid) {
         pl.rest = (int)((unsigned)tot - (unsigned)pl.share * (unsigned)pl.C);
     }
     const long x0 = vl_boundary(pl, c), x1 = vl_boundary(pl, c + 1);
-    pl.begin = {0, 0, 0, 0};
-    pl.end = {p.B, 0, 0, 0};
-    long base = 0;
+    // the sequences in which the share begins and ends: lane 0 then places the
+    // beginning and lane 1 the end, side by side
+    long base = 0, seq_x = 0;
+    VlSeq mine = {};
+    int found = -1;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
         if (p.B > 32) {
             w = 0;
-            if (b < p.B) {
-                s = vl_seq(p, b, false);
+            if (b0 + lane < p.B) {
+                s = vl_seq(p, b0 + lane, false);
                 w = (long)p.Hkv * vl_before(p, s, s.nr);
             }
         }
@@ -187,25 +188,27 @@ __device__ VlPlan vl_plan(const VarlenParams &p, int c, int grid) {
             }
         }
         const long a = base + incl - w, e = base + incl;
-        VlPos ps = {}, pe = {};
-        const bool hs = w > 0 && x0 >= a && x0 < e, he = w > 0 && x1 >= a && x1 < e;
-        if (hs) ps = vl_locate(p, b, s, a, x0);
-        if (he) pe = vl_locate(p, b, s, a, x1);
-        const unsigned ms = __ballot_sync(0xffffffffu, hs), me = __ballot_sync(0xffffffffu, he);
-        if (ms) {
-            const int src = __ffs((int)ms) - 1;
-            pl.begin = {__shfl_sync(0xffffffffu, ps.b, src), __shfl_sync(0xffffffffu, ps.g, src),
-                        __shfl_sync(0xffffffffu, ps.r, src), __shfl_sync(0xffffffffu, ps.t, src)};
-        }
-        if (me) {
-            const int src = __ffs((int)me) - 1;
-            pl.end = {__shfl_sync(0xffffffffu, pe.b, src), __shfl_sync(0xffffffffu, pe.g, src),
-                      __shfl_sync(0xffffffffu, pe.r, src), __shfl_sync(0xffffffffu, pe.t, src)};
-            break;
-        }
-        if (ms && x1 >= base + __shfl_sync(0xffffffffu, incl, 31) && c + 1 == pl.C) break;
-        base = base + __shfl_sync(0xffffffffu, incl, 31);
+        const unsigned ms = __ballot_sync(0xffffffffu, x0 >= a && x0 < e);
+        const unsigned me = __ballot_sync(0xffffffffu, x1 >= a && x1 < e);
+        const unsigned m = lane == 0 ? ms : me;
+        const int src = m ? __ffs((int)m) - 1 : 0;
+        VlSeq t;
+        t.c0 = __shfl_sync(0xffffffffu, s.c0, src);
+        t.q = __shfl_sync(0xffffffffu, s.q, src);
+        t.kv = __shfl_sync(0xffffffffu, s.kv, src);
+        t.nr = __shfl_sync(0xffffffffu, s.nr, src);
+        t.off = t.kv - t.q;
+        const long ta = __shfl_sync(0xffffffffu, a, src);
+        if (m && found < 0) { mine = t; seq_x = ta; found = b0 + src; }
+        if (me) break;
+        base = __shfl_sync(0xffffffffu, e, 31);
     }
+    VlPos at = {p.B, 0, 0, 0};
+    if (lane < 2 && found >= 0) at = vl_locate(p, found, mine, seq_x, lane == 0 ? x0 : x1);
+    pl.begin = {__shfl_sync(0xffffffffu, at.b, 0), __shfl_sync(0xffffffffu, at.g, 0),
+                __shfl_sync(0xffffffffu, at.r, 0), __shfl_sync(0xffffffffu, at.t, 0)};
+    pl.end = {__shfl_sync(0xffffffffu, at.b, 1), __shfl_sync(0xffffffffu, at.g, 1),
+              __shfl_sync(0xffffffffu, at.r, 1), __shfl_sync(0xffffffffu, at.t, 1)};
     return pl;
 }
 
@@ -354,12 +357,14 @@ __device__ __forceinline__ void vl_store4(const VarlenParams &p, long row, int c
     }
 }
 
-// Joins this CTA's n-th of a shared unit's rows (the whole CTA).  Row k of the
+// Joins this CTA's n-th of a shared unit's rows (`nt` threads, numbered by
+// `tid`, that meet at barrier `bar`).  Row k of the
 // unit is query head k % G of token k / G; in a slot the first `tpt` tokens'
 // rows begin at 0 and the others' at `trows`.  Where a CTA has fewer items than threads, `lanes` threads share an item's parts, each taking every lanes-th,
 // and combine by shuffles: always in the same order.
-__device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int trows, int *flag) {
-    const int nt = blockDim.x, tid = threadIdx.x;
+__device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int trows, int *flag, int tid, int nt,
+                        int bar) {
+    auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(nt) : "memory"); };
     unsigned int *ctr = p.ctr + sh.c0;
     unsigned int ticket = 0;
     if (tid == 0) {
@@ -370,7 +375,7 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
         // of the 2 n increments returns the counter to zero (nobody reads it then)
         ticket = atomicAdd(ctr, 1u);
     }
-    __syncthreads();
+    meet();
     if (*flag) {
         // an item: 8 columns of a row; rows fastest, as the slots hold them
         const int G = p.Hq / p.Hkv, R = sh.ntok * G, items = R * (p.D / 8);
@@ -379,68 +384,77 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
         while (lanes < 32 && 2 * lanes <= sh.n && (ie - ia) * lanes * 2 <= nt) lanes *= 2;
         const int sub = tid & (lanes - 1);
         const long cstep = p.rows, sstep = (long)(p.D / 4) * p.rows;
-        // the loop runs the same number of times in every thread, so that whole
-        // warps meet at the shuffles
-        for (int i0 = ia; i0 < ie; i0 += nt / lanes) {
-            const int i = i0 + tid / lanes;
-            const bool live_i = i < ie;
-            const int c8 = live_i ? i / R : 0, k = live_i ? i - c8 * R : 0;
-            const int row = k < tpt * G ? k : trows + k - tpt * G;
-            const float4 *src = reinterpret_cast<const float4 *>(p.o_part) + 2 * c8 * cstep + row;
-            const float2 *mls = p.ml_part + row;
-            float M = -INFINITY, l = 0.f;
-            float acc[8];
+        // kJoinItems items of a thread at a time, so that the loads of all are in
+        // flight together; the loops run the same number of times in every thread,
+        // so that whole warps meet at the shuffles
+        constexpr int kJoinItems = 4;
+        const int stride = nt / lanes;
+        for (int i0 = ia + tid / lanes; __any_sync(0xffffffffu, i0 < ie); i0 += kJoinItems * stride) {
+            float M[kJoinItems], l[kJoinItems], acc[kJoinItems][8];
+            const float4 *src[kJoinItems];
+            const float2 *mls[kJoinItems];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) acc[q] = 0.f;
-            for (int e0 = sub; e0 < sh.n; e0 += 2 * lanes) {
-                float4 v[2][2];
-                float2 ml[2];
+            for (int q = 0; q < kJoinItems; ++q) {
+                const int i = min(i0 + q * stride, items - 1);
+                const int c8 = i / R, k = i - c8 * R;
+                const int row = k < tpt * G ? k : trows + k - tpt * G;
+                src[q] = reinterpret_cast<const float4 *>(p.o_part) + 2 * c8 * cstep + row;
+                mls[q] = p.ml_part + row;
+                M[q] = -INFINITY;
+                l[q] = 0.f;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int e = e0 + q * lanes;
-                    const bool live = live_i && e < sh.n;
-                    const long slot = e == 0 ? 2L * sh.c0 + 1 : 2L * (sh.c0 + e);
-                    v[q][0] = live ? __ldcg(src + slot * sstep) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    v[q][1] = live ? __ldcg(src + slot * sstep + cstep) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    ml[q] = live ? __ldcg(mls + slot * p.rows) : make_float2(-INFINITY, 0.f);
+                for (int x = 0; x < 8; ++x) acc[q][x] = 0.f;
+            }
+            for (int e = sub; e < sh.n; e += lanes) {
+                const long slot = e == 0 ? 2L * sh.c0 + 1 : 2L * (sh.c0 + e);
+                float4 va[kJoinItems], vb[kJoinItems];
+                float2 ml[kJoinItems];
+#pragma unroll
+                for (int q = 0; q < kJoinItems; ++q) {
+                    const bool live = i0 + q * stride < ie;
+                    va[q] = live ? __ldcg(src[q] + slot * sstep) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    vb[q] = live ? __ldcg(src[q] + slot * sstep + cstep) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    ml[q] = live ? __ldcg(mls[q] + slot * p.rows) : make_float2(-INFINITY, 0.f);
                 }
-                const float bm = fmaxf(fmaxf(ml[0].x, ml[1].x), M);
-                if (bm == -INFINITY) continue;
-                const float f = exp2f(M - bm);                // 0 while nothing is held
-                M = bm;
-                l *= f;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] *= f;
+                for (int q = 0; q < kJoinItems; ++q) {
+                    const float m = fmaxf(M[q], ml[q].x);
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const float f = exp2f(M[q] - ref), w = exp2f(ml[q].x - ref);   // 0 for what saw nothing
+                    M[q] = m;
+                    l[q] = l[q] * f + w * ml[q].y;
+                    const float v[8] = {va[q].x, va[q].y, va[q].z, va[q].w, vb[q].x, vb[q].y, vb[q].z, vb[q].w};
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float w = exp2f(ml[q].x - M);      // 0 for a part that saw nothing
-                    l = fmaf(w, ml[q].y, l);
-                    acc[0] = fmaf(w, v[q][0].x, acc[0]); acc[1] = fmaf(w, v[q][0].y, acc[1]);
-                    acc[2] = fmaf(w, v[q][0].z, acc[2]); acc[3] = fmaf(w, v[q][0].w, acc[3]);
-                    acc[4] = fmaf(w, v[q][1].x, acc[4]); acc[5] = fmaf(w, v[q][1].y, acc[5]);
-                    acc[6] = fmaf(w, v[q][1].z, acc[6]); acc[7] = fmaf(w, v[q][1].w, acc[7]);
+                    for (int x = 0; x < 8; ++x) acc[q][x] = acc[q][x] * f + w * v[x];
                 }
             }
-            for (int o = 1; o < lanes; o <<= 1) {
-                const float M2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-                const float m = fmaxf(M, M2);
-                const float f1 = m == -INFINITY ? 0.f : exp2f(M - m), f2 = m == -INFINITY ? 0.f : exp2f(M2 - m);
-                l = f1 * l + f2 * l2;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] = f1 * acc[q] + f2 * __shfl_xor_sync(0xffffffffu, acc[q], o);
-                M = m;
-            }
-            if (live_i && sub == 0) {
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                const int tok = k / G;
-                const long orow = (long)(sh.row0 + tok) * p.Hq + sh.g * G + (k - tok * G);
-                vl_store4(p, orow, 2 * c8, make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv));
-                vl_store4(p, orow, 2 * c8 + 1, make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv));
+            for (int q = 0; q < kJoinItems; ++q) {
+                for (int o = 1; o < lanes; o <<= 1) {
+                    const float M2 = __shfl_xor_sync(0xffffffffu, M[q], o), l2 = __shfl_xor_sync(0xffffffffu, l[q], o);
+                    const float m = fmaxf(M[q], M2), ref = m == -INFINITY ? 0.f : m;
+                    const float f1 = exp2f(M[q] - ref), f2 = exp2f(M2 - ref);
+                    l[q] = f1 * l[q] + f2 * l2;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        acc[q][x] = f1 * acc[q][x] + f2 * __shfl_xor_sync(0xffffffffu, acc[q][x], o);
+                    M[q] = m;
+                }
+                const int i = i0 + q * stride;
+                if (i < ie && sub == 0) {
+                    const float inv = l[q] > 0.f ? 1.f / l[q] : 0.f;
+                    const int c8 = i / R, k = i - c8 * R, tok = k / G;
+                    const long orow = (long)(sh.row0 + tok) * p.Hq + sh.g * G + (k - tok * G);
+                    vl_store4(p, orow, 2 * c8,
+                              make_float4(acc[q][0] * inv, acc[q][1] * inv, acc[q][2] * inv, acc[q][3] * inv));
+                    vl_store4(p, orow, 2 * c8 + 1,
+                              make_float4(acc[q][4] * inv, acc[q][5] * inv, acc[q][6] * inv, acc[q][7] * inv));
+                }
             }
         }
     }
     if (tid == 0 && ticket == 2u * (unsigned)sh.n - 1u) atomicExch(ctr, 0u);
-    __syncthreads();
+    meet();
 }
 
 // announces this CTA's part of a shared unit (one thread, after a barrier that
