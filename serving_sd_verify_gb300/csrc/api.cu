@@ -936,12 +936,16 @@ void varlen_units(VarlenParams &p, int path) {
     p.tile_log2 = path >= 2 ? kVarlenTcTileLog2 : kVarlenGenTileLog2;
 }
 
-// at most `cap` CTAs, and no more than the work line of the largest batch
-// within the bounds has shares
+// length of the work line of the largest batch within the bounds, in keys
+double varlen_line(const VarlenParams &p) {
+    const double units = (double)p.Hkv * std::min((double)p.N / p.tb + p.B,
+                                                  (double)p.B * ((p.max_q + p.tb - 1) / p.tb));
+    return units * ((double)std::max(p.max_kv, p.max_q) + kVarlenFixed);
+}
+
+// at most `cap` CTAs, and no more than that line has shares
 int varlen_grid(const VarlenParams &p, int cap) {
-    const long units = (long)p.Hkv * ((long)p.N / p.tb + p.B);
-    const long line = units * ((long)p.max_kv + kVarlenFixed);
-    return (int)std::max(1L, std::min((long)cap, line / kVarlenMinShare));
+    return (int)std::max(1.0, std::min((double)cap, varlen_line(p) / kVarlenMinShare + 1.0));
 }
 
 struct VarlenLayout {
@@ -995,6 +999,11 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     p.fault = fault_ptr();
     if (!p.fault) return fail(SD_ERR_CUDA, "no CUDA device / fault word unavailable");
     varlen_units(p, path);
+    p.line_shift = 0;
+    while (ldexp(varlen_line(p), -p.line_shift) > 2.1e9) ++p.line_shift;
+    if (p.line_shift > kVarlenMaxShift)
+        return fail(SD_ERR_UNSUPPORTED, "tokens times heads times keys exceed one call");
+    p.min_share = std::max(kVarlenMinShare >> p.line_shift, ((kVarlenMinShare - 8) >> p.line_shift) + 2);
     const int cap = varlen_max_grid(path, p);
     if (cap < 1) return fail(SD_ERR_CUDA, "the attention kernel's occupancy is unavailable");
     int grid = varlen_grid(p, cap);
@@ -1008,6 +1017,7 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     p.ml_part = reinterpret_cast<float2 *>(w + l.ml);
     p.wt = wait_test();
     for (;;) {
+        p.inv_grid = 1.0f / (float)grid;
         const cudaError_t e = path == 2 ? launch_varlen_tc(p, grid, st) : launch_varlen_generic(p, grid, st);
         if (e == cudaErrorCooperativeLaunchTooLarge && grid > 1) {
             // a device that cannot hold that many CTAs at once (a partitioned one): any number serves
@@ -1144,6 +1154,7 @@ size_t sd_paged_attention_workspace_size(int N, int B, int max_q, int Hq, int Hk
     // page size and a forced path): tensor cores one CTA per SM and 256 rows,
     // CUDA cores kVarlenGenPerSm CTAs per SM of 64 rows
     p.tb = 1;
+    if (ldexp(varlen_line(p), -kVarlenMaxShift - 7) > 2.1e9) return 0;    // beyond any call, whatever its units
     const int sms = device_sm_count();
     const int g2 = varlen_grid(p, sms), g1 = varlen_grid(p, kVarlenGenPerSm * sms);
     return std::max(varlen_layout(g2, kVarlenTcRows, D).total, varlen_layout(g1, 64, D).total);

@@ -63,8 +63,8 @@ attn_varlen_generic_kernel(const VarlenParams p) {
     const int cta = (int)blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid < 32) {
-        const VlPlan q = vl_plan(p, cta, (int)gridDim.x);
-        if (tid == 0) pl = q;
+        const VlPlan q = vl_plan(p, cta);
+        vl_plan_store(q, &pl);
     }
     __syncthreads();
     if (pl.idle) return;

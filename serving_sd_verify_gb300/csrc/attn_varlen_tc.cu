@@ -149,9 +149,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0) {
-        const VlPlan q = vl_plan(p, cta, (int)gridDim.x);
-        if (lane == 0) misc->plan = q;
-        __syncwarp();
+        const VlPlan q = vl_plan(p, cta);
+        vl_plan_store(q, &misc->plan);
         // the producer goes straight on to its copies (it set up the barriers itself); the others wait for the plan
         asm volatile("bar.arrive 15, %0;" ::"n"(kThreads) : "memory");
     } else {

@@ -103,6 +103,9 @@ struct VarlenParams {
     sd_dtype dt;
     int tb;                         // tokens per unit
     int tile_log2;                  // keys per tile: a power of two
+    int line_shift;                 // the work line counts keys >> line_shift
+    int min_share;                  // smallest share of a CTA on it
+    float inv_grid;                 // 1 / CTAs
     int rows;                       // rows of a partial slot
     float *o_part;                  // [2 * grid][D / 4][rows] float4, weighted sums of a CTA's first and last unit
     float2 *ml_part;                // [2 * grid][rows] (running max in log2 units, running sum)
@@ -116,10 +119,11 @@ constexpr int kVarlenTcTileLog2 = 7;    // its keys per tile: 128
 constexpr int kVarlenGenTileLog2 = 6;   // keys per tile of the CUDA-core kernel: 64
 constexpr int kVarlenGenPerSm = 4;      // and its CTAs per SM at most
 constexpr int kVarlenFixed = 768;       // a unit's fixed cost, in keys (its queries, filling the pipeline, its epilogue)
-constexpr int kVarlenMinShare = 648;    // smallest share of a CTA, in the same keys: less than a unit of one key
 constexpr int kVarlenGroup = 2;         // a unit is cut at multiples of this many tiles
+// a share is longer than a group of any unit, and not longer than a unit of one key
+constexpr int kVarlenMinShare = 2 * 128 + kVarlenFixed / 2 + 8;
+constexpr int kVarlenMaxShift = 8;      // of the work line: a unit keeps a length of 3 at least
 constexpr int kVarlenMaxKv = 1 << 26;   // keys of a sequence
-static_assert(2 * 128 + kVarlenFixed / 2 < kVarlenMinShare, "a share is longer than a group of any unit");
 bool varlen_tc_supported(const VarlenParams &p);
 int varlen_generic_rows(const VarlenParams &p);        // rows per unit of the CUDA-core kernel
 int varlen_max_grid(int path, const VarlenParams &p);  // its CTAs that are resident at once (0: none)

@@ -55,15 +55,19 @@ __device__ __forceinline__ int vl_keys(const VarlenParams &p, const VlSeq &s, in
     return max(0, s.off + min(s.q, (r + 1) * p.tb));
 }
 
-// length of units [0, r) of one kv head on the work line, r <= nr
-__device__ __forceinline__ long vl_before(const VarlenParams &p, const VlSeq &s, int r) {
+// Length of units [0, r) of one kv head on the work line, r <= nr, in keys >>
+// line_shift: the exact sum, shifted, so that it never decreases with r.
+__device__ __forceinline__ int vl_before(const VarlenParams &p, const VlSeq &s, int r) {
     if (r == 0) return 0;
-    const int full = (p.causal ? max(0, s.off) + (r == s.nr ? s.q : 0) : s.kv) + kVarlenFixed;   // the last unit's
-    if (r == 1 && r == s.nr) return full;
-    if (!p.causal) return (long)r * full;
-    const int r1 = r == s.nr ? r - 1 : r;      // units of tb tokens among them
-    const long w = (long)r1 * (max(0, s.off) + kVarlenFixed) + (long)p.tb * ((long)r1 * (r1 + 1) / 2);
-    return r == s.nr ? w + full : w;
+    const int full = (p.causal ? max(s.kv, s.q) : s.kv) + kVarlenFixed;   // the last unit's
+    if (s.nr == 1) return full >> p.line_shift;
+    long w = (long)r * full;
+    if (p.causal) {
+        const int r1 = r == s.nr ? r - 1 : r;      // units of tb tokens among them
+        w = (long)r1 * (max(0, s.off) + kVarlenFixed) + (long)p.tb * ((long)r1 * (r1 + 1) / 2);
+        if (r == s.nr) w += full;
+    }
+    return (int)(w >> p.line_shift);
 }
 
 struct VlPos {          // a place on the work line: tile t of unit (b, g, r)
@@ -87,8 +91,8 @@ struct VlShared {
 struct VlPlan {
     int idle;
     VlPos begin, end;
-    long share;         // the line's length W = share * C + rest
-    int C, rest;        // CTAs that share it
+    VlSeq s;            // the sequence of `begin`
+    int share, total;   // CTA c takes [c share, (c + 1) share) of the line
 };
 
 __device__ __forceinline__ int vl_tiles(const VarlenParams &p, int keys) {
@@ -97,119 +101,134 @@ __device__ __forceinline__ int vl_tiles(const VarlenParams &p, int keys) {
 
 // cut of a unit of length len and `tiles` tiles at `off` (0 <= off <= len): the
 // tiles before it, in whole groups of kVarlenGroup.  Non-decreasing in off, and
-// two boundaries at least kVarlenMinShare apart never give the same cut inside
-// a unit of several groups (a group is at most 2 * 128 + kVarlenFixed / 2 long;
-// fp32 holds the quotient to 2^-4 of a group up to kVarlenMaxKv keys).
-__device__ __forceinline__ int vl_cut(long off, long len, int tiles, bool splittable) {
+// two boundaries a share apart never give the same cut inside a unit of several
+// groups (a share is longer than any group; fp32 holds the quotient to 2^-5 of
+// a group up to kVarlenMaxKv keys).
+__device__ __forceinline__ int vl_cut(int off, int len, int tiles, bool splittable) {
     const int groups = (tiles + kVarlenGroup - 1) / kVarlenGroup;
     if (!splittable || groups < 2) return 2 * off >= len ? tiles : 0;
-    const int g = (int)fmaf((float)off, (float)groups / (float)len, 0.5f);
+    const int g = (int)((float)off * ((float)groups / (float)len) + 0.5f);
     return min(tiles, g * kVarlenGroup);
 }
 __device__ __forceinline__ bool vl_splittable(const VarlenParams &p, const VlSeq &s) {
     return !p.causal || s.off >= 0;
 }
 
-// floor(W c / C): both products of the remainder are below 2^31
-__device__ __forceinline__ long vl_boundary(const VlPlan &pl, int c) {
-    return pl.share * c + (int)((unsigned)(pl.rest * c) / (unsigned)pl.C);
-}
-
-// the place of boundary x on the line, within sequence b whose part begins at `seq_x`
-__device__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, long seq_x, long x) {
-    const long head = vl_before(p, s, s.nr);
-    long o = x - seq_x;
+// the place of the boundary `o` past the beginning of sequence b's part of the line
+__device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, int o) {
+    const int head = vl_before(p, s, s.nr);
     int g = min((int)((float)o / (float)head), p.Hkv - 1);     // at most 4096 heads: one off at most
-    o -= (long)g * head;
+    o -= g * head;
     if (o < 0) { --g; o += head; }
     else if (o >= head && g < p.Hkv - 1) { ++g; o -= head; }
-    int lo = 0, hi = s.nr - 1;                  // the last unit that begins at or before o
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (vl_before(p, s, mid) <= o) lo = mid;
+    int r = 0, hi = s.nr - 1;                                  // the last unit that begins at or before o
+    while (r < hi) {
+        const int mid = (r + hi + 1) >> 1;
+        if (vl_before(p, s, mid) <= o) r = mid;
         else hi = mid - 1;
     }
-    const long u0 = vl_before(p, s, lo), len = vl_before(p, s, lo + 1) - u0;
-    const int tiles = vl_tiles(p, vl_keys(p, s, lo));
-    const int t = vl_cut(o - u0, len, tiles, vl_splittable(p, s));
-    VlPos r = {b, g, lo, t};
-    if (t >= tiles && (tiles > 0 || 2 * (o - u0) >= len)) {      // at its end: the next unit's beginning
-        r.t = 0;
-        if (++r.r == s.nr) { r.r = 0; ++r.g; }
-        if (r.g == p.Hkv) { r.g = 0; ++r.b; }
+    const int u0 = vl_before(p, s, r), len = vl_before(p, s, r + 1) - u0;
+    const int tiles = vl_tiles(p, vl_keys(p, s, r));
+    int t = vl_cut(o - u0, len, tiles, vl_splittable(p, s));
+    if (t >= tiles && (tiles > 0 || 2 * (o - u0) >= len)) {    // at its end: the next unit's beginning
+        t = 0;
+        if (++r == s.nr) {
+            r = 0;
+            if (++g == p.Hkv) { g = 0; ++b; }
+        }
     }
-    return r;
+    return {b, g, r, t};
 }
 
-// The share of CTA `c` of `grid` (one full warp).  Up to 32 sequences are read
-// once and kept in the lanes' registers.
-__device__ VlPlan vl_plan(const VarlenParams &p, int c, int grid) {
+// The share of CTA `c` (one full warp).  The code runs once per CTA, so it is
+// kept short: most of its time is instruction fetch.  The line's length stays
+// below 2^31 (the host picks line_shift by its bounds); offsets that are no
+// offsets could exceed it and then nothing is computed.
+__device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
     const int lane = threadIdx.x & 31;
     VlPlan pl = {};
     VlSeq s = {};
-    long w = 0, tot = 0;
-    for (int b = lane; b < p.B; b += 32) {
-        s = vl_seq(p, b, c == 0);
-        w = (long)p.Hkv * vl_before(p, s, s.nr);
-        tot += w;
+    unsigned w = 0, total = 0, coarse = 0;
+    auto read = [&](int b, bool report) {
+        w = 0;
+        if (b < p.B) {
+            s = vl_seq(p, b, report);
+            w = (unsigned)p.Hkv * (unsigned)vl_before(p, s, s.nr);
+        }
+    };
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        read(b0 + lane, c == 0);
+        total += __reduce_add_sync(0xffffffffu, w);
+        coarse = min(coarse + __reduce_add_sync(0xffffffffu, w >> 8), 1u << 30);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    pl.C = tot < (long)grid * kVarlenMinShare ? max(1, (int)((unsigned)tot / (unsigned)kVarlenMinShare)) : grid;
-    pl.idle = tot == 0 || c >= pl.C;
+    pl.total = (int)total;
+    if (coarse >= (1u << 23) - 1024u) {
+        if (c == 0 && lane == 0) set_fault(p.fault, FAULT_BAD_LENGTH);
+        pl.total = 0;
+    }
+    // the smallest share the grid covers the line with (rounded up past fp32's error)
+    pl.share = max(p.min_share, (int)((float)pl.total * p.inv_grid * (1.0f + 0x1p-20f)) + 1);
+    const int x0 = c * pl.share, x1 = x0 + pl.share;
+    pl.idle = x0 >= pl.total;
     if (pl.idle) return pl;
-    if (tot >> 32) {
-        pl.share = tot / pl.C;
-        pl.rest = (int)(tot - pl.share * pl.C);
-    } else {
-        pl.share = (unsigned)tot / (unsigned)pl.C;
-        pl.rest = (int)((unsigned)tot - (unsigned)pl.share * (unsigned)pl.C);
-    }
-    const long x0 = vl_boundary(pl, c), x1 = vl_boundary(pl, c + 1);
     // the sequences in which the share begins and ends: lane 0 then places the
     // beginning and lane 1 the end, side by side
-    long base = 0, seq_x = 0;
-    VlSeq mine = {};
-    int found = -1;
+    const int x = lane == 0 ? x0 : x1;
+    int base = 0, o = 0, found = p.B;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        if (p.B > 32) {
-            w = 0;
-            if (b0 + lane < p.B) {
-                s = vl_seq(p, b0 + lane, false);
-                w = (long)p.Hkv * vl_before(p, s, s.nr);
-            }
-        }
-        long incl = w;
+        if (p.B > 32) read(b0 + lane, false);
+        int e = (int)w;
         if (p.B > 1) {
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
+#pragma unroll 1
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, e, d);
+                if (lane >= d) e += y;
             }
         }
-        const long a = base + incl - w, e = base + incl;
+        e += base;
+        const int a = e - (int)w;
         const unsigned ms = __ballot_sync(0xffffffffu, x0 >= a && x0 < e);
         const unsigned me = __ballot_sync(0xffffffffu, x1 >= a && x1 < e);
         const unsigned m = lane == 0 ? ms : me;
-        const int src = m ? __ffs((int)m) - 1 : 0;
+        const int src = __ffs((int)m) - 1;         // -1 where there is none: lane 31, not used
         VlSeq t;
         t.c0 = __shfl_sync(0xffffffffu, s.c0, src);
         t.q = __shfl_sync(0xffffffffu, s.q, src);
         t.kv = __shfl_sync(0xffffffffu, s.kv, src);
         t.nr = __shfl_sync(0xffffffffu, s.nr, src);
-        t.off = t.kv - t.q;
-        const long ta = __shfl_sync(0xffffffffu, a, src);
-        if (m && found < 0) { mine = t; seq_x = ta; found = b0 + src; }
+        const int ta = __shfl_sync(0xffffffffu, a, src);
+        if (m && found == p.B) {
+            t.off = t.kv - t.q;
+            pl.s = t;
+            o = x - ta;
+            found = b0 + src;
+        }
         if (me) break;
         base = __shfl_sync(0xffffffffu, e, 31);
     }
     VlPos at = {p.B, 0, 0, 0};
-    if (lane < 2 && found >= 0) at = vl_locate(p, found, mine, seq_x, lane == 0 ? x0 : x1);
-    pl.begin = {__shfl_sync(0xffffffffu, at.b, 0), __shfl_sync(0xffffffffu, at.g, 0),
-                __shfl_sync(0xffffffffu, at.r, 0), __shfl_sync(0xffffffffu, at.t, 0)};
-    pl.end = {__shfl_sync(0xffffffffu, at.b, 1), __shfl_sync(0xffffffffu, at.g, 1),
-              __shfl_sync(0xffffffffu, at.r, 1), __shfl_sync(0xffffffffu, at.t, 1)};
+    if (lane < 2 && found < p.B) at = vl_locate(p, found, pl.s, o);
+    if (at.b != found) pl.s.nr = 0;   // the next sequence's beginning: not yet read
+    pl.begin = at;      // lane 0's; lane 1 holds the end
+    pl.end = at;
     return pl;
+}
+
+// writes the plan that lanes 0 and 1 hold
+__device__ __forceinline__ void vl_plan_store(const VlPlan &q, VlPlan *to) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        to->idle = q.idle;
+        to->begin = q.begin;
+        to->s = q.s;
+        to->share = q.share;
+        to->total = q.total;
+    } else if (lane == 1) {
+        to->end = q.end;
+    }
+    __syncwarp();
 }
 
 // Walks a CTA's units in order; every warp role runs its own copy.
@@ -218,7 +237,7 @@ struct VlWalk {
     VlSeq s;
     bool fresh;         // s is that of at.b
 
-    __device__ __forceinline__ explicit VlWalk(const VlPlan &pl) : at(pl.begin), fresh(false) {}
+    __device__ __forceinline__ explicit VlWalk(const VlPlan &pl) : at(pl.begin), s(pl.s), fresh(pl.s.nr > 0) {}
 
     __device__ __forceinline__ bool next(const VarlenParams &p, const VlPlan &pl, VlUnit &u) {
         for (;;) {
@@ -257,45 +276,14 @@ __device__ __forceinline__ int vl_limit(const VarlenParams &p, const VlUnit &u, 
     return p.causal ? max(0, min(u.kv, u.off + i + 1)) : u.kv;
 }
 
-// The CTAs of a unit that CTA c shares: `opens` when its part begins at tile 0.
-// seq_x: where the unit's sequence begins on the line.
-__device__ VlShared vl_shared(const VarlenParams &p, const VlPlan &pl, int c, const VlUnit &u, long seq_x) {
-    const VlSeq s = vl_seq(p, u.b, false);
-    const long X = seq_x + (long)u.g * vl_before(p, s, s.nr) + vl_before(p, s, u.r);
-    const long len = vl_before(p, s, u.r + 1) - vl_before(p, s, u.r);
-    const bool sp = vl_splittable(p, s);
-    // the first boundary that cuts after at least one tile, and the last that cuts before the last;
-    // c is within a few of both where the unit has few CTAs, else the estimates start nearby
-    const float inv = 1.0f / ((float)pl.share + (float)pl.rest / (float)pl.C);
-    int lo = max(0, (int)((float)X * inv) - 1);
-    while (lo > 0 && vl_boundary(pl, lo - 1) >= X) --lo;
-    while (lo < pl.C && (vl_boundary(pl, lo) < X || vl_cut(vl_boundary(pl, lo) - X, len, u.tiles, sp) < 1)) ++lo;
-    int hi = min(pl.C, (int)((float)(X + len) * inv) + 1);
-    while (hi < pl.C && vl_boundary(pl, hi + 1) <= X + len) ++hi;
-    while (hi > lo && (vl_boundary(pl, hi) > X + len ||
-                       vl_cut(vl_boundary(pl, hi) - X, len, u.tiles, sp) >= u.tiles)) --hi;
-    VlShared r;
-    r.c0 = lo - 1;
-    r.n = hi - lo + 2;
-    r.s = c - r.c0;
-    r.slot = u.t0 == 0 ? 2 * c + 1 : 2 * c;
-    r.g = u.g;
-    r.row0 = u.row0;
-    r.ntok = u.ntok;
-    return r;
-}
-
 // where sequence b begins on the work line (one full warp)
-__device__ long vl_seq_start(const VarlenParams &p, int b_end) {
-    const int lane = threadIdx.x & 31;
-    long tot = 0;
-    for (int b = lane; b < b_end; b += 32) {
+__device__ int vl_seq_start(const VarlenParams &p, int b_end) {
+    unsigned tot = 0;
+    for (int b = threadIdx.x & 31; b < b_end; b += 32) {
         const VlSeq s = vl_seq(p, b, false);
-        tot += (long)p.Hkv * vl_before(p, s, s.nr);
+        tot += (unsigned)p.Hkv * (unsigned)vl_before(p, s, s.nr);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    return tot;
+    return (int)__reduce_add_sync(0xffffffffu, tot);
 }
 
 // the units that CTA c shares with others (one full warp): the one its share
@@ -306,24 +294,35 @@ struct VlEnds {
 };
 __device__ VlEnds vl_ends(const VarlenParams &p, const VlPlan &pl, int c) {
     VlEnds e = {};
-    auto unit_at = [&](const VlPos &at, int t0) {
-        const VlSeq s = vl_seq(p, at.b, false);
-        VlUnit u = {};
-        u.b = at.b; u.g = at.g; u.r = at.r;
-        u.row0 = s.c0 + at.r * p.tb;
-        u.ntok = min(p.tb, s.q - at.r * p.tb);
-        u.tiles = vl_tiles(p, vl_keys(p, s, at.r));
-        u.t0 = t0;
-        return u;
-    };
     const bool same = pl.begin.b == pl.end.b && pl.begin.g == pl.end.g && pl.begin.r == pl.end.r;
-    if (pl.begin.t > 0) {
-        const long x = vl_seq_start(p, pl.begin.b);
-        e.u[e.n++] = vl_shared(p, pl, c, unit_at(pl.begin, pl.begin.t), x);
-    }
-    if (pl.end.t > 0 && !(same && pl.begin.t > 0)) {
-        const long x = vl_seq_start(p, pl.end.b);
-        e.u[e.n++] = vl_shared(p, pl, c, unit_at(pl.end, 0), x);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const VlPos at = i == 0 ? pl.begin : pl.end;
+        if (at.t == 0 || (i == 1 && same && pl.begin.t > 0)) continue;
+        const VlSeq s = vl_seq(p, at.b, false);
+        const int u0 = vl_before(p, s, at.r), len = vl_before(p, s, at.r + 1) - u0;
+        const int X = vl_seq_start(p, at.b) + at.g * vl_before(p, s, s.nr) + u0;
+        const int tiles = vl_tiles(p, vl_keys(p, s, at.r));
+        // the CTAs whose shares meet the unit, but for those whose part is cut to nothing:
+        // c - 1 down to the first boundary that leaves tiles before it, and up to the last
+        // that leaves tiles behind it
+        auto cuts = [&](int k) {       // whether boundary k lies inside the unit
+            const int x = k * pl.share;
+            if (k < 1 || x <= X || x >= X + len || x >= pl.total) return false;
+            const int t = vl_cut(x - X, len, tiles, vl_splittable(p, s));
+            return t > 0 && t < tiles;
+        };
+        int lo = X / pl.share + 1, hi = (X + len) / pl.share;     // boundaries within the unit
+        while (lo < hi && !cuts(lo)) ++lo;                        // the one that makes it shared is among them
+        while (hi > lo && !cuts(hi)) --hi;
+        VlShared &r = e.u[e.n++];
+        r.c0 = lo - 1;
+        r.n = hi - lo + 2;
+        r.s = c - r.c0;
+        r.slot = i == 0 ? 2 * c : 2 * c + 1;
+        r.g = at.g;
+        r.row0 = s.c0 + at.r * p.tb;
+        r.ntok = min(p.tb, s.q - at.r * p.tb);
     }
     return e;
 }
@@ -357,6 +356,12 @@ __device__ __forceinline__ void vl_store4(const VarlenParams &p, long row, int c
     }
 }
 
+__device__ __forceinline__ float vl_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Joins this CTA's n-th of a shared unit's rows (`nt` threads, numbered by
 // `tid`, that meet at barrier `bar`).  Row k of the
 // unit is query head k % G of token k / G; in a slot the first `tpt` tokens'
@@ -387,7 +392,7 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
         // kJoinItems items of a thread at a time, so that the loads of all are in
         // flight together; the loops run the same number of times in every thread,
         // so that whole warps meet at the shuffles
-        constexpr int kJoinItems = 4;
+        constexpr int kJoinItems = 2;
         const int stride = nt / lanes;
         for (int i0 = ia + tid / lanes; __any_sync(0xffffffffu, i0 < ie); i0 += kJoinItems * stride) {
             float M[kJoinItems], l[kJoinItems], acc[kJoinItems][8];
@@ -405,6 +410,7 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
 #pragma unroll
                 for (int x = 0; x < 8; ++x) acc[q][x] = 0.f;
             }
+#pragma unroll 1
             for (int e = sub; e < sh.n; e += lanes) {
                 const long slot = e == 0 ? 2L * sh.c0 + 1 : 2L * (sh.c0 + e);
                 float4 va[kJoinItems], vb[kJoinItems];
@@ -420,7 +426,7 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
                 for (int q = 0; q < kJoinItems; ++q) {
                     const float m = fmaxf(M[q], ml[q].x);
                     const float ref = m == -INFINITY ? 0.f : m;
-                    const float f = exp2f(M[q] - ref), w = exp2f(ml[q].x - ref);   // 0 for what saw nothing
+                    const float f = vl_ex2(M[q] - ref), w = vl_ex2(ml[q].x - ref);   // 0 for what saw nothing
                     M[q] = m;
                     l[q] = l[q] * f + w * ml[q].y;
                     const float v[8] = {va[q].x, va[q].y, va[q].z, va[q].w, vb[q].x, vb[q].y, vb[q].z, vb[q].w};
@@ -430,10 +436,11 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
             }
 #pragma unroll
             for (int q = 0; q < kJoinItems; ++q) {
+#pragma unroll 1
                 for (int o = 1; o < lanes; o <<= 1) {
                     const float M2 = __shfl_xor_sync(0xffffffffu, M[q], o), l2 = __shfl_xor_sync(0xffffffffu, l[q], o);
                     const float m = fmaxf(M[q], M2), ref = m == -INFINITY ? 0.f : m;
-                    const float f1 = exp2f(M[q] - ref), f2 = exp2f(M2 - ref);
+                    const float f1 = vl_ex2(M[q] - ref), f2 = vl_ex2(M2 - ref);
                     l[q] = f1 * l[q] + f2 * l2;
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
