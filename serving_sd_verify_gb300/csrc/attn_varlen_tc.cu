@@ -43,7 +43,8 @@ constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;   // 216 * 256 + 72 * 128 = 1
 constexpr int kLaunchRegs = 168;
 static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads, "register shares within the launch's");
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescale = 8.0f;            // log2 units
+constexpr float kRescale = 16.0f;           // log2 units
+constexpr int kPFirst = 64;                 // keys of P announced first; P V of these runs while the others' weights are made
 
 template <int D> struct Lay {
     static constexpr int kHalves = D / 64;
@@ -52,8 +53,9 @@ template <int D> struct Lay {
     static constexpr int kOffQ = 0;                        // two row tiles
     static constexpr int kOffRing = 2 * kTile;
     static constexpr int kOffBar = kOffRing + kSlots * kTile;
-    // full[slots] empty[slots] qfull qempty sfull[2] pfull[2][2] ofull[2] ofree[2]
-    static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 2 + 2;
+    static constexpr int kMaxSlots = kSlots + 1;           // where no unit has a second row tile, its room too
+    // full[max] empty[max] qfull qempty sfull[2] pfull[2][2] ofull[2] ofree[2]
+    static constexpr int kBars = 2 * kMaxSlots + 2 + 2 + 4 + 2 + 2;
     static constexpr int kOffMl = kOffBar + 8 * kBars + 8; // [2][128] max and sum of stream 1
     static constexpr int kOffMisc = kOffMl + 2 * 128 * 4;
     static constexpr int kSmem = kOffMisc + 256 + 1024;    // + alignment slack
@@ -93,6 +95,38 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     }
 }
 
+// K or V of 128 keys of the packed rows, or one page's 64 columns, with an L2 policy
+__device__ __forceinline__ void load_kv_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, uint64_t policy, int row,
+                                           int g) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(0), "r"(g), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void load_kv_5d(uint32_t dst, const CUtensorMap *map, uint32_t bar, uint64_t policy, int slot,
+                                           int half, int g, int page) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(slot), "r"(half), "r"(g), "r"(page), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13,"
+        " %14, %15}, [%16];"
+        : SDV_R8(0), SDV_R8(8)
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_bind16(uint32_t (&r)[16]) { asm volatile("" : SDV_W8(0), SDV_W8(8)); }
+
 // true in one lane of a converged warp, the same one each time
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -103,7 +137,8 @@ __device__ __forceinline__ bool elect_one() {
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                      const __grid_constant__ CUtensorMap tmap_v, const VarlenParams p, const int tpt, const int box) {
+                      const __grid_constant__ CUtensorMap tmap_v, const VarlenParams p, const int tpt, const int box,
+                      const int small) {
     using L = Lay<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -112,10 +147,11 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = (int)blockIdx.x;
 
-    const uint32_t sQ = base + L::kOffQ, sRing = base + L::kOffRing, bar0 = base + L::kOffBar;
+    const uint32_t sQ = base + L::kOffQ, sRing = base + L::kOffRing - (small ? L::kTile : 0), bar0 = base + L::kOffBar;
+    const int slots = small ? L::kMaxSlots : L::kSlots;
     auto full_bar = [&](int i) { return bar0 + 8u * i; };
-    auto empty_bar = [&](int i) { return bar0 + 8u * (L::kSlots + i); };
-    const uint32_t bar1 = bar0 + 8u * (2 * L::kSlots);
+    auto empty_bar = [&](int i) { return bar0 + 8u * (L::kMaxSlots + i); };
+    const uint32_t bar1 = bar0 + 8u * (2 * L::kMaxSlots);
     const uint32_t qfull_bar = bar1, qempty_bar = bar1 + 8u;
     auto sfull_bar = [&](int i) { return bar1 + 8u * (2 + i); };             // S_i computed
     auto pfull_bar = [&](int i, int h) { return bar1 + 8u * (4 + 2 * i + h); };   // half h of P_i written (4 warps)
@@ -126,7 +162,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     volatile int *abort_flag = &misc->abort_flag;
 
     if (tid == 0) {
-        for (int i = 0; i < L::kSlots; ++i) { mbar_init(full_bar(i), 1); mbar_init(empty_bar(i), 1); }
+        for (int i = 0; i < L::kMaxSlots; ++i) { mbar_init(full_bar(i), 1); mbar_init(empty_bar(i), 1); }
         mbar_init(qfull_bar, 1);
         mbar_init(qempty_bar, 1);
         for (int i = 0; i < 2; ++i) {
@@ -174,11 +210,17 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 uint32_t qphase = 0;
                 long loads = 0, units = 0;
                 bool ok = true;
+                // K and V that one unit alone reads leave L2 first (one token over 25,119: 24.9 -> 23.2 us);
+                // what several units read stays as usual
+                uint64_t once, again;
+                asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+                asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
                 const int per_half = 128 / box;        // copies per 64-column block of a tile
                 while (ok && walk.next(p, pl, u)) {
                     const int n = u.t1 - u.t0;
                     if (n <= 0) continue;
                     const int la = u.ntok <= tpt ? 2 : 1;
+                    const uint64_t policy = walk.s.nr == 1 ? once : again;
                     const int32_t *trow = kPaged ? p.table + (long)u.b * p.table_stride : nullptr;
                     // the lane's page of tile t: looked up a tile ahead, first used (and checked) by its copy
                     auto page_of = [&](int t) {
@@ -191,7 +233,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         return pg;
                     };
                     auto load_tile = [&](bool is_v, int t, int pg) {
-                        if (ok && loads >= L::kSlots)
+                        if (ok && loads >= slots)
                             ok = wait_bar(empty_bar(rp.slot), rp.phase ^ 1u, abort_flag, p.fault);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) return;
@@ -200,7 +242,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         if (!kPaged) {
                             if (lane == 0) {
                                 mbar_arrive_expect_tx(bar, (uint32_t)L::kTile);
-                                tma_load_4d(dst, map, bar, 0, u.row0 - u.tok0 + t * 128, 0, u.g);
+                                load_kv_4d(dst, map, bar, policy, u.row0 - u.tok0 + t * 128, u.g);
                             }
                         } else {
                             const int boxes = min(per_half, (u.kv - t * 128 + box - 1) / box);
@@ -213,11 +255,11 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                     set_fault(p.fault, FAULT_BAD_PAGE);
                                     pg = p.n_pages;
                                 }
-                                tma_load_5d(dst + h * (128 * 128) + i * box * 128, map, bar, 0,
-                                            p.page_log2 >= 0 ? key & (p.page_size - 1) : key % p.page_size, h, u.g, pg);
+                                load_kv_5d(dst + h * (128 * 128) + i * box * 128, map, bar, policy,
+                                           p.page_log2 >= 0 ? key & (p.page_size - 1) : key % p.page_size, h, u.g, pg);
                             }
                         }
-                        rp.step(L::kSlots);
+                        rp.step(slots);
                         ++loads;
                     };
                     int pk = page_of(u.t0), pv = pk;      // pages of the next K tile, of the V tile behind it
@@ -267,10 +309,10 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 }
                 // the copies still in flight land before the CTA's shared memory goes
                 if (*abort_flag) {
-                    const int m = (int)(loads < L::kSlots ? loads : (long)L::kSlots);
+                    const int m = (int)min(loads, (long)slots);
                     RingPos a = rp;
                     for (int i = 0; i < m; ++i) {
-                        if (a.slot == 0) { a.slot = L::kSlots - 1; a.phase ^= 1u; } else --a.slot;
+                        if (a.slot == 0) { a.slot = slots - 1; a.phase ^= 1u; } else --a.slot;
                         wait_bar(full_bar(a.slot), a.phase, nullptr, p.fault);
                     }
                     if (units > 0) wait_bar(qfull_bar, qphase ^ 1u, nullptr, p.fault);
@@ -315,7 +357,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             if (!ok) return;
                             tc_fence_after();
 #pragma unroll
-                            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk)
                                 if (el) umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + kk * (16 * 128 / 16), idO,
                                         (!first || kk > 0) ? 1u : 0u);
                         }
@@ -342,14 +384,14 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         issue_s(0, 0, rp.slot);
                         if (pair) issue_s(1, 1, rp.slot);
                         if (el) umma_commit(empty_bar(rp.slot));
-                        rp.step(L::kSlots);
+                        rp.step(slots);
                         if (pair) {
                             if (n == 1) if (el) umma_commit(qempty_bar);
                             for (int j = 0; ok && j < n; ++j) {
                                 wait_tile();
                                 if (!ok) break;
                                 const RingPos vp = rp;
-                                rp.step(L::kSlots);
+                                rp.step(slots);
                                 if (j == 0) claim(0);
                                 issue_pv(0, vp.slot, j == 0);
                                 if (!ok) break;
@@ -367,7 +409,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 if (j + 1 < n) {
                                     issue_s(1, 1, rp.slot);
                                     if (el) umma_commit(empty_bar(rp.slot));
-                                    rp.step(L::kSlots);
+                                    rp.step(slots);
                                     if (j + 2 == n) if (el) umma_commit(qempty_bar);
                                 } else {
                                     if (el) umma_commit(ofull_bar(1));
@@ -379,7 +421,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 if (!ok) break;
                                 issue_s(1, 0, rp.slot);
                                 if (el) umma_commit(empty_bar(rp.slot));
-                                rp.step(L::kSlots);
+                                rp.step(slots);
                             }
                             if (n <= 2) if (el) umma_commit(qempty_bar);
                             for (int j = 0; ok && j < n; ++j) {
@@ -390,13 +432,13 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 issue_pv(i, rp.slot, j < 2);
                                 if (!ok) break;
                                 if (el) umma_commit(empty_bar(rp.slot));
-                                rp.step(L::kSlots);
+                                rp.step(slots);
                                 if (j + 2 < n) {
                                     wait_tile();
                                     if (!ok) break;
                                     issue_s(i, 0, rp.slot);
                                     if (el) umma_commit(empty_bar(rp.slot));
-                                    rp.step(L::kSlots);
+                                    rp.step(slots);
                                     if (j + 3 == n) if (el) umma_commit(qempty_bar);
                                 } else {
                                     if (el) umma_commit(ofull_bar(i));
@@ -424,7 +466,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             VlWalk walk(pl);
             VlUnit u;
             uint32_t sphase = 0, ophase = 0, ophase1 = 0;
-            long ring = 0;                             // tiles that went through the ring before this unit
+            unsigned ring = 0;                         // tiles that went through the ring before this unit
             bool ok = true;
             while (walk.next(p, pl, u)) {
                 const int n = u.t1 - u.t0;
@@ -446,11 +488,11 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         // slots past the sequence may hold anything, and 0 times that is not 0:
                         // one stream clears those rows of the last V tile before its product
                         const int nk = min(la, n);
-                        const long idx = ring + nk + j + min(j, n - nk);
-                        const int slot = (int)(idx % L::kSlots);
-                        ok = __all_sync(0xffffffffu, wait_bar(full_bar(slot), (uint32_t)(idx / L::kSlots) & 1u,
+                        const unsigned idx = ring + nk + j + min(j, n - nk);
+                        const int slot = (int)(idx % (unsigned)slots);
+                        ok = __all_sync(0xffffffffu, wait_bar(full_bar(slot), (idx / (unsigned)slots) & 1u,
                                                                abort_flag, p.fault)) && ok;
-                        uint8_t *vt = sbase + L::kOffRing + slot * L::kTile;
+                        uint8_t *vt = sbase + (sRing - base) + slot * L::kTile;
                         const int v0 = u.kv - key0;
                         // the live warps share the rows
                         const int live = min(4, ((pair ? tpt : min(u.ntok, tpt)) * G + 31) / 32);
@@ -478,17 +520,32 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 for (int e = 0; e < 32; ++e)
                                     if (32 * c + e >= vis) s[c][e] = 0xff800000u;
                         }
-                        float mx[8];
+                        const float2 qk2 = make_float2(qk, qk);
+                        float2 ls[2], nm2;
+                        uint32_t pk[16];
+                        // weights of 16 keys: 8 words from `at`
+                        auto weights = [&](int at) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t *src = s[i >> 1] + 16 * (i & 1);
-                            float m8 = __uint_as_float(src[0]);
+                            for (int c = at; c < at + 16; ++c) {
+                                const uint32_t *src = s[c >> 4] + 2 * (c & 15);
+                                const float2 x = __ffma2_rn(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])),
+                                                            qk2, nm2);
+                                const float p0 = ex2(x.x), p1 = ex2(x.y);
+                                ls[c & 1] = __fadd2_rn(ls[c & 1], make_float2(p0, p1));
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+                                pk[c & 15] = *reinterpret_cast<const uint32_t *>(&b2);
+                            }
+                        };
+                        float m4[4];
 #pragma unroll
-                            for (int e = 1; e < 16; ++e) m8 = fmaxf(m8, __uint_as_float(src[e]));
-                            mx[i] = m8;
+                        for (int i = 0; i < 4; ++i) {
+                            float m = max3(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]), __uint_as_float(s[i][2]));
+#pragma unroll
+                            for (int e = 3; e < 31; e += 2)
+                                m = max3(m, __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+                            m4[i] = fmaxf(m, __uint_as_float(s[i][31]));
                         }
-                        const float tmax = qk * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                                      fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+                        const float tmax = qk * fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
                         const bool need = tmax > m_used + kRescale;     // true at first while m_used = -inf
                         float alpha = 1.f;
                         if (need) {
@@ -499,41 +556,36 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             // S_j is complete, hence every earlier product of this stream too
                             // (they were issued before it and complete in order)
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32_async(o_col + 32u * c, o);
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16_async(o_col + 16u * c, o);
                                 tmem_ld_wait();
-                                tmem_ld_bind(o);
+                                tmem_ld_bind16(o);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                tmem_st32(o_col + 32u * c, o);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(o_col + 16u * c, o);
                             }
                         }
-                        l *= alpha;
                         const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                        const float2 qk2 = make_float2(qk, qk), nm2 = make_float2(neg_m, neg_m);
-                        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int q = 2 * h; q < 2 * h + 2; ++q) {     // 32 keys at a time
-                                uint32_t pk[16];
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) {
-                                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[q][2 * c]),
-                                                                            __uint_as_float(s[q][2 * c + 1])), qk2, nm2);
-                                    const float p0 = ex2(x.x), p1 = ex2(x.y);
-                                    ls[c & 1] = __fadd2_rn(ls[c & 1], make_float2(p0, p1));
-                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-                                    pk[c] = *reinterpret_cast<const uint32_t *>(&b2);
-                                }
-                                tmem_st16(s_col + 16u * q, pk);
-                            }
-                            tmem_st_wait();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(pfull_bar(w, h));
-                        }
+                        nm2 = make_float2(neg_m, neg_m);
+                        ls[0] = ls[1] = make_float2(0.f, 0.f);
+                        weights(0);
+                        l *= alpha;
+                        tmem_st16(s_col, pk);
+                        weights(16);
+                        tmem_st16(s_col + 16u, pk);
+                        weights(32);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pfull_bar(w, 0));
+                        tmem_st16(s_col + 32u, pk);
+                        weights(48);
+                        tmem_st16(s_col + 48u, pk);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pfull_bar(w, 1));
                         l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
                     } else {
                         tc_fence_before();
@@ -754,7 +806,8 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kPaged>, mq, mk, mv, p, tpt, box_rows);
+    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kPaged>, mq, mk, mv, p, tpt, box_rows,
+                              p.max_q <= tpt ? 1 : 0);
 }
 
 }  // namespace
@@ -762,13 +815,19 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
 bool varlen_tc_supported(const VarlenParams &p) {
     if (p.dt != SD_BF16 || (p.D != 64 && p.D != 128) || p.Hq / p.Hkv > kVarlenMaxGroup) return false;
     if (p.table && p.page_size % 8) return false;      // a copy's rows start on the swizzle's 8-row period
-    if (!encode_fn_vl()) return false;
-    int dev = 0, optin = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return false;
-    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    return optin >= Lay<128>::kSmem && optin >= Lay<64>::kSmem && major == 10 && minor == 3;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    static std::atomic<int> known[kMaxDevices];       // per device: 0 not asked, 1 no, 2 yes
+    int k = known[dev].load(std::memory_order_acquire);
+    if (k == 0) {
+        int optin = 0, major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return false;
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+        k = encode_fn_vl() && optin >= Lay<128>::kSmem && optin >= Lay<64>::kSmem && major == 10 && minor == 3 ? 2 : 1;
+        known[dev].store(k, std::memory_order_release);
+    }
+    return k == 2;
 }
 
 cudaError_t launch_varlen_tc(const VarlenParams &p, int grid, cudaStream_t st) {

@@ -339,7 +339,6 @@ __device__ __noinline__ bool vl_wait(const unsigned int *ctr, unsigned int targe
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
             if (t - t0 > limit_ns) return false;
         }
-        __nanosleep(32);
     }
 }
 

@@ -450,24 +450,44 @@ def sd_latent_compress(queries, features, out, ws, stream=None):
 
 def _on_current_device(*ts):
     """Every tensor (None left out) on the current CUDA device: the calls use
-    its stream and its fault word."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    its stream and its fault word.  Returns the device's number."""
+    dev = -1
     for t in ts:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError("all tensors must be CUDA tensors on the current device")
+        if t is not None:
+            d = t.get_device()       # -1 for a CPU tensor
+            if d != dev:
+                if dev >= 0 or d < 0:
+                    raise ValueError("all tensors must be CUDA tensors on the current device")
+                dev = d
+    if dev != torch.cuda.current_device():
+        raise ValueError("all tensors must be CUDA tensors on the current device")
+    return dev
 
 
-def _table(t, name):
-    if t.dtype != torch.int32 or t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError(f"{name} is int32 [B, columns] with contiguous rows")
+# the current stream's handle without a Stream object: these calls are short
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _paged_cache(k_pages, v_pages, page_table) -> PagedCache:
-    _table(page_table, "page_table")
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
-        raise ValueError("k_pages and v_pages are [pages, page_size, Hkv, D] of equal shape and strides")
-    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), _kv_strides(k_pages), page_table.data_ptr(),
-                      page_table.stride(0), page_table.shape[1], k_pages.shape[0], k_pages.shape[1])
+def _stream_on(stream, dev) -> int:
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+def _paged_cache(k_pages, v_pages, page_table, cu_q, kv_len):
+    """(the C struct, sequences, Hkv, D) of a cache and the lengths that go with it."""
+    shape, strides = k_pages.shape, k_pages.stride()
+    if len(shape) != 4 or shape != v_pages.shape or strides != v_pages.stride() or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k_pages and v_pages are [pages, page_size, Hkv, D] of equal shape, strides and dtype")
+    if strides[3] != 1:
+        raise ValueError("the D axis of the cache must be contiguous")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise ValueError("page_table is int32 [B, columns] with contiguous rows")
+    _i32_cuda(cu_q, kv_len)
+    B, cols = page_table.shape
+    if kv_len.dim() != 1 or cu_q.dim() != 1 or kv_len.numel() != B or cu_q.numel() != B + 1:
+        raise ValueError("cu_q is [B + 1], kv_len [B], and page_table has B rows")
+    cache = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), Strides(strides[0], strides[1], strides[2]),
+                       page_table.data_ptr(), page_table.stride(0), cols, shape[0], shape[1])
+    return cache, B, shape[2], shape[3]
 
 
 def sd_rotary_table(rot_dim, theta, scaling="none", factor=1.0, original_max=0, low=1.0, high=32.0):
@@ -485,24 +505,27 @@ def sd_rotary_table(rot_dim, theta, scaling="none", factor=1.0, original_max=0, 
 def _rope_args(turns, positions, N, layout):
     if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
         raise ValueError("turns is the int64 [rot_dim / 2] table of sd_rotary_table, on the device")
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (N,) or
-                                  not positions.is_contiguous()):
+    if positions is not None and (positions.dtype != torch.int32 or positions.dim() != 1 or
+                                  positions.numel() != N or not positions.is_contiguous()):
         raise ValueError("positions is contiguous int32 [N]")
-    if layout not in ROPE_LAYOUTS:
+    lay = ROPE_LAYOUTS.get(layout)
+    if lay is None:
         raise ValueError(f"layout is one of {sorted(ROPE_LAYOUTS)}")
-    return ROPE_LAYOUTS[layout]
+    return lay
 
 
 def sd_rotary(x, y, positions, turns, magnitude=1.0, layout="half", stream=None):
     """x, y [N, H, D] (D contiguous; y may be x); positions int32 [N]."""
-    _on_current_device(x, y, positions, turns)
-    N, H, D = x.shape
+    dev = _on_current_device(x, y, positions, turns)
+    shape = x.shape
+    N, H, D = shape
     lay = _rope_args(turns, positions, N, layout)
-    if y.shape != x.shape or y.dtype != x.dtype or x.stride(2) != 1 or y.stride(2) != 1:
+    xt, xh, xd = x.stride()
+    yt, yh, yd = y.stride()
+    if y.shape != shape or y.dtype != x.dtype or xd != 1 or yd != 1:
         raise ValueError("x and y are [N, H, D] of one dtype with contiguous last axes")
-    _check(load().sd_rotary(x.data_ptr(), x.stride(0), x.stride(1), y.data_ptr(), y.stride(0), y.stride(1),
-                            positions.data_ptr(), turns.data_ptr(), float(magnitude), N, H, D, 2 * turns.shape[0], lay,
-                            _dt(x), _stream(stream)))
+    _check(load().sd_rotary(x.data_ptr(), xt, xh, y.data_ptr(), yt, yh, positions.data_ptr(), turns.data_ptr(),
+                            magnitude, N, H, D, 2 * turns.numel(), lay, _dt(x), _stream_on(stream, dev)))
 
 
 def sd_rotary_append_paged(q, k, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages,
@@ -511,30 +534,30 @@ def sd_rotary_append_paged(q, k, v, q_out, positions, turns, cu_q, kv_len, page_
     equal strides; positions int32 [N] or None; cu_q int32 [B + 1]; kv_len
     int32 [B]; page_table int32 [B, columns]; k_pages, v_pages [pages,
     page_size, Hkv, D]."""
-    _on_current_device(q, k, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages)
-    N, Hkv, D = k.shape
+    dev = _on_current_device(q, k, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages)
+    shape, strides = k.shape, k.stride()
+    N, Hkv, D = shape
     lay = _rope_args(turns, positions, N, layout)
-    _i32_cuda(cu_q, kv_len)
-    cache = _paged_cache(k_pages, v_pages, page_table)
-    B = kv_len.shape[0]
-    if cu_q.shape != (B + 1,) or page_table.shape[0] != B:
-        raise ValueError("cu_q is [B + 1] and page_table has B rows")
-    if k.shape != v.shape or k.stride() != v.stride() or k.stride(2) != 1:
+    cache, B, heads, dim = _paged_cache(k_pages, v_pages, page_table, cu_q, kv_len)
+    dtype = k.dtype
+    if v.shape != shape or v.stride() != strides or strides[2] != 1:
         raise ValueError("k and v are [N, Hkv, D] with equal strides and contiguous last axes")
-    if k_pages.shape[2:] != k.shape[1:] or not (k.dtype == v.dtype == k_pages.dtype == v_pages.dtype):
+    if heads != Hkv or dim != D or dtype != v.dtype or dtype != k_pages.dtype:
         raise ValueError("pages and new rows share heads, head dimension and dtype")
-    Hq = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
+    Hq = qt = qh = 0
     if q is not None:
-        Hq = q.shape[1]
-        if q.shape != (N, Hq, D) or q_out.shape != q.shape or q.stride(2) != 1 or not q_out.is_contiguous() or \
-                q.dtype != k.dtype or q_out.dtype != k.dtype:
+        qs = q.shape
+        Hq = qs[1]
+        qt, qh, qd = q.stride()
+        if qs[0] != N or qs[2] != D or q_out.shape != qs or qd != 1 or not q_out.is_contiguous() or \
+                q.dtype != dtype or q_out.dtype != dtype:
             raise ValueError("q and q_out are [N, Hq, D] of the pages' dtype; q_out contiguous")
     _check(load().sd_rotary_append_paged(
-        _p(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1), k.data_ptr(), v.data_ptr(),
-        k.stride(0), k.stride(1), _p(q_out), _p(positions), turns.data_ptr(), float(magnitude), 2 * turns.shape[0],
-        lay, cu_q.data_ptr(), kv_len.data_ptr(), cache, N, B, Hq, Hkv, D, _dt(k), _stream(stream)))
+        _p(q), qt, qh, k.data_ptr(), v.data_ptr(), strides[0], strides[1], _p(q_out), _p(positions),
+        turns.data_ptr(), magnitude, 2 * turns.numel(), lay, cu_q.data_ptr(), kv_len.data_ptr(), cache, N, B, Hq, Hkv,
+        D, _dt(k), _stream_on(stream, dev)))
 
 
 def sd_paged_attention_workspace_size(N, B, max_q, Hq, Hkv, D, max_kv, dtype=SD_BF16) -> int:
@@ -546,39 +569,39 @@ def sd_paged_attention(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q, max
     """q [N, Hq, D] (D contiguous); k_pages, v_pages [pages, page_size, Hkv, D];
     page_table int32 [B, columns]; cu_q int32 [B + 1]; kv_len int32 [B]; out
     [N, Hq, D] contiguous, of q's dtype."""
-    _on_current_device(q, k_pages, v_pages, page_table, cu_q, kv_len, out, ws)
-    N, Hq, D = q.shape
-    _i32_cuda(cu_q, kv_len)
-    cache = _paged_cache(k_pages, v_pages, page_table)
-    B = kv_len.shape[0]
-    if cu_q.shape != (B + 1,) or page_table.shape[0] != B:
-        raise ValueError("cu_q is [B + 1] and page_table has B rows")
-    if out.shape != q.shape or not out.is_contiguous() or q.stride(2) != 1 or k_pages.shape[3] != D or \
-            not (q.dtype == out.dtype == k_pages.dtype == v_pages.dtype):
+    dev = _on_current_device(q, k_pages, v_pages, page_table, cu_q, kv_len, out, ws)
+    shape = q.shape
+    N, Hq, D = shape
+    qt, qh, qd = q.stride()
+    cache, B, Hkv, dim = _paged_cache(k_pages, v_pages, page_table, cu_q, kv_len)
+    dtype = q.dtype
+    if out.shape != shape or not out.is_contiguous() or qd != 1 or dim != D or dtype != out.dtype or \
+            dtype != k_pages.dtype:
         raise ValueError("q, out and pages share D and dtype; out is contiguous [N, Hq, D]")
-    _check(load().sd_paged_attention(q.data_ptr(), q.stride(0), q.stride(1), cache, cu_q.data_ptr(),
-                                     kv_len.data_ptr(), int(max_q), int(max_kv), out.data_ptr(), N, B, Hq,
-                                     k_pages.shape[2], D, _dt(q), float(scale), 1 if causal else 0, ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), _stream(stream)))
+    _check(load().sd_paged_attention(q.data_ptr(), qt, qh, cache, cu_q.data_ptr(), kv_len.data_ptr(), max_q, max_kv,
+                                     out.data_ptr(), N, B, Hq, Hkv, D, _dt(q), scale, 1 if causal else 0,
+                                     ws.data_ptr(), ws.nbytes, _stream_on(stream, dev)))
 
 
 def sd_prompt_attention(q, k, v, cu_seqlens, max_len, out, scale, ws, causal=True, stream=None):
     """q [N, Hq, D]; k, v [N, Hkv, D] with equal strides; cu_seqlens int32
     [B + 1]; out [N, Hq, D] contiguous, of q's dtype; ws of
     sd_paged_attention_workspace_size(N, B, max_len, Hq, Hkv, D, max_len)."""
-    _on_current_device(q, k, v, cu_seqlens, out, ws)
-    N, Hq, D = q.shape
+    dev = _on_current_device(q, k, v, cu_seqlens, out, ws)
+    shape, ks, strides = q.shape, k.shape, k.stride()
+    N, Hq, D = shape
+    qt, qh, qd = q.stride()
     _i32_cuda(cu_seqlens)
-    if k.dim() != 3 or k.shape != v.shape or k.stride() != v.stride() or k.shape[0] != N or k.shape[2] != D:
-        raise ValueError("k and v are [N, Hkv, D] of equal shape and strides")
-    if out.shape != q.shape or not out.is_contiguous() or q.stride(2) != 1 or k.stride(2) != 1 or \
-            not (q.dtype == out.dtype == k.dtype == v.dtype):
+    if len(ks) != 3 or ks != v.shape or strides != v.stride() or ks[0] != N or ks[2] != D or strides[2] != 1:
+        raise ValueError("k and v are [N, Hkv, D] of equal shape and strides, their last axis contiguous")
+    dtype = q.dtype
+    if out.shape != shape or not out.is_contiguous() or qd != 1 or \
+            not (dtype == out.dtype == k.dtype == v.dtype):
         raise ValueError("q, k, v, out share dtype and contiguous last axes; out is contiguous [N, Hq, D]")
-    _check(load().sd_prompt_attention(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), v.data_ptr(),
-                                      k.stride(0), k.stride(1), cu_seqlens.data_ptr(), int(max_len), out.data_ptr(),
-                                      N, cu_seqlens.shape[0] - 1, Hq, k.shape[1], D, _dt(q), float(scale),
-                                      1 if causal else 0, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                      _stream(stream)))
+    _check(load().sd_prompt_attention(q.data_ptr(), qt, qh, k.data_ptr(), v.data_ptr(), strides[0], strides[1],
+                                      cu_seqlens.data_ptr(), max_len, out.data_ptr(), N, cu_seqlens.numel() - 1, Hq,
+                                      ks[1], D, _dt(q), scale, 1 if causal else 0, ws.data_ptr(), ws.nbytes,
+                                      _stream_on(stream, dev)))
 
 
 def sd_set_projector_path(path: int) -> int:
