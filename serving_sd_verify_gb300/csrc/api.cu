@@ -945,7 +945,7 @@ double varlen_line(const VarlenParams &p) {
 
 // at most `cap` CTAs, and no more than that line has shares
 int varlen_grid(const VarlenParams &p, int cap) {
-    return (int)std::max(1.0, std::min((double)cap, varlen_line(p) / kVarlenMinShare + 1.0));
+    return (int)std::max(1.0, std::min((double)std::min(cap, kVarlenMaxGrid), varlen_line(p) / kVarlenMinShare + 1.0));
 }
 
 struct VarlenLayout {
@@ -1003,7 +1003,7 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     while (ldexp(varlen_line(p), -p.line_shift) > 2.1e9) ++p.line_shift;
     if (p.line_shift > kVarlenMaxShift)
         return fail(SD_ERR_UNSUPPORTED, "tokens times heads times keys exceed one call");
-    p.min_share = std::max(kVarlenMinShare >> p.line_shift, ((kVarlenMinShare - 8) >> p.line_shift) + 2);
+    p.min_share = std::max(1, kVarlenMinShare >> p.line_shift);
     const int cap = varlen_max_grid(path, p);
     if (cap < 1) return fail(SD_ERR_CUDA, "the attention kernel's occupancy is unavailable");
     int grid = varlen_grid(p, cap);

@@ -217,8 +217,7 @@ attn_varlen_generic_kernel(const VarlenParams p) {
         }
     }
     if (tid < 32) {
-        const VlEnds e = vl_ends(p, pl, cta);
-        if (tid == 0) ends = e;
+        vl_ends(p, pl, cta, &ends);
     }
     __threadfence();
     __syncthreads();

@@ -58,7 +58,7 @@ template <int D> struct Lay {
     static constexpr int kBars = 2 * kMaxSlots + 2 + 2 + 4 + 2 + 2;
     static constexpr int kOffMl = kOffBar + 8 * kBars + 8; // [2][128] max and sum of stream 1
     static constexpr int kOffMisc = kOffMl + 2 * 128 * 4;
-    static constexpr int kSmem = kOffMisc + 256 + 1024;    // + alignment slack
+    static constexpr int kSmem = kOffMisc + 512 + 1024;    // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -70,7 +70,7 @@ struct Misc {
     VlPlan plan;
     VlEnds ends;
 };
-static_assert(sizeof(Misc) <= 256, "the misc area");
+static_assert(sizeof(Misc) <= 512, "the misc area");
 
 struct RingPos {        // slot and phase of the next tile in a ring
     int slot = 0;
@@ -245,17 +245,22 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 load_kv_4d(dst, map, bar, policy, u.row0 - u.tok0 + t * 128, u.g);
                             }
                         } else {
+                            // V comes with both 64-column blocks of a page in one copy (a copy costs about
+                            // 40 clocks besides the 4 of each 128-byte row), and K where that leaves its
+                            // rows evenly spaced: pages of 8, or one 64-column block
                             const int boxes = min(per_half, (u.kv - t * 128 + box - 1) / box);
                             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * L::kHalves));
                             __syncwarp();
+                            const bool both = is_v || box == 8;
                             const int i = lane % per_half, h = lane / per_half;
-                            if (i < boxes && h < L::kHalves) {
+                            if (i < boxes && h < (both ? 1 : L::kHalves)) {
                                 const int key = t * 128 + i * box;
                                 if (pg < 0 || pg >= p.n_pages) {      // read as zeros: the copy's fill
                                     set_fault(p.fault, FAULT_BAD_PAGE);
                                     pg = p.n_pages;
                                 }
-                                load_kv_5d(dst + h * (128 * 128) + i * box * 128, map, bar, policy,
+                                load_kv_5d(dst + (both ? i * box * 128 * L::kHalves : h * (128 * 128) + i * box * 128),
+                                           map, bar, policy,
                                            p.page_log2 >= 0 ? key & (p.page_size - 1) : key % p.page_size, h, u.g, pg);
                             }
                         }
@@ -337,15 +342,22 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         tc_fence_after();
                     };
                     // descriptors by their first tile's, moved on by whole 16-byte units
-                    const uint64_t qd0 = sw128_desc(sQ, 16, 1024), kd0 = sw128_desc(sRing, 16, 1024),
-                                   vd0 = sw128_desc(sRing, 128 * 128, 1024);
+                    // K: its 8-row groups 1024 bytes apart, the 64-column blocks one after the other; from
+                    // pages of 8 slots the blocks alternate every group.  V: 64-column blocks alternate
+                    // every `box` rows (128 where K and V are not paged).
+                    const uint32_t eight = box == 8 ? L::kHalves : 1;
+                    const uint32_t khalf = (box == 8 ? 1024 : 128 * 128) / 16;
+                    const uint64_t qd0 = sw128_desc(sQ, 16, 1024), kd0 = sw128_desc(sRing, 16, 1024 * eight),
+                                   vd0 = sw128_desc(sRing, (uint32_t)box * 128, 1024 * eight);
+                    const int in_box = box - 1;
                     auto issue_s = [&](int i, int qt, int slot) {
                         const uint64_t qd = qd0 + (uint64_t)(qt * (L::kTile / 16)),
                                        kd = kd0 + (uint64_t)(slot * (L::kTile / 16));
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2;
-                            if (el) umma_ss(tmem + 128u * i, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
+                            const uint64_t off = (kk & 3) * 2;
+                            if (el) umma_ss(tmem + 128u * i, qd + off + (kk >> 2) * (128 * 128 / 16),
+                                            kd + off + (kk >> 2) * khalf, idS, kk > 0 ? 1u : 0u);
                         }
                         if (el) umma_commit(sfull_bar(i));
                     };
@@ -358,8 +370,11 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             tc_fence_after();
 #pragma unroll
                             for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk)
-                                if (el) umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + kk * (16 * 128 / 16), idO,
-                                        (!first || kk > 0) ? 1u : 0u);
+                            {
+                                const int r0 = 16 * kk, row = (r0 & ~in_box) * L::kHalves + (r0 & in_box);   // in 128 bytes
+                                if (el) umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
+                                                vd + (uint64_t)(row * (128 / 16)), idO, (!first || kk > 0) ? 1u : 0u);
+                            }
                         }
                         pphase[i] ^= 1u;
                     };
@@ -450,8 +465,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 }
                 __syncwarp();
             } else if (warp == 3) {
-                const VlEnds e = vl_ends(p, pl, cta);
-                if (lane == 0) misc->ends = e;
+                vl_ends(p, pl, cta, &misc->ends);
                 asm volatile("bar.arrive 14, 288;" ::: "memory");
             }
         } else {
@@ -466,6 +480,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             VlWalk walk(pl);
             VlUnit u;
             uint32_t sphase = 0, ophase = 0, ophase1 = 0;
+            bool have_ends = false;
             unsigned ring = 0;                         // tiles that went through the ring before this unit
             bool ok = true;
             while (walk.next(p, pl, u)) {
@@ -498,7 +513,9 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         const int live = min(4, ((pair ? tpt : min(u.ntok, tpt)) * G + 31) / 32);
                         for (int i = r; i < (128 - v0) * 8 * L::kHalves; i += 32 * live) {
                             const int row = v0 + i / (8 * L::kHalves), ch = i % (8 * L::kHalves);
-                            *reinterpret_cast<uint4 *>(vt + (ch >> 3) * (128 * 128) + sw128_off(row, ch & 7)) =
+                            const int in = row & (box - 1);
+                            *reinterpret_cast<uint4 *>(vt + ((row - in) * L::kHalves + (ch >> 3) * box) * 128 +
+                                                       sw128_off(in, ch & 7)) =
                                 make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async_smem();
@@ -594,8 +611,30 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 }
                 // ---- end of the unit: this CTA's rows, normalised, or its part of them
                 const bool whole = u.t0 == 0 && u.t1 == u.tiles;
-                const long slot = u.t0 == 0 ? 2L * cta + 1 : 2L * cta;
                 const bool had0 = n > 0, had1 = pair ? n > 0 : n > 1;     // streams that hold anything
+                // A unit of two CTAs: the one that opens it has it last and keeps its part in tensor
+                // memory; the other had it first and left its part in the workspace long ago.  So one
+                // part is written and read instead of two (a batch of prompts shares about two units
+                // per CTA: 256 KB each way).  Units of more CTAs are joined at the end, by all of them.
+                const VlShared *sh = nullptr;
+                if (!whole) {
+                    if (!have_ends) asm volatile("bar.sync 14, 288;" ::: "memory");      // warp 3's answer
+                    have_ends = true;
+                    sh = misc->ends.u + (u.t0 > 0 ? 0 : misc->ends.n - 1);
+                }
+                const bool two = sh && sh->n == 2, keeper = two && u.t0 == 0;
+                const long slot = keeper ? 2L * sh->last : u.t0 == 0 ? 2L * cta + 1 : 2L * cta;
+                unsigned ticket = 0;
+                if (keeper) {
+                    if (tid == 128) {
+                        const bool got = vl_wait(p.ctr + sh->first, 1u + p.wt.extra, p.wt.limit_ns);
+                        if (!got) set_fault(p.fault, FAULT_WAIT_TIMEOUT);
+                        misc->join_flag = got;
+                        ticket = atomicAdd(p.ctr + sh->first, 1u);
+                    }
+                    named_sync(1, 256);
+                    if (tid == 128 && ticket == 1u) atomicExch(p.ctr + sh->first, 0u);
+                }
                 ring += 2 * n;
                 float a0 = 1.f, a1 = 0.f;
                 if (!pair) {
@@ -626,9 +665,22 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 if (had1) ophase1 ^= 1u;
                 tc_fence_after();
                 if ((pair || w == 0) && warp_live) {
-                    const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                    const long prow = 128 * (pair ? w : 0) + r;
                     const long orow = (long)(u.row0 + tl) * p.Hq + u.g * G + (r - tr * G);
                     const bool dead = n <= 0;
+                    float a2 = 0.f;                    // weight of the other CTA's part
+                    if (keeper && row_ok) {
+                        const float2 other = __ldcg(p.ml_part + slot * kVarlenTcRows + prow);
+                        const float m = fmaxf(m_used, other.x), ref = m == -INFINITY ? 0.f : m;
+                        const float f = ex2(m_used - ref);
+                        a0 *= f;
+                        a1 *= f;
+                        a2 = ex2(other.x - ref);
+                        l = l * f + a2 * other.y;
+                        if (!misc->join_flag) l = 0.f;
+                    }
+                    const bool write = whole || keeper;
+                    const float inv = write ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
@@ -648,7 +700,21 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), a1 * inv, f[e]);
                         }
                         if (row_ok && ok) {
-                            if (whole) {
+                            float4 *part = reinterpret_cast<float4 *>(p.o_part) +
+                                           (slot * (D / 4) + 8 * c) * kVarlenTcRows + prow;
+                            if (keeper) {
+                                float4 v[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) v[e] = __ldcg(part + e * kVarlenTcRows);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    f[4 * e] = fmaf(v[e].x, a2 * inv, f[4 * e]);
+                                    f[4 * e + 1] = fmaf(v[e].y, a2 * inv, f[4 * e + 1]);
+                                    f[4 * e + 2] = fmaf(v[e].z, a2 * inv, f[4 * e + 2]);
+                                    f[4 * e + 3] = fmaf(v[e].w, a2 * inv, f[4 * e + 3]);
+                                }
+                            }
+                            if (write) {
                                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + orow * D + 32 * c;
 #pragma unroll
                                 for (int e = 0; e < 32; e += 8) {
@@ -662,17 +728,27 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                     *reinterpret_cast<uint4 *>(dst + e) = v;
                                 }
                             } else {
-                                float4 *dst = reinterpret_cast<float4 *>(p.o_part) +
-                                              (slot * (D / 4) + 8 * c) * kVarlenTcRows + 128 * (pair ? w : 0) + r;
 #pragma unroll
                                 for (int e = 0; e < 32; e += 4)
-                                    __stcg(dst + (e / 4) * kVarlenTcRows, make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
+                                    __stcg(part + (e / 4) * kVarlenTcRows, make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
                             }
                         }
                     }
-                    if (row_ok && !whole)
-                        __stcg(p.ml_part + slot * kVarlenTcRows + 128 * (pair ? w : 0) + r,
+                    if (row_ok && !write)
+                        __stcg(p.ml_part + slot * kVarlenTcRows + prow,
                                make_float2(ok ? m_used : -INFINITY, ok ? l : 0.f));
+                }
+                if (two && !keeper) {
+                    // announced at once, for the CTA that keeps the other part; should that one have
+                    // given up waiting, the counter goes back to zero here
+                    named_sync(1, 256);
+                    if (tid == 128) {
+                        __threadfence();
+                        unsigned old;
+                        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p.ctr + sh->first)
+                                     : "memory");
+                        if (old == 1u) atomicExch(p.ctr + sh->first, 0u);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -687,10 +763,12 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 if (!pair) named_sync(2, 256);     // stream 1's max and sum have been read
             }
             // the softmax warps (they hold the registers) join the shared units
-            asm volatile("bar.sync 14, 288;" ::: "memory");     // warp 3's answer; every part of this CTA is written
+            if (!have_ends) asm volatile("bar.sync 14, 288;" ::: "memory");
             const VlEnds &ends = misc->ends;
-            if (tid - 128 < ends.n) vl_arrive(p, ends.u[tid - 128]);
-            for (int i = 0; i < ends.n; ++i) vl_join(p, ends.u[i], tpt, 128, &misc->join_flag, tid - 128, 256, 1);
+            named_sync(1, 256);                        // every part of this CTA is written
+            if (tid - 128 < ends.n && ends.u[tid - 128].n > 2) vl_arrive(p, ends.u[tid - 128]);
+            for (int i = 0; i < ends.n; ++i)
+                if (ends.u[i].n > 2) vl_join(p, ends.u[i], tpt, 128, &misc->join_flag, tid - 128, 256, 1);
         }
     }
 
@@ -781,7 +859,8 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
             const cuuint64_t dims[5] = {64, (cuuint64_t)p.page_size, (cuuint64_t)(D / 64), (cuuint64_t)p.Hkv,
                                         (cuuint64_t)p.n_pages};
             const cuuint64_t strides[4] = {(cuuint64_t)p.kv.s * 2, 128, (cuuint64_t)p.kv.h * 2, (cuuint64_t)p.kv.b * 2};
-            const cuuint32_t box[5] = {64, (cuuint32_t)box_rows, 1, 1, 1};
+            const cuuint32_t both = i == 1 || box_rows == 8 ? D / 64 : 1;
+            const cuuint32_t box[5] = {64, (cuuint32_t)box_rows, both, 1, 1};
             if (!encode_vl(m, t, 5, dims, strides, box)) return cudaErrorInvalidValue;
         } else {        // (d % 64, token, d / 64, kv head): one copy per tile
             const cuuint64_t dims[4] = {64, (cuuint64_t)p.N, (cuuint64_t)(D / 64), (cuuint64_t)p.Hkv};

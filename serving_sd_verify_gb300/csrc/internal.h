@@ -118,12 +118,13 @@ constexpr int kVarlenTcRows = 256;      // rows of a unit, tensor cores: two til
 constexpr int kVarlenTcTileLog2 = 7;    // its keys per tile: 128
 constexpr int kVarlenGenTileLog2 = 6;   // keys per tile of the CUDA-core kernel: 64
 constexpr int kVarlenGenPerSm = 4;      // and its CTAs per SM at most
-constexpr int kVarlenFixed = 768;       // a unit's fixed cost, in keys (its queries, filling the pipeline, its epilogue)
-constexpr int kVarlenGroup = 2;         // a unit is cut at multiples of this many tiles
-// a share is longer than a group of any unit, and not longer than a unit of one key
-constexpr int kVarlenMinShare = 2 * 128 + kVarlenFixed / 2 + 8;
-constexpr int kVarlenMaxShift = 8;      // of the work line: a unit keeps a length of 3 at least
+constexpr int kVarlenFixed = 448;       // a unit's fixed cost, in keys (its queries, filling the pipeline, its epilogue)
+constexpr int kVarlenMinShare = 440;    // smallest share of a CTA, in the same keys: not longer than a unit of one key,
+                                        // so that the shortest units get a CTA each
+constexpr int kVarlenGroup = 4;         // units of up to so many tiles are not cut, and at that share others at its multiples
+constexpr int kVarlenMaxShift = 8;      // of the work line: a unit keeps a length of 1 at least
 constexpr int kVarlenMaxKv = 1 << 26;   // keys of a sequence
+constexpr int kVarlenMaxGrid = 1024;
 bool varlen_tc_supported(const VarlenParams &p);
 int varlen_generic_rows(const VarlenParams &p);        // rows per unit of the CUDA-core kernel
 int varlen_max_grid(int path, const VarlenParams &p);  // its CTAs that are resident at once (0: none)

@@ -82,10 +82,13 @@ struct VlUnit {
     int t0, t1, tiles;  // this CTA's tiles of all
 };
 
-// a unit shared by several CTAs, of which this one is `s` of `n`, the first `c0`
+// A unit shared by `n` CTAs: bit k of the mask is set where CTA base + k has a
+// part (a share can fall between two cuts and have none).  The first opens the
+// unit, this CTA's is the s-th.
 struct VlShared {
-    int c0, n, s, slot;
+    int base, first, last, n, s;
     int g, row0, ntok;
+    unsigned mask[(kVarlenMaxGrid + 31) / 32];
 };
 
 struct VlPlan {
@@ -93,6 +96,7 @@ struct VlPlan {
     VlPos begin, end;
     VlSeq s;            // the sequence of `begin`
     int share, total;   // CTA c takes [c share, (c + 1) share) of the line
+    int group;          // and units are cut at multiples of this many tiles
 };
 
 __device__ __forceinline__ int vl_tiles(const VarlenParams &p, int keys) {
@@ -100,22 +104,20 @@ __device__ __forceinline__ int vl_tiles(const VarlenParams &p, int keys) {
 }
 
 // cut of a unit of length len and `tiles` tiles at `off` (0 <= off <= len): the
-// tiles before it, in whole groups of kVarlenGroup.  Non-decreasing in off, and
-// two boundaries a share apart never give the same cut inside a unit of several
-// groups (a share is longer than any group; fp32 holds the quotient to 2^-5 of
-// a group up to kVarlenMaxKv keys).
-__device__ __forceinline__ int vl_cut(int off, int len, int tiles, bool splittable) {
-    const int groups = (tiles + kVarlenGroup - 1) / kVarlenGroup;
-    if (!splittable || groups < 2) return 2 * off >= len ? tiles : 0;
+// tiles before it, in whole groups (a unit of kVarlenGroup tiles or fewer is
+// not cut); non-decreasing in off
+__device__ __forceinline__ int vl_cut(int off, int len, int tiles, bool splittable, int group) {
+    const int groups = (tiles + group - 1) / group;
+    if (!splittable || tiles <= kVarlenGroup) return 2 * off >= len ? tiles : 0;
     const int g = (int)((float)off * ((float)groups / (float)len) + 0.5f);
-    return min(tiles, g * kVarlenGroup);
+    return min(tiles, g * group);
 }
 __device__ __forceinline__ bool vl_splittable(const VarlenParams &p, const VlSeq &s) {
     return !p.causal || s.off >= 0;
 }
 
 // the place of the boundary `o` past the beginning of sequence b's part of the line
-__device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, int o) {
+__device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, int o, int group) {
     const int head = vl_before(p, s, s.nr);
     int g = min((int)((float)o / (float)head), p.Hkv - 1);     // at most 4096 heads: one off at most
     o -= g * head;
@@ -129,7 +131,7 @@ __device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const V
     }
     const int u0 = vl_before(p, s, r), len = vl_before(p, s, r + 1) - u0;
     const int tiles = vl_tiles(p, vl_keys(p, s, r));
-    int t = vl_cut(o - u0, len, tiles, vl_splittable(p, s));
+    int t = vl_cut(o - u0, len, tiles, vl_splittable(p, s), group);
     if (t >= tiles && (tiles > 0 || 2 * (o - u0) >= len)) {    // at its end: the next unit's beginning
         t = 0;
         if (++r == s.nr) {
@@ -169,6 +171,8 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
     }
     // the smallest share the grid covers the line with (rounded up past fp32's error)
     pl.share = max(p.min_share, (int)((float)pl.total * p.inv_grid * (1.0f + 0x1p-20f)) + 1);
+    // joining parts costs about what four tiles cost: a part this short is not worth it
+    pl.group = pl.share > p.min_share ? 1 : kVarlenGroup;
     const int x0 = c * pl.share, x1 = x0 + pl.share;
     pl.idle = x0 >= pl.total;
     if (pl.idle) return pl;
@@ -209,7 +213,7 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
         base = __shfl_sync(0xffffffffu, e, 31);
     }
     VlPos at = {p.B, 0, 0, 0};
-    if (lane < 2 && found < p.B) at = vl_locate(p, found, pl.s, o);
+    if (lane < 2 && found < p.B) at = vl_locate(p, found, pl.s, o, pl.group);
     if (at.b != found) pl.s.nr = 0;   // the next sequence's beginning: not yet read
     pl.begin = at;      // lane 0's; lane 1 holds the end
     pl.end = at;
@@ -225,6 +229,7 @@ __device__ __forceinline__ void vl_plan_store(const VlPlan &q, VlPlan *to) {
         to->s = q.s;
         to->share = q.share;
         to->total = q.total;
+        to->group = q.group;
     } else if (lane == 1) {
         to->end = q.end;
     }
@@ -292,39 +297,51 @@ struct VlEnds {
     int n;              // 0 to 2
     VlShared u[2];
 };
-__device__ VlEnds vl_ends(const VarlenParams &p, const VlPlan &pl, int c) {
-    VlEnds e = {};
+__device__ void vl_ends(const VarlenParams &p, const VlPlan &pl, int c, VlEnds *to) {
+    const int lane = threadIdx.x & 31;
     const bool same = pl.begin.b == pl.end.b && pl.begin.g == pl.end.g && pl.begin.r == pl.end.r;
+    int found = 0;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         const VlPos at = i == 0 ? pl.begin : pl.end;
         if (at.t == 0 || (i == 1 && same && pl.begin.t > 0)) continue;
+        if (same && pl.begin.t == pl.end.t) continue;       // between two boundaries cut alike: no part
         const VlSeq s = vl_seq(p, at.b, false);
         const int u0 = vl_before(p, s, at.r), len = vl_before(p, s, at.r + 1) - u0;
         const int X = vl_seq_start(p, at.b) + at.g * vl_before(p, s, s.nr) + u0;
         const int tiles = vl_tiles(p, vl_keys(p, s, at.r));
-        // the CTAs whose shares meet the unit, but for those whose part is cut to nothing:
-        // c - 1 down to the first boundary that leaves tiles before it, and up to the last
-        // that leaves tiles behind it
-        auto cuts = [&](int k) {       // whether boundary k lies inside the unit
-            const int x = k * pl.share;
-            if (k < 1 || x <= X || x >= X + len || x >= pl.total) return false;
-            const int t = vl_cut(x - X, len, tiles, vl_splittable(p, s));
-            return t > 0 && t < tiles;
+        auto cut = [&](int k) {       // tiles of the unit before boundary k
+            const long x = (long)k * pl.share;
+            if (x <= X) return 0;
+            if (x >= X + len || x >= pl.total) return tiles;
+            return vl_cut((int)(x - X), len, tiles, vl_splittable(p, s), pl.group);
         };
-        int lo = X / pl.share + 1, hi = (X + len) / pl.share;     // boundaries within the unit
-        while (lo < hi && !cuts(lo)) ++lo;                        // the one that makes it shared is among them
-        while (hi > lo && !cuts(hi)) --hi;
-        VlShared &r = e.u[e.n++];
-        r.c0 = lo - 1;
-        r.n = hi - lo + 2;
-        r.s = c - r.c0;
-        r.slot = i == 0 ? 2 * c : 2 * c + 1;
-        r.g = at.g;
-        r.row0 = s.c0 + at.r * p.tb;
-        r.ntok = min(p.tb, s.q - at.r * p.tb);
+        VlShared *r = to->u + found++;
+        const int k0 = X / pl.share, k1 = min((X + len) / pl.share + 1, k0 + kVarlenMaxGrid);
+        int first = -1, last = -1, n = 0, mine = 0;
+#pragma unroll 1
+        for (int k = k0; k < k1; k += 32) {
+            const unsigned m = __ballot_sync(0xffffffffu, k + lane < k1 && cut(k + lane) < cut(k + lane + 1));
+            if (first < 0 && m) first = k + __ffs((int)m) - 1;
+            if (m) last = k + 31 - __clz((int)m);
+            n += __popc(m);
+            const int below = c - k;
+            mine += below >= 32 ? __popc(m) : below > 0 ? __popc(m & ((1u << below) - 1u)) : 0;
+            if (lane == 0) r->mask[(k - k0) >> 5] = m;
+        }
+        if (lane == 0) {
+            r->base = k0;
+            r->first = first;
+            r->last = last;
+            r->n = n;
+            r->s = mine;
+            r->g = at.g;
+            r->row0 = s.c0 + at.r * p.tb;
+            r->ntok = min(p.tb, s.q - at.r * p.tb);
+        }
     }
-    return e;
+    if (lane == 0) to->n = found;
+    __syncwarp();
 }
 
 // Bounded wait until the counter reaches `target`.
@@ -369,7 +386,7 @@ __device__ __forceinline__ float vl_ex2(float x) {
 __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int trows, int *flag, int tid, int nt,
                         int bar) {
     auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(nt) : "memory"); };
-    unsigned int *ctr = p.ctr + sh.c0;
+    unsigned int *ctr = p.ctr + sh.first;
     unsigned int ticket = 0;
     if (tid == 0) {
         const bool ok = vl_wait(ctr, (unsigned)sh.n + p.wt.extra, p.wt.limit_ns);
@@ -387,11 +404,12 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
         int lanes = 1;
         while (lanes < 32 && 2 * lanes <= sh.n && (ie - ia) * lanes * 2 <= nt) lanes *= 2;
         const int sub = tid & (lanes - 1);
+        const bool holes = sh.last - sh.first + 1 > sh.n;
         const long cstep = p.rows, sstep = (long)(p.D / 4) * p.rows;
         // kJoinItems items of a thread at a time, so that the loads of all are in
         // flight together; the loops run the same number of times in every thread,
         // so that whole warps meet at the shuffles
-        constexpr int kJoinItems = 2;
+        constexpr int kJoinItems = 4;
         const int stride = nt / lanes;
         for (int i0 = ia + tid / lanes; __any_sync(0xffffffffu, i0 < ie); i0 += kJoinItems * stride) {
             float M[kJoinItems], l[kJoinItems], acc[kJoinItems][8];
@@ -410,8 +428,9 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
                 for (int x = 0; x < 8; ++x) acc[q][x] = 0.f;
             }
 #pragma unroll 1
-            for (int e = sub; e < sh.n; e += lanes) {
-                const long slot = e == 0 ? 2L * sh.c0 + 1 : 2L * (sh.c0 + e);
+            for (int k = sh.first + sub; k <= sh.last; k += lanes) {
+                if (holes && !((sh.mask[(k - sh.base) >> 5] >> ((k - sh.base) & 31)) & 1u)) continue;
+                const long slot = k == sh.first ? 2L * k + 1 : 2L * k;
                 float4 va[kJoinItems], vb[kJoinItems];
                 float2 ml[kJoinItems];
 #pragma unroll
@@ -435,6 +454,7 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
             }
 #pragma unroll
             for (int q = 0; q < kJoinItems; ++q) {
+                if (!__any_sync(0xffffffffu, i0 + q * stride < ie)) break;
 #pragma unroll 1
                 for (int o = 1; o < lanes; o <<= 1) {
                     const float M2 = __shfl_xor_sync(0xffffffffu, M[q], o), l2 = __shfl_xor_sync(0xffffffffu, l[q], o);
@@ -467,7 +487,7 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
 // follows every thread's writes of it)
 __device__ __forceinline__ void vl_arrive(const VarlenParams &p, const VlShared &sh) {
     __threadfence();
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.ctr + sh.c0) : "memory");
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.ctr + sh.first) : "memory");
 }
 
 }  // namespace
