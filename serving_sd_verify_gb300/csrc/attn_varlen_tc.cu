@@ -349,7 +349,10 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     const uint32_t khalf = (box == 8 ? 1024 : 128 * 128) / 16;
                     const uint64_t qd0 = sw128_desc(sQ, 16, 1024), kd0 = sw128_desc(sRing, 16, 1024 * eight),
                                    vd0 = sw128_desc(sRing, (uint32_t)box * 128, 1024 * eight);
-                    const int in_box = box - 1;
+                    uint32_t vrow[8];              // where the 16 keys of step kk begin in a V tile, in 16 bytes
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        vrow[kk] = (((16 * kk) & ~(box - 1)) * L::kHalves + ((16 * kk) & (box - 1))) * (128 / 16);
                     auto issue_s = [&](int i, int qt, int slot) {
                         const uint64_t qd = qd0 + (uint64_t)(qt * (L::kTile / 16)),
                                        kd = kd0 + (uint64_t)(slot * (L::kTile / 16));
@@ -370,11 +373,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             tc_fence_after();
 #pragma unroll
                             for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk)
-                            {
-                                const int r0 = 16 * kk, row = (r0 & ~in_box) * L::kHalves + (r0 & in_box);   // in 128 bytes
-                                if (el) umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk,
-                                                vd + (uint64_t)(row * (128 / 16)), idO, (!first || kk > 0) ? 1u : 0u);
-                            }
+                                if (el) umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + vrow[kk], idO,
+                                                (!first || kk > 0) ? 1u : 0u);
                         }
                         pphase[i] ^= 1u;
                     };
@@ -681,7 +681,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     }
                     const bool write = whole || keeper;
                     const float inv = write ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-#pragma unroll
+                    // (a loop, not unrolled: the code that runs once per unit is fetched once)
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         if (!dead) {

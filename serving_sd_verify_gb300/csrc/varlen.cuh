@@ -72,6 +72,8 @@ __device__ __forceinline__ int vl_before(const VarlenParams &p, const VlSeq &s, 
 
 struct VlPos {          // a place on the work line: tile t of unit (b, g, r)
     int b, g, r, t;
+    int x, len, tiles;  // where t > 0: the unit's beginning and length on the line, its tiles
+    int row0, ntok;     // and its first packed row and tokens
 };
 
 struct VlUnit {
@@ -116,8 +118,8 @@ __device__ __forceinline__ bool vl_splittable(const VarlenParams &p, const VlSeq
     return !p.causal || s.off >= 0;
 }
 
-// the place of the boundary `o` past the beginning of sequence b's part of the line
-__device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, int o, int group) {
+// the place of boundary x, `o` past the beginning of sequence b's part of the line
+__device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const VlSeq &s, int x, int o, int group) {
     const int head = vl_before(p, s, s.nr);
     int g = min((int)((float)o / (float)head), p.Hkv - 1);     // at most 4096 heads: one off at most
     o -= g * head;
@@ -132,14 +134,13 @@ __device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const V
     const int u0 = vl_before(p, s, r), len = vl_before(p, s, r + 1) - u0;
     const int tiles = vl_tiles(p, vl_keys(p, s, r));
     int t = vl_cut(o - u0, len, tiles, vl_splittable(p, s), group);
-    if (t >= tiles && (tiles > 0 || 2 * (o - u0) >= len)) {    // at its end: the next unit's beginning
-        t = 0;
-        if (++r == s.nr) {
-            r = 0;
-            if (++g == p.Hkv) { g = 0; ++b; }
-        }
+    const VlPos in = {b, g, r, t, x - (o - u0), len, tiles, s.c0 + r * p.tb, min(p.tb, s.q - r * p.tb)};
+    if (t < tiles || (tiles == 0 && 2 * (o - u0) < len)) return in;
+    if (++r == s.nr) {                                         // at its end: the next unit's beginning
+        r = 0;
+        if (++g == p.Hkv) { g = 0; ++b; }
     }
-    return {b, g, r, t};
+    return {b, g, r, 0};
 }
 
 // The share of CTA `c` (one full warp).  The code runs once per CTA, so it is
@@ -213,7 +214,7 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
         base = __shfl_sync(0xffffffffu, e, 31);
     }
     VlPos at = {p.B, 0, 0, 0};
-    if (lane < 2 && found < p.B) at = vl_locate(p, found, pl.s, o, pl.group);
+    if (lane < 2 && found < p.B) at = vl_locate(p, found, pl.s, x, o, pl.group);
     if (at.b != found) pl.s.nr = 0;   // the next sequence's beginning: not yet read
     pl.begin = at;      // lane 0's; lane 1 holds the end
     pl.end = at;
@@ -281,16 +282,6 @@ __device__ __forceinline__ int vl_limit(const VarlenParams &p, const VlUnit &u, 
     return p.causal ? max(0, min(u.kv, u.off + i + 1)) : u.kv;
 }
 
-// where sequence b begins on the work line (one full warp)
-__device__ int vl_seq_start(const VarlenParams &p, int b_end) {
-    unsigned tot = 0;
-    for (int b = threadIdx.x & 31; b < b_end; b += 32) {
-        const VlSeq s = vl_seq(p, b, false);
-        tot += (unsigned)p.Hkv * (unsigned)vl_before(p, s, s.nr);
-    }
-    return (int)__reduce_add_sync(0xffffffffu, tot);
-}
-
 // the units that CTA c shares with others (one full warp): the one its share
 // begins in the middle of, and the one it opens and leaves unfinished
 struct VlEnds {
@@ -306,18 +297,15 @@ __device__ void vl_ends(const VarlenParams &p, const VlPlan &pl, int c, VlEnds *
         const VlPos at = i == 0 ? pl.begin : pl.end;
         if (at.t == 0 || (i == 1 && same && pl.begin.t > 0)) continue;
         if (same && pl.begin.t == pl.end.t) continue;       // between two boundaries cut alike: no part
-        const VlSeq s = vl_seq(p, at.b, false);
-        const int u0 = vl_before(p, s, at.r), len = vl_before(p, s, at.r + 1) - u0;
-        const int X = vl_seq_start(p, at.b) + at.g * vl_before(p, s, s.nr) + u0;
-        const int tiles = vl_tiles(p, vl_keys(p, s, at.r));
+        // (a unit that is cut is one that can be)
         auto cut = [&](int k) {       // tiles of the unit before boundary k
-            const long x = (long)k * pl.share;
-            if (x <= X) return 0;
-            if (x >= X + len || x >= pl.total) return tiles;
-            return vl_cut((int)(x - X), len, tiles, vl_splittable(p, s), pl.group);
+            const int x = k * pl.share;
+            if (x <= at.x) return 0;
+            if (x >= at.x + at.len || x >= pl.total) return at.tiles;
+            return vl_cut(x - at.x, at.len, at.tiles, true, pl.group);
         };
         VlShared *r = to->u + found++;
-        const int k0 = X / pl.share, k1 = min((X + len) / pl.share + 1, k0 + kVarlenMaxGrid);
+        const int k0 = at.x / pl.share, k1 = min((at.x + at.len) / pl.share + 1, k0 + kVarlenMaxGrid);
         int first = -1, last = -1, n = 0, mine = 0;
 #pragma unroll 1
         for (int k = k0; k < k1; k += 32) {
@@ -336,8 +324,8 @@ __device__ void vl_ends(const VarlenParams &p, const VlPlan &pl, int c, VlEnds *
             r->n = n;
             r->s = mine;
             r->g = at.g;
-            r->row0 = s.c0 + at.r * p.tb;
-            r->ntok = min(p.tb, s.q - at.r * p.tb);
+            r->row0 = at.row0;
+            r->ntok = at.ntok;
         }
     }
     if (lane == 0) to->n = found;
