@@ -388,27 +388,30 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
     if (*flag) {
         // an item: 8 columns of a row; rows fastest, as the slots hold them
         const int G = p.Hq / p.Hkv, R = sh.ntok * G, items = R * (p.D / 8);
-        const int ia = (int)((long)sh.s * items / sh.n), ie = (int)((long)(sh.s + 1) * items / sh.n);
+        const int ia = sh.s * items / sh.n, ie = (sh.s + 1) * items / sh.n;   // at most 1024 * 64 * 16
         int lanes = 1;
         while (lanes < 32 && 2 * lanes <= sh.n && (ie - ia) * lanes * 2 <= nt) lanes *= 2;
         const int sub = tid & (lanes - 1);
         const bool holes = sh.last - sh.first + 1 > sh.n;
         const long cstep = p.rows, sstep = (long)(p.D / 4) * p.rows;
-        // kJoinItems items of a thread at a time, so that the loads of all are in
-        // flight together; the loops run the same number of times in every thread,
-        // so that whole warps meet at the shuffles
-        constexpr int kJoinItems = 4;
+        // kJoinItems items and kJoinParts parts of each at a time, so that their loads
+        // are in flight together; the loops run the same number of times in every
+        // thread, so that whole warps meet at the shuffles
+        constexpr int kJoinItems = 2, kJoinParts = 4;
         const int stride = nt / lanes;
+#pragma unroll 1
         for (int i0 = ia + tid / lanes; __any_sync(0xffffffffu, i0 < ie); i0 += kJoinItems * stride) {
             float M[kJoinItems], l[kJoinItems], acc[kJoinItems][8];
+            int c8[kJoinItems], kr[kJoinItems];
             const float4 *src[kJoinItems];
             const float2 *mls[kJoinItems];
 #pragma unroll
             for (int q = 0; q < kJoinItems; ++q) {
-                const int i = min(i0 + q * stride, items - 1);
-                const int c8 = i / R, k = i - c8 * R;
-                const int row = k < tpt * G ? k : trows + k - tpt * G;
-                src[q] = reinterpret_cast<const float4 *>(p.o_part) + 2 * c8 * cstep + row;
+                const unsigned i = (unsigned)min(i0 + q * stride, items - 1);
+                c8[q] = (int)(i / (unsigned)R);
+                kr[q] = (int)i - c8[q] * R;
+                const int row = kr[q] < tpt * G ? kr[q] : trows + kr[q] - tpt * G;
+                src[q] = reinterpret_cast<const float4 *>(p.o_part) + 2 * c8[q] * cstep + row;
                 mls[q] = p.ml_part + row;
                 M[q] = -INFINITY;
                 l[q] = 0.f;
@@ -416,28 +419,43 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
                 for (int x = 0; x < 8; ++x) acc[q][x] = 0.f;
             }
 #pragma unroll 1
-            for (int k = sh.first + sub; k <= sh.last; k += lanes) {
-                if (holes && !((sh.mask[(k - sh.base) >> 5] >> ((k - sh.base) & 31)) & 1u)) continue;
-                const long slot = k == sh.first ? 2L * k + 1 : 2L * k;
-                float4 va[kJoinItems], vb[kJoinItems];
-                float2 ml[kJoinItems];
+            for (int k0 = sh.first + sub; k0 <= sh.last; k0 += kJoinParts * lanes) {
+                float4 va[kJoinItems][kJoinParts], vb[kJoinItems][kJoinParts];
+                float2 ml[kJoinItems][kJoinParts];
 #pragma unroll
-                for (int q = 0; q < kJoinItems; ++q) {
-                    const bool live = i0 + q * stride < ie;
-                    va[q] = live ? __ldcg(src[q] + slot * sstep) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    vb[q] = live ? __ldcg(src[q] + slot * sstep + cstep) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    ml[q] = live ? __ldcg(mls[q] + slot * p.rows) : make_float2(-INFINITY, 0.f);
+                for (int e = 0; e < kJoinParts; ++e) {
+                    const int k = k0 + e * lanes;
+                    const bool part = k <= sh.last &&
+                                      (!holes || ((sh.mask[(k - sh.base) >> 5] >> ((k - sh.base) & 31)) & 1u));
+                    const long slot = k == sh.first ? 2L * k + 1 : 2L * k;
+#pragma unroll
+                    for (int q = 0; q < kJoinItems; ++q) {
+                        const bool live = part && i0 + q * stride < ie;
+                        va[q][e] = live ? __ldcg(src[q] + slot * sstep) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        vb[q][e] = live ? __ldcg(src[q] + slot * sstep + cstep) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        ml[q][e] = live ? __ldcg(mls[q] + slot * p.rows) : make_float2(-INFINITY, 0.f);
+                    }
                 }
 #pragma unroll
                 for (int q = 0; q < kJoinItems; ++q) {
-                    const float m = fmaxf(M[q], ml[q].x);
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    const float f = vl_ex2(M[q] - ref), w = vl_ex2(ml[q].x - ref);   // 0 for what saw nothing
-                    M[q] = m;
-                    l[q] = l[q] * f + w * ml[q].y;
-                    const float v[8] = {va[q].x, va[q].y, va[q].z, va[q].w, vb[q].x, vb[q].y, vb[q].z, vb[q].w};
+                    float m = M[q];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) acc[q][x] = acc[q][x] * f + w * v[x];
+                    for (int e = 0; e < kJoinParts; ++e) m = fmaxf(m, ml[q][e].x);
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const float f = vl_ex2(M[q] - ref);                // 0 for what saw nothing
+                    M[q] = m;
+                    l[q] *= f;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) acc[q][x] *= f;
+#pragma unroll
+                    for (int e = 0; e < kJoinParts; ++e) {
+                        const float w = vl_ex2(ml[q][e].x - ref);
+                        const float v[8] = {va[q][e].x, va[q][e].y, va[q][e].z, va[q][e].w,
+                                            vb[q][e].x, vb[q][e].y, vb[q][e].z, vb[q][e].w};
+                        l[q] = fmaf(w, ml[q][e].y, l[q]);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) acc[q][x] = fmaf(w, v[x], acc[q][x]);
+                    }
                 }
             }
 #pragma unroll
@@ -454,14 +472,13 @@ __device__ void vl_join(const VarlenParams &p, const VlShared &sh, int tpt, int 
                         acc[q][x] = f1 * acc[q][x] + f2 * __shfl_xor_sync(0xffffffffu, acc[q][x], o);
                     M[q] = m;
                 }
-                const int i = i0 + q * stride;
-                if (i < ie && sub == 0) {
+                if (i0 + q * stride < ie && sub == 0) {
                     const float inv = l[q] > 0.f ? 1.f / l[q] : 0.f;
-                    const int c8 = i / R, k = i - c8 * R, tok = k / G;
-                    const long orow = (long)(sh.row0 + tok) * p.Hq + sh.g * G + (k - tok * G);
-                    vl_store4(p, orow, 2 * c8,
+                    const int tok = (int)((unsigned)kr[q] / (unsigned)G);
+                    const long orow = (long)(sh.row0 + tok) * p.Hq + sh.g * G + (kr[q] - tok * G);
+                    vl_store4(p, orow, 2 * c8[q],
                               make_float4(acc[q][0] * inv, acc[q][1] * inv, acc[q][2] * inv, acc[q][3] * inv));
-                    vl_store4(p, orow, 2 * c8 + 1,
+                    vl_store4(p, orow, 2 * c8[q] + 1,
                               make_float4(acc[q][4] * inv, acc[q][5] * inv, acc[q][6] * inv, acc[q][7] * inv));
                 }
             }
