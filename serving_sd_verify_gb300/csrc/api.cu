@@ -933,6 +933,9 @@ void varlen_units(VarlenParams &p, int path) {
     p.rows = path >= 2 ? kVarlenTcRows : varlen_generic_rows(p);
     p.tb = path >= 2 ? 2 * (128 / G) : p.rows / G;
     if (p.tb < 1) p.tb = 1;      // 64 rows, a group of at most 64
+    p.fixed = path >= 2 ? kVarlenTcFixed : kVarlenGenFixed;
+    p.group = path >= 2 ? kVarlenTcGroup : kVarlenGenGroup;
+    p.min_share = path >= 2 ? kVarlenTcMinShare : kVarlenGenMinShare;
     p.tile_log2 = path >= 2 ? kVarlenTcTileLog2 : kVarlenGenTileLog2;
 }
 
@@ -940,12 +943,12 @@ void varlen_units(VarlenParams &p, int path) {
 double varlen_line(const VarlenParams &p) {
     const double units = (double)p.Hkv * std::min((double)p.N / p.tb + p.B,
                                                   (double)p.B * ((p.max_q + p.tb - 1) / p.tb));
-    return units * ((double)std::max(p.max_kv, p.max_q) + kVarlenFixed);
+    return units * ((double)std::max(p.max_kv, p.max_q) + p.fixed);
 }
 
 // at most `cap` CTAs, and no more than that line has shares
 int varlen_grid(const VarlenParams &p, int cap) {
-    return (int)std::max(1.0, std::min((double)std::min(cap, kVarlenMaxGrid), varlen_line(p) / kVarlenMinShare + 1.0));
+    return (int)std::max(1.0, std::min((double)std::min(cap, kVarlenMaxGrid), varlen_line(p) / p.min_share + 1.0));
 }
 
 struct VarlenLayout {
@@ -1001,9 +1004,9 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     varlen_units(p, path);
     p.line_shift = 0;
     while (ldexp(varlen_line(p), -p.line_shift) > 2.1e9) ++p.line_shift;
-    if (p.line_shift > kVarlenMaxShift)
+    if (p.fixed >> p.line_shift < 1)      // every unit keeps a length
         return fail(SD_ERR_UNSUPPORTED, "tokens times heads times keys exceed one call");
-    p.min_share = std::max(1, kVarlenMinShare >> p.line_shift);
+    p.min_share = std::max(1, p.min_share >> p.line_shift);
     const int cap = varlen_max_grid(path, p);
     if (cap < 1) return fail(SD_ERR_CUDA, "the attention kernel's occupancy is unavailable");
     int grid = varlen_grid(p, cap);
@@ -1016,6 +1019,7 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     p.o_part = reinterpret_cast<float *>(w + l.o);
     p.ml_part = reinterpret_cast<float2 *>(w + l.ml);
     p.wt = wait_test();
+    p.out32 = aligned_to(p.out, 32) && p.D * es % 32 == 0;
     for (;;) {
         p.inv_grid = 1.0f / (float)grid;
         const cudaError_t e = path == 2 ? launch_varlen_tc(p, grid, st) : launch_varlen_generic(p, grid, st);
@@ -1154,7 +1158,8 @@ size_t sd_paged_attention_workspace_size(int N, int B, int max_q, int Hq, int Hk
     // page size and a forced path): tensor cores one CTA per SM and 256 rows,
     // CUDA cores kVarlenGenPerSm CTAs per SM of 64 rows
     p.tb = 1;
-    if (ldexp(varlen_line(p), -kVarlenMaxShift - 7) > 2.1e9) return 0;    // beyond any call, whatever its units
+    p.fixed = kVarlenTcFixed;
+    p.min_share = kVarlenGenMinShare;
     const int sms = device_sm_count();
     const int g2 = varlen_grid(p, sms), g1 = varlen_grid(p, kVarlenGenPerSm * sms);
     return std::max(varlen_layout(g2, kVarlenTcRows, D).total, varlen_layout(g1, 64, D).total);

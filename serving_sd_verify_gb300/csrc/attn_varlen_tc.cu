@@ -127,6 +127,12 @@ __device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_ld_bind16(uint32_t (&r)[16]) { asm volatile("" : SDV_W8(0), SDV_W8(8)); }
 
+__device__ __forceinline__ void store_32b(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // true in one lane of a converged warp, the same one each time
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -717,16 +723,21 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             }
                             if (write) {
                                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + orow * D + 32 * c;
+                                uint32_t v[16];
 #pragma unroll
-                                for (int e = 0; e < 32; e += 8) {
-                                    uint4 v;
-                                    uint32_t *vw = reinterpret_cast<uint32_t *>(&v);
+                                for (int q = 0; q < 16; ++q) {
+                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
+                                    v[q] = *reinterpret_cast<const uint32_t *>(&b2);
+                                }
+                                // whole 32-byte sectors where the rows allow it
+                                if (p.out32) {
+                                    store_32b(dst, v);
+                                    store_32b(dst + 16, v + 8);
+                                } else {
 #pragma unroll
-                                    for (int q = 0; q < 4; ++q) {
-                                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[e + 2 * q], f[e + 2 * q + 1]);
-                                        vw[q] = *reinterpret_cast<const uint32_t *>(&b2);
-                                    }
-                                    *reinterpret_cast<uint4 *>(dst + e) = v;
+                                    for (int q = 0; q < 4; ++q)
+                                        *reinterpret_cast<uint4 *>(dst + 8 * q) =
+                                            make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                                 }
                             } else {
 #pragma unroll

@@ -106,6 +106,8 @@ struct VarlenParams {
     int line_shift;                 // the work line counts keys >> line_shift
     int min_share;                  // smallest share of a CTA on it
     float inv_grid;                 // 1 / CTAs
+    int fixed, group;               // its cost constants, below
+    int out32;                      // the output's rows are on 32-byte boundaries
     int rows;                       // rows of a partial slot
     float *o_part;                  // [2 * grid][D / 4][rows] float4, weighted sums of a CTA's first and last unit
     float2 *ml_part;                // [2 * grid][rows] (running max in log2 units, running sum)
@@ -118,11 +120,15 @@ constexpr int kVarlenTcRows = 256;      // rows of a unit, tensor cores: two til
 constexpr int kVarlenTcTileLog2 = 7;    // its keys per tile: 128
 constexpr int kVarlenGenTileLog2 = 6;   // keys per tile of the CUDA-core kernel: 64
 constexpr int kVarlenGenPerSm = 4;      // and its CTAs per SM at most
-constexpr int kVarlenFixed = 448;       // a unit's fixed cost, in keys (its queries, filling the pipeline, its epilogue)
-constexpr int kVarlenMinShare = 440;    // smallest share of a CTA, in the same keys: not longer than a unit of one key,
-                                        // so that the shortest units get a CTA each
-constexpr int kVarlenGroup = 4;         // units of up to so many tiles are not cut, and at that share others at its multiples
-constexpr int kVarlenMaxShift = 8;      // of the work line: a unit keeps a length of 1 at least
+// What the work line counts, in keys: a unit's fixed cost (its queries, filling
+// the pipeline, its epilogue); the smallest share of a CTA, not longer than a
+// unit of one key, so that the shortest units get a CTA each; and the tiles up
+// to which a unit is not cut, whose multiples it is cut at in that smallest share
+// (what a join costs).  From the kernels' times per unit and tile: tensor cores
+// 9,000 and 2,800 clocks a unit and a tile of 128 keys; the CUDA-core kernel
+// spends longer on its tiles than on the rest.
+constexpr int kVarlenTcFixed = 448, kVarlenTcMinShare = 440, kVarlenTcGroup = 4;
+constexpr int kVarlenGenFixed = 64, kVarlenGenMinShare = 64, kVarlenGenGroup = 1;
 constexpr int kVarlenMaxKv = 1 << 26;   // keys of a sequence
 constexpr int kVarlenMaxGrid = 1024;
 bool varlen_tc_supported(const VarlenParams &p);

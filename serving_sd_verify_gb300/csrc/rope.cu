@@ -29,34 +29,32 @@ __device__ __forceinline__ float2 rope_cs(uint64_t word, int pos, float m) {
     return make_float2(c * m, s * m);
 }
 
-template <typename T> struct Vec;
-template <> struct Vec<float> {
-    static constexpr int n = 4;
-    float f[4];
-    __device__ __forceinline__ void load(const float *p) {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+// V elements as loaded: a 16-byte vector, or one element
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
+template <typename T, int V> struct Raw {
+    uint4 w;
+    __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = w; }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const { unpack_bf16x8(w, f); }
+    __device__ __forceinline__ void unpack(float (&f)[4]) const {
+        f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
+        f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
     }
-    __device__ __forceinline__ void store(float *p) const {
-        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    __device__ __forceinline__ static uint32_t two(float a, float b) {      // rounded once, to nearest
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    __device__ __forceinline__ void pack(const float (&f)[8]) {
+        w = make_uint4(two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7]));
+    }
+    __device__ __forceinline__ void pack(const float (&f)[4]) {
+        w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
 };
-template <> struct Vec<__nv_bfloat16> {
-    static constexpr int n = 8;
-    float f[8];
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-        unpack_bf16x8(*reinterpret_cast<const uint4 *>(p), f);
-    }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
-        uint4 v;
-        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);   // rounded once, to nearest
-            w[i] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-        *reinterpret_cast<uint4 *>(p) = v;
-    }
+template <typename T> struct Raw<T, 1> {
+    T w;
+    __device__ __forceinline__ void load(const T *p) { w = *p; }
+    __device__ __forceinline__ void store(T *p) const { *p = w; }
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -113,90 +111,94 @@ rope_kernel(const RopeParams p, const int rot_chunks, const int chunks, const in
         const long t = id / chunks;
         const int grp = (int)(t % groups), n = (int)(t / groups);
         const int h0 = grp * kHeads, h1 = min(h0 + kHeads, p.Hq + (kAppend ? p.Hk : 0));
-        int pos = 0;
-        long slot = 0;
-        if (kAppend) {
-            slot = append_slot(p, n, pos);
-            if (slot == -2) return;
-        }
-        if (p.positions) pos = p.positions[n];
+        // the rows' loads go out first: neither the slot nor the angles hold them up
         const T *src[kHeads];
-        T *dst[kHeads];
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
             const int h = h0 + i;
-            src[i] = nullptr;
-            if (h >= h1) continue;
-            if (h < p.Hq) {
-                src[i] = x + (long)n * p.x_tok + (long)h * p.x_head;
-                dst[i] = y + (long)n * p.y_tok + (long)h * p.y_head;
-            } else if (slot >= 0) {
-                src[i] = static_cast<const T *>(p.k) + (long)n * p.kv_tok + (long)(h - p.Hq) * p.kv_head;
-                dst[i] = static_cast<T *>(p.k_pages) + slot + (long)(h - p.Hq) * p.pages.h;
+            src[i] = h >= h1 ? nullptr
+                     : h < p.Hq ? x + (long)n * p.x_tok + (long)h * p.x_head
+                                : static_cast<const T *>(p.k) + (long)n * p.kv_tok + (long)(h - p.Hq) * p.kv_head;
+        }
+        const bool turned = c < rot_chunks;
+        // a chunk's elements: [oa, oa + V) and, of a pair in the half layout, [ob, ob + V)
+        const int oa = !turned ? p.rot + (c - rot_chunks) * V : kInter ? c * (V > 1 ? V : 2) : c * V;
+        const int ob = kInter ? oa + 1 : oa + p.rot / 2;
+        const bool two = turned && (!kInter || V == 1);
+        Raw<T, V> a[kHeads], b[kHeads];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+            if (src[i]) {
+                a[i].load(src[i] + oa);
+                if (two) b[i].load(src[i] + ob);
+            }
+        int pos = p.positions ? p.positions[n] : 0;
+        long slot = 0;
+        if (kAppend) {
+            if (h1 <= p.Hq && p.positions) {           // queries with their positions: only whether n is anyone's
+                if (n < p.cu[0] || n >= p.cu[p.B]) return;
+            } else {
+                int cached = 0;
+                slot = append_slot(p, n, cached);
+                if (slot == -2) return;
+                if (!p.positions) pos = cached;
             }
         }
-        if (c < rot_chunks) {
-            float2 cs[NP];
+        float2 cs[NP];
+        if (turned) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) cs[i] = rope_cs(__ldg(p.turns + c * NP + i), pos, p.magnitude);
-            if constexpr (V > 1) {
-                Vec<T> a[kHeads], b[kHeads];
-                const int oa = c * V, ob = oa + p.rot / 2;
+        }
 #pragma unroll
-                for (int i = 0; i < kHeads; ++i)
-                    if (src[i]) {
-                        a[i].load(src[i] + oa);
-                        if (!kInter) b[i].load(src[i] + ob);
+        for (int i = 0; i < kHeads; ++i) {
+            const int h = h0 + i;
+            if (!src[i] || (h >= p.Hq && slot < 0)) continue;
+            T *dst = h < p.Hq ? y + (long)n * p.y_tok + (long)h * p.y_head
+                              : static_cast<T *>(p.k_pages) + slot + (long)(h - p.Hq) * p.pages.h;
+            if (turned) {
+                if constexpr (V > 1) {
+                    float fa[V], fb[V];
+                    a[i].unpack(fa);
+                    if (!kInter) b[i].unpack(fb);
+#pragma unroll
+                    for (int e = 0; e < NP; ++e) {
+                        float &u = kInter ? fa[2 * e] : fa[e];
+                        float &v = kInter ? fa[2 * e + 1] : fb[e];
+                        const float u0 = u, v0 = v;
+                        u = u0 * cs[e].x - v0 * cs[e].y;
+                        v = v0 * cs[e].x + u0 * cs[e].y;
                     }
-#pragma unroll
-                for (int i = 0; i < kHeads; ++i)
-                    if (src[i]) {
-#pragma unroll
-                        for (int e = 0; e < NP; ++e) {
-                            float &u = kInter ? a[i].f[2 * e] : a[i].f[e];
-                            float &v = kInter ? a[i].f[2 * e + 1] : b[i].f[e];
-                            const float u0 = u, v0 = v;
-                            u = u0 * cs[e].x - v0 * cs[e].y;
-                            v = v0 * cs[e].x + u0 * cs[e].y;
-                        }
-                        a[i].store(dst[i] + oa);
-                        if (!kInter) b[i].store(dst[i] + ob);
-                    }
-            } else {
-                const int oa = kInter ? 2 * c : c, ob = kInter ? 2 * c + 1 : c + p.rot / 2;
-#pragma unroll
-                for (int i = 0; i < kHeads; ++i)
-                    if (src[i]) {
-                        const float u0 = to_f(src[i][oa]), v0 = to_f(src[i][ob]);
-                        from_f(dst[i] + oa, u0 * cs[0].x - v0 * cs[0].y);
-                        from_f(dst[i] + ob, v0 * cs[0].x + u0 * cs[0].y);
-                    }
-            }
-        } else {
-            const int o = p.rot + (c - rot_chunks) * V;
-#pragma unroll
-            for (int i = 0; i < kHeads; ++i)
-                if (src[i] && dst[i] != src[i]) {
-                    if constexpr (V > 1)
-                        *reinterpret_cast<uint4 *>(dst[i] + o) = *reinterpret_cast<const uint4 *>(src[i] + o);
-                    else
-                        dst[i][o] = src[i][o];
+                    a[i].pack(fa);
+                    if (!kInter) b[i].pack(fb);
+                } else {
+                    const float u0 = to_f(a[i].w), v0 = to_f(b[i].w);
+                    from_f(&a[i].w, u0 * cs[0].x - v0 * cs[0].y);
+                    from_f(&b[i].w, v0 * cs[0].x + u0 * cs[0].y);
                 }
+            } else if (dst == src[i]) {
+                continue;                              // in place: what is not turned stays
+            }
+            a[i].store(dst + oa);
+            if (two) b[i].store(dst + ob);
         }
     } else if (kAppend && id < items + val_items) {
         const long v = id - items;
         const int c = (int)(v % val_chunks);
         const long t = v / val_chunks;
         const int grp = (int)(t % val_groups), n = (int)(t / val_groups);
+        const int h0 = grp * kHeads;
+        Raw<T, V> a[kHeads];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+            if (h0 + i < p.Hk)
+                a[i].load(static_cast<const T *>(p.v) + (long)n * p.kv_tok + (long)(h0 + i) * p.kv_head + c * V);
         int pos = 0;
         const long slot = append_slot(p, n, pos);
         if (slot < 0) return;
-        for (int h = grp * kHeads; h < min(grp * kHeads + kHeads, p.Hk); ++h) {
-            const T *src = static_cast<const T *>(p.v) + (long)n * p.kv_tok + (long)h * p.kv_head + c * V;
-            T *dst = static_cast<T *>(p.v_pages) + slot + (long)h * p.pages.h + c * V;
-            if constexpr (V > 1) *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(src);
-            else *dst = *src;
-        }
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+            if (h0 + i < p.Hk)
+                a[i].store(static_cast<T *>(p.v_pages) + slot + (long)(h0 + i) * p.pages.h + c * V);
     }
 }
 
@@ -235,7 +237,7 @@ cudaError_t launch_v(const RopeParams &p, cudaStream_t st) {
 // 16-byte vectors: whole vectors of rotated pairs and of the rest, every row on a 16-byte boundary
 template <typename T>
 bool vectors_fit(const RopeParams &p) {
-    constexpr int V = Vec<T>::n;
+    constexpr int V = kVec<T>;
     auto al = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
     if (p.D % V || p.rot % (p.interleaved ? V : 2 * V)) return false;
     if (p.Hq && (!al(p.x) || !al(p.y) || p.x_tok % V || p.x_head % V || p.y_tok % V || p.y_head % V)) return false;

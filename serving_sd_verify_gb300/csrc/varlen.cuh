@@ -59,12 +59,12 @@ __device__ __forceinline__ int vl_keys(const VarlenParams &p, const VlSeq &s, in
 // line_shift: the exact sum, shifted, so that it never decreases with r.
 __device__ __forceinline__ int vl_before(const VarlenParams &p, const VlSeq &s, int r) {
     if (r == 0) return 0;
-    const int full = (p.causal ? max(s.kv, s.q) : s.kv) + kVarlenFixed;   // the last unit's
+    const int full = (p.causal ? max(s.kv, s.q) : s.kv) + p.fixed;   // the last unit's
     if (s.nr == 1) return full >> p.line_shift;
     long w = (long)r * full;
     if (p.causal) {
         const int r1 = r == s.nr ? r - 1 : r;      // units of tb tokens among them
-        w = (long)r1 * (max(0, s.off) + kVarlenFixed) + (long)p.tb * ((long)r1 * (r1 + 1) / 2);
+        w = (long)r1 * (max(0, s.off) + p.fixed) + (long)p.tb * ((long)r1 * (r1 + 1) / 2);
         if (r == s.nr) w += full;
     }
     return (int)(w >> p.line_shift);
@@ -106,11 +106,11 @@ __device__ __forceinline__ int vl_tiles(const VarlenParams &p, int keys) {
 }
 
 // cut of a unit of length len and `tiles` tiles at `off` (0 <= off <= len): the
-// tiles before it, in whole groups (a unit of kVarlenGroup tiles or fewer is
+// tiles before it, in whole groups (a unit of p.group tiles or fewer is
 // not cut); non-decreasing in off
-__device__ __forceinline__ int vl_cut(int off, int len, int tiles, bool splittable, int group) {
+__device__ __forceinline__ int vl_cut(const VarlenParams &p, int off, int len, int tiles, bool splittable, int group) {
     const int groups = (tiles + group - 1) / group;
-    if (!splittable || tiles <= kVarlenGroup) return 2 * off >= len ? tiles : 0;
+    if (!splittable || tiles <= p.group) return 2 * off >= len ? tiles : 0;
     const int g = (int)((float)off * ((float)groups / (float)len) + 0.5f);
     return min(tiles, g * group);
 }
@@ -133,7 +133,7 @@ __device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const V
     }
     const int u0 = vl_before(p, s, r), len = vl_before(p, s, r + 1) - u0;
     const int tiles = vl_tiles(p, vl_keys(p, s, r));
-    int t = vl_cut(o - u0, len, tiles, vl_splittable(p, s), group);
+    int t = vl_cut(p, o - u0, len, tiles, vl_splittable(p, s), group);
     const VlPos in = {b, g, r, t, x - (o - u0), len, tiles, s.c0 + r * p.tb, min(p.tb, s.q - r * p.tb)};
     if (t < tiles || (tiles == 0 && 2 * (o - u0) < len)) return in;
     if (++r == s.nr) {                                         // at its end: the next unit's beginning
@@ -172,8 +172,8 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
     }
     // the smallest share the grid covers the line with (rounded up past fp32's error)
     pl.share = max(p.min_share, (int)((float)pl.total * p.inv_grid * (1.0f + 0x1p-20f)) + 1);
-    // joining parts costs about what four tiles cost: a part this short is not worth it
-    pl.group = pl.share > p.min_share ? 1 : kVarlenGroup;
+    // joining parts costs about what p.group tiles cost: a part this short is not worth it
+    pl.group = pl.share > p.min_share ? 1 : p.group;
     const int x0 = c * pl.share, x1 = x0 + pl.share;
     pl.idle = x0 >= pl.total;
     if (pl.idle) return pl;
@@ -302,7 +302,7 @@ __device__ void vl_ends(const VarlenParams &p, const VlPlan &pl, int c, VlEnds *
             const int x = k * pl.share;
             if (x <= at.x) return 0;
             if (x >= at.x + at.len || x >= pl.total) return at.tiles;
-            return vl_cut(x - at.x, at.len, at.tiles, true, pl.group);
+            return vl_cut(p, x - at.x, at.len, at.tiles, true, pl.group);
         };
         VlShared *r = to->u + found++;
         const int k0 = at.x / pl.share, k1 = min((at.x + at.len) / pl.share + 1, k0 + kVarlenMaxGrid);

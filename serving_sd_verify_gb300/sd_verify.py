@@ -455,7 +455,7 @@ def _on_current_device(*ts):
     for t in ts:
         if t is not None:
             d = t.get_device()       # -1 for a CPU tensor
-            if d != dev:
+            if d != dev or d < 0:
                 if dev >= 0 or d < 0:
                     raise ValueError("all tensors must be CUDA tensors on the current device")
                 dev = d
