@@ -84,12 +84,26 @@ __device__ long append_slot(const RopeParams &p, int n, int &pos) {
         set_fault(p.fault, FAULT_BAD_LENGTH);
         return -1;
     }
-    const int pg = p.table[(long)lo * p.table_stride + ps / p.page_size];
+    const unsigned col = (unsigned)ps / (unsigned)p.page_size;       // a position fits 31 bits: kv_len does
+    const int pg = p.table[(long)lo * p.table_stride + col];
     if (pg < 0 || pg >= p.n_pages) {
         set_fault(p.fault, FAULT_BAD_PAGE);
         return -1;
     }
-    return (long)pg * p.pages.b + (ps % p.page_size) * p.pages.s;
+    return (long)pg * p.pages.b + (long)((unsigned)ps - col * (unsigned)p.page_size) * p.pages.s;
+}
+
+// q and the remainder of a / b, in 32 bits where a fits (a 64-bit division is a
+// hundred instructions)
+__device__ __forceinline__ long divide(long a, int b, int &rem) {
+    if (a >> 32) {
+        const long q = a / b;
+        rem = (int)(a - q * b);
+        return q;
+    }
+    const unsigned q = (unsigned)a / (unsigned)b;
+    rem = (int)((unsigned)a - q * (unsigned)b);
+    return q;
 }
 
 // One thread: one chunk of a token for up to kHeads heads.  A chunk is NP
@@ -107,9 +121,8 @@ rope_kernel(const RopeParams p, const int rot_chunks, const int chunks, const in
     T *y = static_cast<T *>(p.y);
     if (id < items) {
         // consecutive threads: consecutive chunks, then head groups, then tokens
-        const int c = (int)(id % chunks);
-        const long t = id / chunks;
-        const int grp = (int)(t % groups), n = (int)(t / groups);
+        int c, grp;
+        const int n = (int)divide(divide(id, chunks, c), groups, grp);
         const int h0 = grp * kHeads, h1 = min(h0 + kHeads, p.Hq + (kAppend ? p.Hk : 0));
         // the rows' loads go out first: neither the slot nor the angles hold them up
         const T *src[kHeads];
@@ -183,9 +196,8 @@ rope_kernel(const RopeParams p, const int rot_chunks, const int chunks, const in
         }
     } else if (kAppend && id < items + val_items) {
         const long v = id - items;
-        const int c = (int)(v % val_chunks);
-        const long t = v / val_chunks;
-        const int grp = (int)(t % val_groups), n = (int)(t / val_groups);
+        int c, grp;
+        const int n = (int)divide(divide(v, val_chunks, c), val_groups, grp);
         const int h0 = grp * kHeads;
         Raw<T, V> a[kHeads];
 #pragma unroll
