@@ -126,11 +126,9 @@ attn_varlen_generic_kernel(const VarlenParams p) {
                 }
             }
             __syncthreads();
-            float s[TM][4];
+            float2 s2[TM][2];
 #pragma unroll
-            for (int a = 0; a < TM; ++a)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) s[a][c] = 0.f;
+            for (int a = 0; a < TM; ++a) s2[a][0] = s2[a][1] = make_float2(0.f, 0.f);
 #pragma unroll 8
             for (int d = 0; d < D; ++d) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(Ks + d * L::kKs + 4 * tx);
@@ -142,10 +140,16 @@ attn_varlen_generic_kernel(const VarlenParams p) {
                     q[0] = Qs[d * L::kQs + ty];
                 }
 #pragma unroll
-                for (int a = 0; a < TM; ++a) {
-                    s[a][0] = fmaf(q[a], k4.x, s[a][0]); s[a][1] = fmaf(q[a], k4.y, s[a][1]);
-                    s[a][2] = fmaf(q[a], k4.z, s[a][2]); s[a][3] = fmaf(q[a], k4.w, s[a][3]);
+                for (int a = 0; a < TM; ++a) {       // two multiply-adds an instruction
+                    s2[a][0] = __ffma2_rn(make_float2(q[a], q[a]), make_float2(k4.x, k4.y), s2[a][0]);
+                    s2[a][1] = __ffma2_rn(make_float2(q[a], q[a]), make_float2(k4.z, k4.w), s2[a][1]);
                 }
+            }
+            float s[TM][4];
+#pragma unroll
+            for (int a = 0; a < TM; ++a) {
+                s[a][0] = s2[a][0].x; s[a][1] = s2[a][0].y;
+                s[a][2] = s2[a][1].x; s[a][3] = s2[a][1].y;
             }
             __syncthreads();       // K has been read; P goes over it
 #pragma unroll
@@ -190,8 +194,11 @@ attn_varlen_generic_kernel(const VarlenParams p) {
                     const float4 v4 = *reinterpret_cast<const float4 *>(Vs + kk * D + 16 * c + 4 * tx);
 #pragma unroll
                     for (int a = 0; a < TM; ++a) {
-                        o[a][c] = fmaf(q[a], v4.x, o[a][c]); o[a][c + 1] = fmaf(q[a], v4.y, o[a][c + 1]);
-                        o[a][c + 2] = fmaf(q[a], v4.z, o[a][c + 2]); o[a][c + 3] = fmaf(q[a], v4.w, o[a][c + 3]);
+                        const float2 w = make_float2(q[a], q[a]);
+                        float2 lo = make_float2(o[a][c], o[a][c + 1]), hi = make_float2(o[a][c + 2], o[a][c + 3]);
+                        lo = __ffma2_rn(w, make_float2(v4.x, v4.y), lo);
+                        hi = __ffma2_rn(w, make_float2(v4.z, v4.w), hi);
+                        o[a][c] = lo.x; o[a][c + 1] = lo.y; o[a][c + 2] = hi.x; o[a][c + 3] = hi.y;
                     }
                 }
             }

@@ -362,13 +362,15 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     auto issue_s = [&](int i, int qt, int slot) {
                         const uint64_t qd = qd0 + (uint64_t)(qt * (L::kTile / 16)),
                                        kd = kd0 + (uint64_t)(slot * (L::kTile / 16));
+                        if (el) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = (kk & 3) * 2;
-                            if (el) umma_ss(tmem + 128u * i, qd + off + (kk >> 2) * (128 * 128 / 16),
-                                            kd + off + (kk >> 2) * khalf, idS, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint64_t off = (kk & 3) * 2;
+                                umma_ss(tmem + 128u * i, qd + off + (kk >> 2) * (128 * 128 / 16),
+                                        kd + off + (kk >> 2) * khalf, idS, kk > 0 ? 1u : 0u);
+                            }
+                            umma_commit(sfull_bar(i));
                         }
-                        if (el) umma_commit(sfull_bar(i));
                     };
                     auto issue_pv = [&](int i, int slot, bool first) {
                         const uint64_t vd = vd0 + (uint64_t)(slot * (L::kTile / 16));
@@ -377,10 +379,12 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             ok = ok && wait_bar(pfull_bar(i, h), pphase[i], abort_flag, p.fault);
                             if (!ok) return;
                             tc_fence_after();
+                            if (el) {
 #pragma unroll
-                            for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk)
-                                if (el) umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + vrow[kk], idO,
-                                                (!first || kk > 0) ? 1u : 0u);
+                                for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk)
+                                    umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + vrow[kk], idO,
+                                            (!first || kk > 0) ? 1u : 0u);
+                            }
                         }
                         pphase[i] ^= 1u;
                     };
