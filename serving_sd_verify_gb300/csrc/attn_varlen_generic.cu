@@ -26,23 +26,26 @@ constexpr float kGLog2e = 1.4426950408889634f;
 
 template <int D, int R> struct GLay {
     static constexpr int kQs = R + 4;               // transposed rows, padded: 16-byte aligned, bank-shifted
-    static constexpr int kKs = kGTile + 4;
+    static constexpr int kKs = kGTile;              // transposed keys, swizzled (key_at)
     static constexpr int kQ = D * kQs;              // floats
     static constexpr int kK = D * kKs;              // P overlays K: [kGTile][kQs]
     static constexpr int kV = kGTile * D;
-    static constexpr int kSmem = (kQ + kK + kV) * 4;
-    static_assert(kGTile * kQs <= kK, "P fits over K");
+    static constexpr int kP = kGTile * kQs;         // P has its own room where K's is too small
+    static constexpr int kSmem = (kQ + (kK > kP ? kK : kP) + kV) * 4;
 };
 
-// first element of key `key`'s row of the unit's kv head, or null for a bad page
-template <typename T>
-__device__ __forceinline__ const T *key_row(const VarlenParams &p, const VlUnit &u, const void *base, int key) {
-    const T *t = static_cast<const T *>(base);
-    if (!p.table) return t + (long)(u.row0 - u.tok0 + key) * p.kv.s + (long)u.g * p.kv.h;
-    const int pi = p.page_log2 >= 0 ? key >> p.page_log2 : key / p.page_size;
+// Element (d, key) of the transposed keys: groups of 4 keys, exchanged within a
+// row by d / 4, so that a warp that stores 8 vectors of 4 keys hits 32 banks and
+// one that reads 64 keys of a row does too.
+__device__ __forceinline__ int key_at(int d, int key4) { return d * kGTile + ((key4 ^ ((d >> 2) & 15)) << 2); }
+
+// offset of key `key`'s row of the unit's kv head, or -1 for a bad page
+__device__ __forceinline__ long key_offset(const VarlenParams &p, const VlUnit &u, int key) {
+    if (!p.table) return (long)(u.row0 - u.tok0 + key) * p.kv.s + (long)u.g * p.kv.h;
+    const unsigned pi = p.page_log2 >= 0 ? (unsigned)key >> p.page_log2 : (unsigned)key / (unsigned)p.page_size;
     const int pg = __ldg(p.table + (long)u.b * p.table_stride + pi);
-    if (pg < 0 || pg >= p.n_pages) { set_fault(p.fault, FAULT_BAD_PAGE); return nullptr; }
-    return t + (long)pg * p.kv.b + (long)(key - pi * p.page_size) * p.kv.s + (long)u.g * p.kv.h;
+    if (pg < 0 || pg >= p.n_pages) { set_fault(p.fault, FAULT_BAD_PAGE); return -1; }
+    return (long)pg * p.kv.b + (long)(key - (int)pi * p.page_size) * p.kv.s + (long)u.g * p.kv.h;
 }
 
 template <typename T, int D, int R>
@@ -53,9 +56,9 @@ attn_varlen_generic_kernel(const VarlenParams p) {
     constexpr int VP = Elem<T>::kPerVec, VPR = D / VP;
     extern __shared__ float4 smem4[];
     float *Qs = reinterpret_cast<float *>(smem4);    // [D][R + 4]
-    float *Ks = Qs + L::kQ;                          // [D][64 + 4]
+    float *Ks = Qs + L::kQ;                          // [D][64], swizzled
     float *Ps = Ks;                                  // [64][R + 4]
-    float *Vs = Ks + L::kK;                          // [64][D]
+    float *Vs = Ks + (L::kK > L::kP ? L::kK : L::kP);  // [64][D]
     __shared__ VlPlan pl;
     __shared__ VlEnds ends;
     __shared__ int join_flag;
@@ -104,13 +107,17 @@ attn_varlen_generic_kernel(const VarlenParams p) {
         for (int t = u.t0; t < u.t1; ++t) {
             const int key0 = t * kGTile;
             __syncthreads();
-            for (int i = tid; i < kGTile * VPR; i += kGThreads) {
-                const int kk = i / VPR, v = i % VPR;
+            // a warp takes 8 vectors of 4 keys at a time
+            for (int i = tid >> 5; i < (kGTile / 4) * (VPR / 8); i += kGThreads / 32) {
+                const int kk = 4 * (i / (VPR / 8)) + ((tid >> 3) & 3), v = 8 * (i % (VPR / 8)) + (tid & 7);
                 float kf[VP], vf[VP];
                 const T *kp = nullptr, *vp = nullptr;
                 if (key0 + kk < u.kv) {
-                    kp = key_row<T>(p, u, p.k, key0 + kk);
-                    vp = key_row<T>(p, u, p.v, key0 + kk);
+                    const long at = key_offset(p, u, key0 + kk);
+                    if (at >= 0) {
+                        kp = static_cast<const T *>(p.k) + at;
+                        vp = static_cast<const T *>(p.v) + at;
+                    }
                 }
                 if (kp) {
                     Elem<T>::load_vec(kp + v * VP, kf);
@@ -120,10 +127,10 @@ attn_varlen_generic_kernel(const VarlenParams p) {
                     for (int e = 0; e < VP; ++e) { kf[e] = 0.f; vf[e] = 0.f; }
                 }
 #pragma unroll
-                for (int e = 0; e < VP; ++e) {
-                    Ks[(v * VP + e) * L::kKs + kk] = kf[e];
-                    Vs[kk * D + v * VP + e] = vf[e];
-                }
+                for (int e = 0; e < VP; ++e) Ks[key_at(v * VP + e, kk >> 2) + (kk & 3)] = kf[e];
+#pragma unroll
+                for (int e = 0; e < VP; e += 4)
+                    *reinterpret_cast<float4 *>(Vs + kk * D + v * VP + e) = make_float4(vf[e], vf[e + 1], vf[e + 2], vf[e + 3]);
             }
             __syncthreads();
             float2 s2[TM][2];
@@ -131,7 +138,7 @@ attn_varlen_generic_kernel(const VarlenParams p) {
             for (int a = 0; a < TM; ++a) s2[a][0] = s2[a][1] = make_float2(0.f, 0.f);
 #pragma unroll 8
             for (int d = 0; d < D; ++d) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(Ks + d * L::kKs + 4 * tx);
+                const float4 k4 = *reinterpret_cast<const float4 *>(Ks + key_at(d, tx));
                 float q[TM];
                 if constexpr (TM == 4) {
                     const float4 q4 = *reinterpret_cast<const float4 *>(Qs + d * L::kQs + 4 * ty);
@@ -169,15 +176,20 @@ attn_varlen_generic_kernel(const VarlenParams p) {
                 float sum = 0.f;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float pv = exp2f(s[a][c] - ref);
-                    sum += pv;
-                    Ps[(4 * tx + c) * L::kQs + ty * TM + a] = pv;
+                    s[a][c] = exp2f(s[a][c] - ref);
+                    sum += s[a][c];
                 }
 #pragma unroll
                 for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
                 l[a] = fmaf(l[a], alpha, sum);
 #pragma unroll
                 for (int e = 0; e < TN; ++e) o[a][e] *= alpha;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float *to = Ps + (4 * tx + c) * L::kQs + ty * TM;
+                if constexpr (TM == 4) *reinterpret_cast<float4 *>(to) = make_float4(s[0][c], s[1][c], s[2][c], s[3][c]);
+                else *to = s[0][c];
             }
             __syncthreads();
 #pragma unroll 4
