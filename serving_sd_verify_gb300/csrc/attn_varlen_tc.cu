@@ -140,11 +140,14 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-template <int D, bool kPaged>
+// kSmall: no sequence has more rows of a kv head than one tile holds (decoding,
+// block verification).  Those calls are bound by memory, so P goes into the
+// second product as two bf16 terms, to 2^-16 of each weight, and the second row
+// tile's room is a ring slot more.
+template <int D, bool kPaged, bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                      const __grid_constant__ CUtensorMap tmap_v, const VarlenParams p, const int tpt, const int box,
-                      const int small) {
+                      const __grid_constant__ CUtensorMap tmap_v, const VarlenParams p, const int tpt, const int box) {
     using L = Lay<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -153,8 +156,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = (int)blockIdx.x;
 
-    const uint32_t sQ = base + L::kOffQ, sRing = base + L::kOffRing - (small ? L::kTile : 0), bar0 = base + L::kOffBar;
-    const int slots = small ? L::kMaxSlots : L::kSlots;
+    const uint32_t sQ = base + L::kOffQ, sRing = base + L::kOffRing - (kSmall ? L::kTile : 0), bar0 = base + L::kOffBar;
+    constexpr int slots = kSmall ? L::kMaxSlots : L::kSlots;
     auto full_bar = [&](int i) { return bar0 + 8u * i; };
     auto empty_bar = [&](int i) { return bar0 + 8u * (L::kMaxSlots + i); };
     const uint32_t bar1 = bar0 + 8u * (2 * L::kMaxSlots);
@@ -225,7 +228,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 while (ok && walk.next(p, pl, u)) {
                     const int n = u.t1 - u.t0;
                     if (n <= 0) continue;
-                    const int la = u.ntok <= tpt ? 2 : 1;
+                    const int la = kSmall || u.ntok <= tpt ? 2 : 1;
                     const uint64_t policy = walk.s.nr == 1 ? once : again;
                     const int32_t *trow = kPaged ? p.table + (long)u.b * p.table_stride : nullptr;
                     // the lane's page of tile t: looked up a tile ahead, first used (and checked) by its copy
@@ -284,7 +287,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         if (!ok) break;
                     }
                     if (lane == 0) {
-                        const int nq = u.ntok <= tpt ? 1 : 2;
+                        const int nq = kSmall || u.ntok <= tpt ? 1 : 2;
                         mbar_arrive_expect_tx(qfull_bar, (uint32_t)(nq * L::kHalves * 128 * G * tpt));
                         for (int i = 0; i < nq; ++i)
                             for (int h = 0; h < L::kHalves; ++h)
@@ -381,9 +384,13 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             tc_fence_after();
                             if (el) {
 #pragma unroll
-                                for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk)
+                                for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk) {
                                     umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + vrow[kk], idO,
                                             (!first || kk > 0) ? 1u : 0u);
+                                    if (kSmall)
+                                        umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 64u + 8u * kk, vd + vrow[kk],
+                                                idO, 1u);
+                                }
                             }
                         }
                         pphase[i] ^= 1u;
@@ -400,7 +407,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     while (ok && walk.next(p, pl, u)) {
                         const int n = u.t1 - u.t0;
                         if (n <= 0) continue;
-                        const bool pair = u.ntok > tpt;
+                        const bool pair = !kSmall && u.ntok > tpt;
                         ok = wait_bar(qfull_bar, qphase, abort_flag, p.fault);
                         if (!ok) break;
                         qphase ^= 1u;
@@ -495,7 +502,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             bool ok = true;
             while (walk.next(p, pl, u)) {
                 const int n = u.t1 - u.t0;
-                const bool pair = u.ntok > tpt;
+                const bool pair = !kSmall && u.ntok > tpt;
                 const int tl = tr + (pair && w ? tpt : 0);             // token within the unit
                 const bool row_ok = tr < tpt && tl < u.ntok;
                 const int lim = row_ok ? vl_limit(p, u, u.tok0 + tl) : 0;
@@ -549,7 +556,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         }
                         const float2 qk2 = make_float2(qk, qk);
                         float2 ls[2], nm2;
-                        uint32_t pk[16];
+                        uint32_t pk[16], lo[kSmall ? 16 : 1];
                         // weights of 16 keys: 8 words from `at`
                         auto weights = [&](int at) {
 #pragma unroll
@@ -560,7 +567,13 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 const float p0 = ex2(x.x), p1 = ex2(x.y);
                                 ls[c & 1] = __fadd2_rn(ls[c & 1], make_float2(p0, p1));
                                 const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-                                pk[c & 15] = *reinterpret_cast<const uint32_t *>(&b2);
+                                const uint32_t hi = *reinterpret_cast<const uint32_t *>(&b2);
+                                pk[c & 15] = hi;
+                                if constexpr (kSmall) {       // what the rounding left, exact in fp32
+                                    const __nv_bfloat162 r2 = __floats2bfloat162_rn(
+                                        p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+                                    lo[c & 15] = *reinterpret_cast<const uint32_t *>(&r2);
+                                }
                             }
                         };
                         float m4[4];
@@ -598,17 +611,23 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         ls[0] = ls[1] = make_float2(0.f, 0.f);
                         weights(0);
                         l *= alpha;
-                        tmem_st16(s_col, pk);
+                        // 32 keys' weights, over the scores' first 64 columns (what is left of them over the others)
+                        auto put = [&](uint32_t q) {
+                            tmem_st16(s_col + 16u * q, pk);
+                            if constexpr (kSmall) tmem_st16(s_col + 64u + 16u * q, lo);
+                        };
+                        put(0);
                         weights(16);
-                        tmem_st16(s_col + 16u, pk);
-                        weights(32);
+                        put(1);
+                        if (!kSmall) weights(32);      // while the stores run (the small form has no registers for it)
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(pfull_bar(w, 0));
-                        tmem_st16(s_col + 32u, pk);
+                        if (kSmall) weights(32);
+                        put(2);
                         weights(48);
-                        tmem_st16(s_col + 48u, pk);
+                        put(3);
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
@@ -838,7 +857,7 @@ int page_box(int page_size) {       // slots per copy: the largest power of two 
     return b;
 }
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kSmall>
 cudaError_t configure() {
     // the shared-memory limit, and the registers that the warps share out
     static std::atomic<bool> done[kMaxDevices];
@@ -847,16 +866,16 @@ cudaError_t configure() {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, attn_varlen_tc_kernel<D, kPaged>);
+    e = cudaFuncGetAttributes(&a, attn_varlen_tc_kernel<D, kPaged, kSmall>);
     if (e != cudaSuccess) return e;
     if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;   // setmaxnreg would wait for registers that are not there
-    e = cudaFuncSetAttribute(attn_varlen_tc_kernel<D, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_varlen_tc_kernel<D, kPaged, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Lay<D>::kSmem);
     if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
     return e;
 }
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kSmall>
 cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     const int G = p.Hq / p.Hkv, tpt = 128 / G;
     alignas(64) CUtensorMap mq, mk, mv;
@@ -885,7 +904,7 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
             if (!encode_vl(m, t, 4, dims, strides, box)) return cudaErrorInvalidValue;
         }
     }
-    cudaError_t e = configure<D, kPaged>();
+    cudaError_t e = configure<D, kPaged, kSmall>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -901,8 +920,7 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kPaged>, mq, mk, mv, p, tpt, box_rows,
-                              p.max_q <= tpt ? 1 : 0);
+    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kPaged, kSmall>, mq, mk, mv, p, tpt, box_rows);
 }
 
 }  // namespace
@@ -926,8 +944,13 @@ bool varlen_tc_supported(const VarlenParams &p) {
 }
 
 cudaError_t launch_varlen_tc(const VarlenParams &p, int grid, cudaStream_t st) {
-    if (p.table) return p.D == 128 ? launch_tc<128, true>(p, grid, st) : launch_tc<64, true>(p, grid, st);
-    return p.D == 128 ? launch_tc<128, false>(p, grid, st) : launch_tc<64, false>(p, grid, st);
+    const bool small = p.max_q <= 128 / (p.Hq / p.Hkv);
+    if (p.D == 128) {
+        if (p.table) return small ? launch_tc<128, true, true>(p, grid, st) : launch_tc<128, true, false>(p, grid, st);
+        return small ? launch_tc<128, false, true>(p, grid, st) : launch_tc<128, false, false>(p, grid, st);
+    }
+    if (p.table) return small ? launch_tc<64, true, true>(p, grid, st) : launch_tc<64, true, false>(p, grid, st);
+    return small ? launch_tc<64, false, true>(p, grid, st) : launch_tc<64, false, false>(p, grid, st);
 }
 
 }  // namespace sdv
