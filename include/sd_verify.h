@@ -518,8 +518,8 @@ sd_status sd_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, c
  *
  *   q     device [N, Hq, D], element strides (q_tok, q_head), multiples of 16 bytes
  *   out   device [N, Hq, D] contiguous, of the inputs' dtype (fp32 sums and
- *         softmax, one rounding at the end); rows from cu_q[B] on are left as
- *         they were
+ *         softmax, one rounding at the end), overlapping no input; rows from
+ *         cu_q[B] on are left as they were
  *   max_q, max_kv  host upper bounds of the sequences' new tokens and kv_len;
  *         N, max_q and max_kv at most 2^26
  *   query head h reads kv head h / (Hq / Hkv); Hq / Hkv <= 64; D in {64, 128}

@@ -147,8 +147,12 @@ __device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const V
 // kept short: most of its time is instruction fetch.  The line's length stays
 // below 2^31 (the host picks line_shift by its bounds); offsets that are no
 // offsets could exceed it and then nothing is computed.
+// Up to 32 sequences a lane holds one each.  More go in blocks of 32 whose
+// lengths the lanes hold (32 blocks at a time), so that only the two blocks in
+// which the share begins and ends are read again.
 __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
     const int lane = threadIdx.x & 31;
+    constexpr unsigned kAll = 0xffffffffu;
     VlPlan pl = {};
     VlSeq s = {};
     unsigned w = 0, total = 0, coarse = 0;
@@ -158,12 +162,41 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
             s = vl_seq(p, b, report);
             w = (unsigned)p.Hkv * (unsigned)vl_before(p, s, s.nr);
         }
+        return w;
     };
+    auto scan = [&](unsigned v) {
+        int e = (int)v;
 #pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        read(b0 + lane, c == 0);
-        total += __reduce_add_sync(0xffffffffu, w);
-        coarse = min(coarse + __reduce_add_sync(0xffffffffu, w >> 8), 1u << 30);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(kAll, e, d);
+            if (lane >= d) e += y;
+        }
+        return e;
+    };
+    // the lengths of blocks s0 / 32 .. s0 / 32 + 31, one per lane
+    auto blocks = [&](int s0, bool report) {
+        unsigned mine = 0;
+#pragma unroll 4
+        for (int k = 0; k < 32; ++k) {
+            const int b0 = s0 + 32 * k;
+            if (b0 >= p.B) break;
+            const unsigned t = __reduce_add_sync(kAll, read(b0 + lane, report));
+            if (lane == k) mine = t;
+        }
+        return mine;
+    };
+    unsigned held = 0;
+    if (p.B <= 32) {
+        held = read(lane, c == 0);
+        total = __reduce_add_sync(kAll, held);
+        coarse = __reduce_add_sync(kAll, held >> 8);
+    } else {
+#pragma unroll 1
+        for (int s0 = 0; s0 < p.B; s0 += 1024) {
+            held = blocks(s0, c == 0);
+            total += __reduce_add_sync(kAll, held);
+            coarse = min(coarse + __reduce_add_sync(kAll, held >> 8), 1u << 30);
+        }
     }
     pl.total = (int)total;
     if (coarse >= (1u << 23) - 1024u) {
@@ -180,38 +213,44 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
     // the sequences in which the share begins and ends: lane 0 then places the
     // beginning and lane 1 the end, side by side
     const int x = lane == 0 ? x0 : x1;
-    int base = 0, o = 0, found = p.B;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        if (p.B > 32) read(b0 + lane, false);
-        int e = (int)w;
-        if (p.B > 1) {
-#pragma unroll 1
-            for (int d = 1; d < 32; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, e, d);
-                if (lane >= d) e += y;
-            }
-        }
-        e += base;
-        const int a = e - (int)w;
-        const unsigned ms = __ballot_sync(0xffffffffu, x0 >= a && x0 < e);
-        const unsigned me = __ballot_sync(0xffffffffu, x1 >= a && x1 < e);
+    int o = 0, found = p.B;
+    // among 32 sequences from b0 whose first begins at `base`
+    auto find = [&](int b0, int base) {
+        const int e = base + (p.B > 1 ? scan(w) : (int)w), a = e - (int)w;
+        const unsigned ms = __ballot_sync(kAll, x0 >= a && x0 < e), me = __ballot_sync(kAll, x1 >= a && x1 < e);
         const unsigned m = lane == 0 ? ms : me;
         const int src = __ffs((int)m) - 1;         // -1 where there is none: lane 31, not used
         VlSeq t;
-        t.c0 = __shfl_sync(0xffffffffu, s.c0, src);
-        t.q = __shfl_sync(0xffffffffu, s.q, src);
-        t.kv = __shfl_sync(0xffffffffu, s.kv, src);
-        t.nr = __shfl_sync(0xffffffffu, s.nr, src);
-        const int ta = __shfl_sync(0xffffffffu, a, src);
+        t.c0 = __shfl_sync(kAll, s.c0, src);
+        t.q = __shfl_sync(kAll, s.q, src);
+        t.kv = __shfl_sync(kAll, s.kv, src);
+        t.nr = __shfl_sync(kAll, s.nr, src);
+        const int ta = __shfl_sync(kAll, a, src);
         if (m && found == p.B) {
             t.off = t.kv - t.q;
             pl.s = t;
             o = x - ta;
             found = b0 + src;
         }
-        if (me) break;
-        base = __shfl_sync(0xffffffffu, e, 31);
+    };
+    if (p.B <= 32) {
+        find(0, 0);
+    } else {
+        int base = 0;
+#pragma unroll 1
+        for (int s0 = 0; s0 < p.B; s0 += 1024) {
+            if (p.B > 1024) held = blocks(s0, false);
+            const int e = base + scan(held), a = e - (int)held;
+            unsigned at = __ballot_sync(kAll, x0 >= a && x0 < e) | __ballot_sync(kAll, x1 >= a && x1 < e);
+            while (at) {                           // one block or two
+                const int k = __ffs((int)at) - 1;
+                at &= at - 1;
+                read(s0 + 32 * k + lane, false);
+                find(s0 + 32 * k, __shfl_sync(kAll, a, k));
+            }
+            base = __shfl_sync(kAll, e, 31);
+            if (x1 < base) break;
+        }
     }
     VlPos at = {p.B, 0, 0, 0};
     if (lane < 2 && found < p.B) at = vl_locate(p, found, pl.s, x, o, pl.group);

@@ -604,3 +604,117 @@ def test_workspace_too_small_and_reuse_across_shapes(S):
         S.sd_paged_attention(*args[:10], big)
         torch.cuda.synchronize()
         assert torch.equal(out[:21], good[:21])
+
+
+# --------------------------------------------------------------------------
+# large pools, many sequences, shared pages
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,path", [(torch.float32, 0), (torch.bfloat16, 1), (torch.bfloat16, 2)])
+def test_pools_beyond_32_bit_offsets(S, dtype, path):
+    """Pages whose first element lies past 2^31: a pool of 2^31 + 2^21 elements of which a few pages
+    at both ends are used, through the append, the attention and a table that is a view."""
+    Hq, Hkv, D, page = 8, 4, 128, 64
+    per = page * Hkv * D
+    n_pages = (1 << 31) // per + 64
+    kp = torch.empty(n_pages, page, Hkv, D, dtype=dtype, device="cuda")
+    vp = torch.empty_like(kp)
+    g = torch.Generator().manual_seed(6)
+    ids = torch.tensor([n_pages - 1, 0, n_pages - 2, 3], dtype=torch.int32)
+    wide = torch.full((2, 9), -7, dtype=torch.int32)
+    wide[0, 2:4], wide[1, 2:4] = ids[:2], ids[2:]
+    table = wide.cuda()[:, 2:7]
+    lens = [100, 70]
+    x = randn(g, sum(lens), Hq + 2 * Hkv, D, dtype=dtype)
+    dev, cu = x.cuda(), cumulative(lens).cuda()
+    kv = torch.tensor(lens, dtype=torch.int32).cuda()
+    turns = torch.zeros(D // 2, dtype=torch.int64, device="cuda")        # turned by nothing: the cache holds x
+    q = torch.empty(sum(lens), Hq, D, dtype=dtype, device="cuda")
+    S.sd_rotary_append_paged(dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:], q, None, turns, cu, kv, table, kp, vp)
+    out = torch.empty_like(q)
+    ws = S.workspace(S.sd_paged_attention_workspace_size(sum(lens), 2, 100, Hq, Hkv, D, 100, dt_code(S, dtype)))
+    S.sd_set_attention_path(path)
+    scale = 1 / math.sqrt(D)
+    S.sd_paged_attention(q, kp, vp, table, cu, kv, 100, 100, out, scale, ws)
+    torch.cuda.synchronize()
+    used = S.sd_last_attention_path()[0]
+    assert S.sd_fault_word() == 0
+    at = 0
+    for c in lens:
+        r = x[at:at + c]
+        check(out[at:at + c], *ref_attend(r[:, :Hq], r[:, Hq:Hq + Hkv], r[:, Hq + Hkv:], scale, True), dtype, used == 2)
+        at += c
+    del kp, vp
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,path", [(torch.float32, 0), (torch.bfloat16, 2)])
+@pytest.mark.parametrize("B", [33, 300, 1500])
+def test_many_sequences(S, dtype, path, B):
+    q_lens = [(i * 7) % 4 for i in range(B)]
+    kv_lens = [max(a, (i * 37) % 150) for i, a in enumerate(q_lens)]
+    paged_case(S, q_lens, kv_lens, 4, 2, 64, dtype, 16, True, path, seed=B)
+
+
+@pytest.mark.parametrize("path", [1, 2])
+def test_sequences_that_share_pages(S, path):
+    """Two sequences with one prefix (the same pages), and one that appears twice."""
+    g = torch.Generator().manual_seed(9)
+    Hq, Hkv, D, page, dtype = 28, 4, 128, 16, torch.bfloat16
+    kp, vp = (randn(g, 12, page, Hkv, D, dtype=dtype) for _ in range(2))
+    table = torch.tensor([[1, 5, 7, 2], [1, 5, 3, 0], [1, 5, 7, 2]], dtype=torch.int32)
+    kv_lens, q_lens = [60, 40, 60], [2, 5, 2]
+    q = randn(g, 9, Hq, D, dtype=dtype)
+    q[7:] = q[:2]
+    out = torch.empty(9, Hq, D, dtype=dtype, device="cuda")
+    ws = S.workspace(S.sd_paged_attention_workspace_size(9, 3, 5, Hq, Hkv, D, 60))
+    S.sd_set_attention_path(path)
+    S.sd_paged_attention(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), cumulative(q_lens).cuda(),
+                         torch.tensor(kv_lens, dtype=torch.int32).cuda(), 5, 60, out, 0.1, ws)
+    at = 0
+    for b, c in enumerate(q_lens):
+        i = torch.arange(kv_lens[b])
+        k, v = (t[table[b, i // page].long(), i % page] for t in (kp, vp))
+        check(out[at:at + c], *ref_attend(q[at:at + c], k, v, 0.1, True), dtype, path == 2)
+        at += c
+    assert torch.equal(out[7:], out[:2])
+
+
+def test_values_behind_what_a_unit_sees_may_be_anything(S):
+    """Non-finite keys and values in the slots past kv_len, inside the last page and in the pages behind it."""
+    g = torch.Generator().manual_seed(10)
+    Hq, Hkv, D, page, dtype = 8, 2, 64, 32, torch.bfloat16
+    for bad in (float("nan"), float("inf"), -float("inf"), 3e38):
+        pool = Pool(g, [70, 33], page, Hkv, D, dtype, fill=bad)
+        ks, vs = [], []
+        for b, m in enumerate((70, 33)):
+            ks.append(randn(g, m, Hkv, D, dtype=dtype))
+            vs.append(randn(g, m, Hkv, D, dtype=dtype))
+            pool.write(b, ks[b], vs[b])
+        kp, vp, table = pool.cuda()
+        q = randn(g, 40, Hq, D, dtype=dtype)
+        ws = S.workspace(S.sd_paged_attention_workspace_size(40, 2, 39, Hq, Hkv, D, 70))
+        for path in (1, 2):
+            for causal in (True, False):
+                out = torch.empty(40, Hq, D, dtype=dtype, device="cuda")
+                S.sd_set_attention_path(path)
+                S.sd_paged_attention(q.cuda(), kp, vp, table, cumulative([39, 1]).cuda(),
+                                     torch.tensor([70, 33], dtype=torch.int32).cuda(), 39, 70, out, 0.125, ws, causal=causal)
+                check(out[:39], *ref_attend(q[:39], ks[0], vs[0], 0.125, causal), dtype, path == 2)
+                check(out[39:], *ref_attend(q[39:], ks[1], vs[1], 0.125, causal), dtype, path == 2)
+
+
+def test_output_rows_on_16_byte_boundaries(S):
+    g = torch.Generator().manual_seed(12)
+    x = randn(g, 150, 12, 64, dtype=torch.bfloat16)
+    dev = x.cuda()
+    buf = torch.full((150 * 8 * 64 + 64,), 5.0, dtype=torch.bfloat16, device="cuda")
+    ws = S.workspace(S.sd_paged_attention_workspace_size(150, 1, 150, 8, 2, 64, 150))
+    for off in (0, 8, 16, 24):
+        out = buf[off:off + 150 * 8 * 64].view(150, 8, 64)
+        S.sd_prompt_attention(dev[:, :8], dev[:, 8:10], dev[:, 10:], cumulative([150]).cuda(), 150, out, 0.125, ws)
+        check(out, *ref_attend(x[:, :8], x[:, 8:10], x[:, 10:], 0.125, True), torch.bfloat16, True)
+    with pytest.raises(S.SdError) as e:
+        S.sd_prompt_attention(dev[:, :8], dev[:, 8:10], dev[:, 10:], cumulative([150]).cuda(), 150,
+                              buf[4:4 + 150 * 8 * 64].view(150, 8, 64), 0.125, ws)
+    assert e.value.status == S.SD_ERR_INVALID_ARG
