@@ -56,7 +56,7 @@ template <int D> struct Lay {
     static constexpr int kMaxSlots = kSlots + 1;           // where no unit has a second row tile, its room too
     // full[max] empty[max] qfull qempty sfull[2] pfull[2][2] ofull[2] ofree[2]
     static constexpr int kBars = 2 * kMaxSlots + 2 + 2 + 4 + 2 + 2;
-    static constexpr int kOffMl = kOffBar + 8 * kBars + 8; // [2][128] max and sum of stream 1
+    static constexpr int kOffMl = kOffBar + 8 * kBars + 8; // [2][128] exchange between the streams
     static constexpr int kOffMisc = kOffMl + 2 * 128 * 4;
     static constexpr int kSmem = kOffMisc + 512 + 1024;    // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
@@ -166,7 +166,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     auto pfull_bar = [&](int i, int h) { return bar1 + 8u * (4 + 2 * i + h); };   // half h of P_i written (4 warps)
     auto ofull_bar = [&](int i) { return bar1 + 8u * (8 + i); };             // O_i complete for the unit
     auto ofree_bar = [&](int i) { return bar1 + 8u * (10 + i); };            // O_i read out (4 warps)
-    float *ml1 = reinterpret_cast<float *>(sbase + L::kOffMl);
+    float *xrow = reinterpret_cast<float *>(sbase + L::kOffMl);      // [2][128]: one value per stream and row
     Misc *misc = reinterpret_cast<Misc *>(sbase + L::kOffMisc);
     volatile int *abort_flag = &misc->abort_flag;
 
@@ -496,7 +496,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             const int tr = r / G;                      // token of the row within its tile
             VlWalk walk(pl);
             VlUnit u;
-            uint32_t sphase = 0, ophase = 0, ophase1 = 0;
+            uint32_t sphase = 0, ophase0 = 0, ophase1 = 0;
             bool have_ends = false;
             unsigned ring = 0;                         // tiles that went through the ring before this unit
             bool ok = true;
@@ -667,33 +667,33 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 ring += 2 * n;
                 float a0 = 1.f, a1 = 0.f;
                 if (!pair) {
-                    // join the two streams of the one row tile: stream 1 leaves its max and sum
-                    if (w == 1) {
-                        ml1[r] = m_used;
-                        ml1[128 + r] = l;
-                    }
+                    // join the two streams of the one row tile: they exchange the row's maximum, then
+                    // its sum, and each takes half of the columns of both accumulators
+                    xrow[128 * w + r] = m_used;
                     named_sync(1, 256);
-                    if (w == 0) {
-                        const float m1 = ml1[r], l1 = ml1[128 + r];
-                        const float m = fmaxf(m_used, m1);
-                        a0 = m_used == -INFINITY ? 0.f : ex2(m_used - m);
-                        a1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
-                        l = a0 * l + a1 * l1;
-                        m_used = m;
-                    }
+                    const float mo = xrow[128 * (w ^ 1) + r];
+                    const float m = fmaxf(m_used, mo), ref = m == -INFINITY ? 0.f : m;
+                    const float own = ex2(m_used - ref), other = ex2(mo - ref);
+                    l *= own;
+                    m_used = m;
+                    a0 = w == 0 ? own : other;
+                    a1 = w == 0 ? other : own;
+                    named_sync(2, 256);
+                    xrow[128 * w + r] = l;
+                    named_sync(1, 256);
+                    l += xrow[128 * (w ^ 1) + r];
                 }
-                if (pair ? (w == 0 ? had0 : had1) : (w == 0 && had0)) {
-                    ok = __all_sync(0xffffffffu, wait_bar(ofull_bar(w), ophase, abort_flag, p.fault)) && ok;
-                    ophase ^= 1u;
-                }
-                if (!pair && had1) {
-                    // both warpgroups follow stream 1's barrier, so that its phase stays known to each
-                    if (w == 0) ok = __all_sync(0xffffffffu, wait_bar(ofull_bar(1), ophase1, abort_flag, p.fault)) && ok;
-                    else ophase ^= 1u;
-                }
+                // each warpgroup follows both barriers' phases; past the exchange above neither can be a unit behind
+                if (pair ? n > 0 && w == 0 : had0)
+                    ok = __all_sync(0xffffffffu, wait_bar(ofull_bar(0), ophase0, abort_flag, p.fault)) && ok;
+                if (pair ? n > 0 && w == 1 : had1)
+                    ok = __all_sync(0xffffffffu, wait_bar(ofull_bar(1), ophase1, abort_flag, p.fault)) && ok;
+                if (had0) ophase0 ^= 1u;
                 if (had1) ophase1 ^= 1u;
                 tc_fence_after();
-                if ((pair || w == 0) && warp_live) {
+                if (warp_live) {
+                    const int c0 = pair ? 0 : w * (D / 64), c1 = pair ? D / 32 : c0 + D / 64;
+                    const uint32_t o0 = tmem + lane_off + 256u + (pair ? 128u * w : 0u);
                     const long prow = 128 * (pair ? w : 0) + r;
                     const long orow = (long)(u.row0 + tl) * p.Hq + u.g * G + (r - tr * G);
                     const bool dead = n <= 0;
@@ -712,10 +712,10 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     const float inv = write ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
                     // (a loop, not unrolled: the code that runs once per unit is fetched once)
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
+                    for (int c = c0; c < c1; ++c) {
                         uint32_t o[32];
                         if (!dead) {
-                            tmem_ld32_async(o_col + 32u * c, o);
+                            tmem_ld32_async(o0 + 32u * c, o);
                             tmem_ld_wait();
                             tmem_ld_bind(o);
                         }
@@ -723,7 +723,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
 #pragma unroll
                         for (int e = 0; e < 32; ++e) f[e] = dead ? 0.f : __uint_as_float(o[e]) * (a0 * inv);
                         if (!pair && had1) {
-                            tmem_ld32_async(o_col + 128u + 32u * c, o);
+                            tmem_ld32_async(o0 + 128u + 32u * c, o);
                             tmem_ld_wait();
                             tmem_ld_bind(o);
 #pragma unroll
@@ -769,7 +769,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             }
                         }
                     }
-                    if (row_ok && !write)
+                    if (row_ok && !write && (pair || w == 0))
                         __stcg(p.ml_part + slot * kVarlenTcRows + prow,
                                make_float2(ok ? m_used : -INFINITY, ok ? l : 0.f));
                 }
@@ -787,15 +787,12 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && n > 0) {
-                    if (pair) {
-                        mbar_arrive(ofree_bar(w));
-                    } else if (w == 0) {
-                        mbar_arrive(ofree_bar(0));
-                        if (had1) mbar_arrive(ofree_bar(1));
-                    }
+                if (pair) {
+                    if (lane == 0 && n > 0) mbar_arrive(ofree_bar(w));
+                } else {
+                    named_sync(2, 256);                // both warpgroups have read both accumulators
+                    if (lane == 0 && (w == 0 ? had0 : had1)) mbar_arrive(ofree_bar(w));
                 }
-                if (!pair) named_sync(2, 256);     // stream 1's max and sum have been read
             }
             // the softmax warps (they hold the registers) join the shared units
             if (!have_ends) asm volatile("bar.sync 14, 288;" ::: "memory");
