@@ -375,7 +375,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             umma_commit(sfull_bar(i));
                         }
                     };
-                    auto issue_pv = [&](int i, int slot, bool first) {
+                    auto issue_pv = [&](int i, int slot, bool first, int steps) {
                         const uint64_t vd = vd0 + (uint64_t)(slot * (L::kTile / 16));
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -385,6 +385,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             if (el) {
 #pragma unroll
                                 for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk) {
+                                    if (kSmall && kk >= steps) break;
                                     umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + vrow[kk], idO,
                                             (!first || kk > 0) ? 1u : 0u);
                                     if (kSmall)
@@ -408,6 +409,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         const int n = u.t1 - u.t0;
                         if (n <= 0) continue;
                         const bool pair = !kSmall && u.ntok > tpt;
+                        // the small form's second products stop at the step of 16 that holds the last key
+                        auto steps = [&](int j) { return kSmall ? (u.kv - (u.t0 + j) * 128 + 15) >> 4 : 8; };
                         ok = wait_bar(qfull_bar, qphase, abort_flag, p.fault);
                         if (!ok) break;
                         qphase ^= 1u;
@@ -425,7 +428,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 const RingPos vp = rp;
                                 rp.step(slots);
                                 if (j == 0) claim(0);
-                                issue_pv(0, vp.slot, j == 0);
+                                issue_pv(0, vp.slot, j == 0, 8);
                                 if (!ok) break;
                                 if (j + 1 < n) {
                                     wait_tile();
@@ -435,7 +438,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                     if (el) umma_commit(ofull_bar(0));
                                 }
                                 if (j == 0) claim(1);
-                                issue_pv(1, vp.slot, j == 0);
+                                issue_pv(1, vp.slot, j == 0, 8);
                                 if (!ok) break;
                                 if (el) umma_commit(empty_bar(vp.slot));
                                 if (j + 1 < n) {
@@ -461,7 +464,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 wait_tile();
                                 if (!ok) break;
                                 if (j < 2) claim(i);
-                                issue_pv(i, rp.slot, j < 2);
+                                issue_pv(i, rp.slot, j < 2, steps(j));
                                 if (!ok) break;
                                 if (el) umma_commit(empty_bar(rp.slot));
                                 rp.step(slots);
@@ -516,19 +519,18 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     ok = __all_sync(0xffffffffu, wait_bar(sfull_bar(w), sphase, abort_flag, p.fault)) && ok;
                     sphase ^= 1u;
                     tc_fence_after();
-                    if (warp_live && key0 + 128 > u.kv && (!pair || w == 0)) {
+                    if (key0 + 128 > u.kv && (!pair || w == 0)) {
                         // slots past the sequence may hold anything, and 0 times that is not 0:
-                        // one stream clears those rows of the last V tile before its product
+                        // one stream, all its warps, clears those rows of the last V tile that its
+                        // product reads before that begins
                         const int nk = min(la, n);
                         const unsigned idx = ring + nk + j + min(j, n - nk);
                         const int slot = (int)(idx % (unsigned)slots);
                         ok = __all_sync(0xffffffffu, wait_bar(full_bar(slot), (idx / (unsigned)slots) & 1u,
                                                                abort_flag, p.fault)) && ok;
                         uint8_t *vt = sbase + (sRing - base) + slot * L::kTile;
-                        const int v0 = u.kv - key0;
-                        // the live warps share the rows
-                        const int live = min(4, ((pair ? tpt : min(u.ntok, tpt)) * G + 31) / 32);
-                        for (int i = r; i < (128 - v0) * 8 * L::kHalves; i += 32 * live) {
+                        const int v0 = u.kv - key0, v1 = kSmall ? (v0 + 15) & ~15 : 128;
+                        for (int i = r; i < (v1 - v0) * 8 * L::kHalves; i += 128) {
                             const int row = v0 + i / (8 * L::kHalves), ch = i % (8 * L::kHalves);
                             const int in = row & (box - 1);
                             *reinterpret_cast<uint4 *>(vt + ((row - in) * L::kHalves + (ch >> 3) * box) * 128 +
@@ -536,8 +538,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                                 make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async_smem();
-                        // every live warp's rows, before any arrival lets the product start
-                        named_sync(3 + w, 32 * live);
+                        // every warp's rows, before any arrival lets the product start
+                        named_sync(3 + w, 128);
                     }
                     if (warp_live) {
                         uint32_t s[4][32];
