@@ -528,9 +528,13 @@ sd_status sd_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, c
  * Slots at and past kv_len[b] may hold anything.  Values inside a sequence are
  * taken to be finite: bf16 weights are 0 for masked positions, and 0 times a
  * non-finite value of a later position of the same tile is not 0.
- * bf16 pages of a multiple of 8 slots run on the tensor cores (the softmax
- * weights are rounded to bf16 for the second product); fp32, and other page
- * sizes, on CUDA cores.  One launch.
+ * bf16 over pages of a multiple of 8 slots runs on the tensor cores: the softmax
+ * weights enter the second product as one bf16 term, or, where max_q * Hq / Hkv
+ * <= 128, as two (2^-16 of each weight).  fp32, and other page sizes, run on CUDA
+ * cores.  sd_set_attention_path applies.  One launch.
+ * Deterministic: a call's result depends on its arguments alone.  How a
+ * sequence's keys are divided, and with it the last bits, depends on the lengths
+ * of the whole batch.
  *
  * workspace: at least the size below, zero-filled before the first call on it;
  * every call leaves its counters zero again (a call whose bounded wait gave up

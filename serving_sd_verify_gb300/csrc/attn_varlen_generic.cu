@@ -8,9 +8,11 @@
 // R / 16 rows x 4 keys of S = Q K^T from transposed tiles in shared memory,
 // the 16 threads of a row find its maximum and sum by shuffles, and the same
 // thread adds P V for its rows and D / 16 of the columns, O in registers.
-// Every number of S and P V costs R / 16 x 4 multiply-adds per pair of 16-byte
-// shared loads: with 64 rows the FMA pipe is the bound (half its rate), with
-// 16 the shared-memory reads of K and V, at about the rate HBM delivers them.
+// The keys lie transposed and swizzled in shared memory, the weights go over
+// them, and multiply-adds come two an instruction.  What bounds it: with 64 rows
+// the shared-memory reads that feed the FMA pipe (410 tokens of 64 heads over 544
+// keys, fp32: 394 us, 32 TFLOP/s), with 16 the latency of a tile's load, product
+// and softmax one after the other (16 rows of 4 heads over 527 keys: 16 us).
 #include "varlen.cuh"
 
 #include <math.h>
