@@ -718,3 +718,49 @@ def test_output_rows_on_16_byte_boundaries(S):
         S.sd_prompt_attention(dev[:, :8], dev[:, 8:10], dev[:, 10:], cumulative([150]).cuda(), 150,
                               buf[4:4 + 150 * 8 * 64].view(150, 8, 64), 0.125, ws)
     assert e.value.status == S.SD_ERR_INVALID_ARG
+
+
+def test_nothing_is_written_outside_the_buffers(S):
+    """Canary bytes around the output, the pools and the workspace of each call."""
+    PAD = 4096
+
+    def padded(shape, dtype, fill=0):
+        n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((PAD + n + (-n) % 256 + PAD,), 0xA5, dtype=torch.uint8, device="cuda")
+        t = buf[PAD:PAD + n].view(dtype).view(shape)
+        t.fill_(fill)
+        return t, (buf, n)
+
+    g = torch.Generator().manual_seed(14)
+    for dtype in (torch.bfloat16, torch.float32):
+        Hq, Hkv, D, page = 12, 4, 128, 24
+        q_lens, kv_lens = [3, 40, 0, 150], [3, 77, 5, 400]
+        n = sum(q_lens)
+        marks = []
+        pages = [padded((24, page, Hkv, D), dtype, 0.5) for _ in range(2)]
+        q_out, out = padded((n, Hq, D), dtype), padded((n, Hq, D), dtype)
+        size = S.sd_paged_attention_workspace_size(n, 4, 150, Hq, Hkv, D, 400, dt_code(S, dtype))
+        ws = padded((size,), torch.uint8)
+        marks += [m for _, m in (*pages, q_out, out, ws)]
+        table = torch.randperm(24, generator=g).to(torch.int32)
+        rows, at = torch.zeros(4, 17, dtype=torch.int32), 0
+        for b, m in enumerate(kv_lens):
+            c = -(-m // page)
+            rows[b, :c] = table[at:at + c]
+            at += c
+        x = randn(g, n, Hq + 2 * Hkv, D, dtype=dtype).cuda()
+        turns = S.sd_rotary_table(64, 1e4)[0].cuda()
+        cu, kv = cumulative(q_lens).cuda(), torch.tensor(kv_lens, dtype=torch.int32).cuda()
+        S.sd_rotary_append_paged(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], q_out[0], None, turns, cu, kv,
+                                 rows.cuda(), pages[0][0], pages[1][0])
+        pool = pages[0][0].clone(), pages[1][0].clone()
+        for path in (1, 2) if dtype == torch.bfloat16 else (1,):
+            S.sd_set_attention_path(path)
+            S.sd_paged_attention(q_out[0], pages[0][0], pages[1][0], rows.cuda(), cu, kv, 150, 400, out[0], 0.1, ws[0])
+            S.sd_prompt_attention(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cu, 150, out[0], 0.1, ws[0])
+        S.sd_rotary(out[0], out[0], torch.arange(n, dtype=torch.int32, device="cuda"), turns, layout="interleaved")
+        torch.cuda.synchronize()
+        assert torch.equal(pool[0], pages[0][0]) and torch.equal(pool[1], pages[1][0])
+        for buf, nb in marks:
+            assert bool((buf[:PAD] == 0xA5).all()) and bool((buf[PAD + nb:] == 0xA5).all())
+    assert S.sd_fault_word() == 0
