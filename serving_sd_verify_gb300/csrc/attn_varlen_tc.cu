@@ -162,11 +162,24 @@ __device__ __forceinline__ bool elect_one() {
 // block verification).  Those calls are bound by memory, so P goes into the
 // second product as two bf16 terms, to 2^-16 of each weight, and the second row
 // tile's room is a ring slot more.
-template <int D, bool kPaged, bool kSmall>
+// kFrom: where K and V are.  kPacked: the prompts' own rows.  kPages: a paged
+// cache.  kPages16: one at D = 128 that is copied 16 slots at a time, with both
+// 64-column blocks of those slots in one copy for K too.  K's 8-row groups then
+// lie in two evenly spaced sets, the first and the second of each 16, and the
+// scores come as two products of 64 columns: column c < 64 is key
+// 16 (c / 8) + c % 8 of the tile, column 64 + c the key 8 further on; P and V
+// follow that order.
+template <bool kSets> __device__ __forceinline__ constexpr int key_of(int c) {
+    return kSets ? 16 * ((c & 63) >> 3) + 8 * (c >> 6) + (c & 7) : c;
+}
+enum From { kPacked, kPages, kPages16 };
+template <int D, From kFrom, bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const VarlenParams p, const int tpt, const int box) {
     using L = Lay<D>;
+    constexpr bool kPaged = kFrom != kPacked, kSets = kFrom == kPages16;
+    static_assert(!kSets || D == 128, "one 64-column block lies evenly anyway");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t base = (raw_u32 + 1023u) & ~1023u;
@@ -278,7 +291,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             const int boxes = min(per_half, (u.kv - t * 128 + box - 1) / box);
                             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * L::kHalves));
                             __syncwarp();
-                            const bool both = is_v || box == 8;
+                            const bool both = kSets || is_v || box == 8;
                             const int i = lane % per_half, h = lane / per_half;
                             if (i < boxes && h < (both ? 1 : L::kHalves)) {
                                 const int key = t * 128 + i * box;
@@ -375,20 +388,34 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     const uint32_t eight = box == 8 ? L::kHalves : 1;
                     const uint32_t khalf = (box == 8 ? 1024 : 128 * 128) / 16;
                     const uint64_t qd0 = sw128_desc(sQ, 16, 1024), kd0 = sw128_desc(sRing, 16, 1024 * eight),
-                                   vd0 = sw128_desc(sRing, (uint32_t)box * 128, 1024 * eight);
+                                   vd0 = sw128_desc(sRing, (uint32_t)box * 128, kSets ? 4096 : 1024 * eight);
+                    const uint64_t ksets = sw128_desc(sRing, 16, 4096);       // a set's groups, one per 16 slots
                     uint32_t vrow[8];              // where the 16 keys of step kk begin in a V tile, in 16 bytes
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        vrow[kk] = (((16 * kk) & ~(box - 1)) * L::kHalves + ((16 * kk) & (box - 1))) * (128 / 16);
+                        vrow[kk] = kSets ? (kk & 3) * (8192 / 16) + (kk >> 2) * (1024 / 16)
+                                         : (((16 * kk) & ~(box - 1)) * L::kHalves + ((16 * kk) & (box - 1))) * (128 / 16);
                     auto issue_s = [&](int i, int qt, int slot) {
                         const uint64_t qd = qd0 + (uint64_t)(qt * (L::kTile / 16)),
                                        kd = kd0 + (uint64_t)(slot * (L::kTile / 16));
                         if (el) {
+                            if constexpr (kSets) {
+                                const uint64_t kb = ksets + (uint64_t)(slot * (L::kTile / 16));
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint64_t off = (kk & 3) * 2;
-                                umma_ss(tmem + 128u * i, qd + off + (kk >> 2) * (128 * 128 / 16),
-                                        kd + off + (kk >> 2) * khalf, idS, kk > 0 ? 1u : 0u);
+                                for (int set = 0; set < 2; ++set)
+#pragma unroll
+                                    for (int kk = 0; kk < D / 16; ++kk)
+                                        umma_ss(tmem + 128u * i + 64u * set,
+                                                qd + (kk & 3) * 2 + (kk >> 2) * (128 * 128 / 16),
+                                                kb + set * (1024 / 16) + (kk & 3) * 2 + (kk >> 2) * (2048 / 16),
+                                                idesc_bf16(128, 64, false), kk > 0 ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int kk = 0; kk < D / 16; ++kk) {
+                                    const uint64_t off = (kk & 3) * 2;
+                                    umma_ss(tmem + 128u * i, qd + off + (kk >> 2) * (128 * 128 / 16),
+                                            kd + off + (kk >> 2) * khalf, idS, kk > 0 ? 1u : 0u);
+                                }
                             }
                             umma_commit(sfull_bar(i));
                         }
@@ -403,7 +430,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             if (el) {
 #pragma unroll
                                 for (int kk = h ? kPFirst / 16 : 0; kk < (h ? 8 : kPFirst / 16); ++kk) {
-                                    if (kSmall && kk >= steps) break;
+                                    if (kSmall && (kSets ? 2 * (kk & 3) : kk) >= steps) continue;
                                     umma_ts(tmem + 256u + 128u * i, tmem + 128u * i + 8u * kk, vd + vrow[kk], idO,
                                             (!first || kk > 0) ? 1u : 0u);
                                     if (kSmall)
@@ -547,7 +574,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         ok = __all_sync(0xffffffffu, wait_bar(full_bar(slot), (idx / (unsigned)slots) & 1u,
                                                                abort_flag, p.fault)) && ok;
                         uint8_t *vt = sbase + (sRing - base) + slot * L::kTile;
-                        const int v0 = u.kv - key0, v1 = kSmall ? (v0 + 15) & ~15 : 128;
+                        const int v0 = u.kv - key0, v1 = !kSmall ? 128 : kSets ? (v0 + 31) & ~31 : (v0 + 15) & ~15;
                         for (int i = r; i < (v1 - v0) * 8 * L::kHalves; i += 128) {
                             const int row = v0 + i / (8 * L::kHalves), ch = i % (8 * L::kHalves);
                             const int in = row & (box - 1);
@@ -572,7 +599,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             for (int c = 0; c < 4; ++c)
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
-                                    if (32 * c + e >= vis) s[c][e] = 0xff800000u;
+                                    if (key_of<kSets>(32 * c + e) >= vis) s[c][e] = 0xff800000u;
                         }
                         const float2 qk2 = make_float2(qk, qk);
                         float2 ls[2], nm2;
@@ -874,7 +901,7 @@ int page_box(int page_size) {       // slots per copy: the largest power of two 
     return b;
 }
 
-template <int D, bool kPaged, bool kSmall>
+template <int D, From kFrom, bool kSmall>
 cudaError_t configure() {
     // the shared-memory limit, and the registers that the warps share out
     static std::atomic<bool> done[kMaxDevices];
@@ -883,16 +910,16 @@ cudaError_t configure() {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, attn_varlen_tc_kernel<D, kPaged, kSmall>);
+    e = cudaFuncGetAttributes(&a, attn_varlen_tc_kernel<D, kFrom, kSmall>);
     if (e != cudaSuccess) return e;
     if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;   // setmaxnreg would wait for registers that are not there
-    e = cudaFuncSetAttribute(attn_varlen_tc_kernel<D, kPaged, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_varlen_tc_kernel<D, kFrom, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Lay<D>::kSmem);
     if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
     return e;
 }
 
-template <int D, bool kPaged, bool kSmall>
+template <int D, From kFrom, bool kSmall>
 cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     const int G = p.Hq / p.Hkv, tpt = 128 / G;
     alignas(64) CUtensorMap mq, mk, mv;
@@ -906,12 +933,12 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     for (int i = 0; i < 2; ++i) {
         const void *t = i ? p.v : p.k;
         CUtensorMap *m = i ? &mv : &mk;
-        if (kPaged) {   // (d % 64, slot, d / 64, kv head, page): a copy per page and 64-column block
+        if (kFrom != kPacked) {   // (d % 64, slot, d / 64, kv head, page): a copy per page and 64-column block
             box_rows = page_box(p.page_size);
             const cuuint64_t dims[5] = {64, (cuuint64_t)p.page_size, (cuuint64_t)(D / 64), (cuuint64_t)p.Hkv,
                                         (cuuint64_t)p.n_pages};
             const cuuint64_t strides[4] = {(cuuint64_t)p.kv.s * 2, 128, (cuuint64_t)p.kv.h * 2, (cuuint64_t)p.kv.b * 2};
-            const cuuint32_t both = i == 1 || box_rows == 8 ? D / 64 : 1;
+            const cuuint32_t both = i == 1 || kFrom == kPages16 || box_rows == 8 ? D / 64 : 1;
             const cuuint32_t box[5] = {64, (cuuint32_t)box_rows, both, 1, 1};
             if (!encode_vl(m, t, 5, dims, strides, box)) return cudaErrorInvalidValue;
         } else {        // (d % 64, token, d / 64, kv head): one copy per tile
@@ -921,7 +948,7 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
             if (!encode_vl(m, t, 4, dims, strides, box)) return cudaErrorInvalidValue;
         }
     }
-    cudaError_t e = configure<D, kPaged, kSmall>();
+    cudaError_t e = configure<D, kFrom, kSmall>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -937,7 +964,7 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kPaged, kSmall>, mq, mk, mv, p, tpt, box_rows);
+    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kFrom, kSmall>, mq, mk, mv, p, tpt, box_rows);
 }
 
 }  // namespace
@@ -963,11 +990,13 @@ bool varlen_tc_supported(const VarlenParams &p) {
 cudaError_t launch_varlen_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     const bool small = p.max_q <= 128 / (p.Hq / p.Hkv);
     if (p.D == 128) {
-        if (p.table) return small ? launch_tc<128, true, true>(p, grid, st) : launch_tc<128, true, false>(p, grid, st);
-        return small ? launch_tc<128, false, true>(p, grid, st) : launch_tc<128, false, false>(p, grid, st);
+        if (!p.table) return small ? launch_tc<128, kPacked, true>(p, grid, st) : launch_tc<128, kPacked, false>(p, grid, st);
+        if (page_box(p.page_size) == 16)
+            return small ? launch_tc<128, kPages16, true>(p, grid, st) : launch_tc<128, kPages16, false>(p, grid, st);
+        return small ? launch_tc<128, kPages, true>(p, grid, st) : launch_tc<128, kPages, false>(p, grid, st);
     }
-    if (p.table) return small ? launch_tc<64, true, true>(p, grid, st) : launch_tc<64, true, false>(p, grid, st);
-    return small ? launch_tc<64, false, true>(p, grid, st) : launch_tc<64, false, false>(p, grid, st);
+    if (!p.table) return small ? launch_tc<64, kPacked, true>(p, grid, st) : launch_tc<64, kPacked, false>(p, grid, st);
+    return small ? launch_tc<64, kPages, true>(p, grid, st) : launch_tc<64, kPages, false>(p, grid, st);
 }
 
 }  // namespace sdv
