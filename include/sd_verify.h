@@ -625,7 +625,8 @@ int sd_set_attention_path(int path);
  * above) and its split count: for the CUDA-core kernel the key splits of every
  * (sequence, kv head); for the tensor-core kernel the CTAs of its grid, which
  * the kernel spreads over the (sequence, kv head, row block) units by their
- * lengths (a unit left with one CTA writes its output itself). */
+ * lengths (a unit left with one CTA writes its output itself); for the packed
+ * calls the CTAs of the grid. */
 int sd_last_attention_path(int *n_splits);
 
 /* How many kernels the last attention call on this thread launched: 1 when the

@@ -39,8 +39,8 @@
 // 1.45 ms.  One token over 25,119 takes 20 us for its 51 MB: 7.6 us of memory
 // time between 6 us of start (the plan, the page table, the first tile) and 6 us
 // of end (the last product, the join over 38 CTAs).  16 rows each of 8 sequences of
-// 4,096 to 32,768 take 53 us with pages of 64 slots and 64 with pages of 16, whose
-// copies cost about 40 clocks each besides their bytes.
+// 4,096 to 32,768 take 54 us with pages of 64 slots, 58 with pages of 16 and 70 with
+// pages of 8: a copy costs about 40 clocks besides the 4 of each 128-byte row.
 // Short units are bound by what surrounds their tiles: about 9,000 clocks a unit
 // against 2,800 a tile.
 //
