@@ -250,7 +250,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 uint32_t qphase = 0;
                 long loads = 0, units = 0;
                 bool ok = true;
-                // K and V that one unit alone reads leave L2 first (one token over 25,119: 24.9 -> 23.2 us);
+                // K and V that one unit alone reads leave L2 first (one token over 25,119: 22.2 -> 20.2 us);
                 // what several units read stays as usual
                 uint64_t once, again;
                 asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
@@ -286,8 +286,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             }
                         } else {
                             // V comes with both 64-column blocks of a page in one copy (a copy costs about
-                            // 40 clocks besides the 4 of each 128-byte row), and K where that leaves its
-                            // rows evenly spaced: pages of 8, or one 64-column block
+                            // 40 clocks besides the 4 of each 128-byte row), and K where its rows then lie
+                            // evenly enough for the products: copies of 8 slots, and of 16 (From)
                             const int boxes = min(per_half, (u.kv - t * 128 + box - 1) / box);
                             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * L::kHalves));
                             __syncwarp();
@@ -383,8 +383,8 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     };
                     // descriptors by their first tile's, moved on by whole 16-byte units
                     // K: its 8-row groups 1024 bytes apart, the 64-column blocks one after the other; from
-                    // pages of 8 slots the blocks alternate every group.  V: 64-column blocks alternate
-                    // every `box` rows (128 where K and V are not paged).
+                    // copies of 8 slots the blocks alternate every group, from copies of 16 as `From` says.
+                    // V: 64-column blocks alternate every `box` rows (128 where K and V are not paged).
                     const uint32_t eight = box == 8 ? L::kHalves : 1;
                     const uint32_t khalf = (box == 8 ? 1024 : 128 * 128) / 16;
                     const uint64_t qd0 = sw128_desc(sQ, 16, 1024), kd0 = sw128_desc(sRing, 16, 1024 * eight),
