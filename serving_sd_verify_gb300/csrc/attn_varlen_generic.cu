@@ -305,8 +305,8 @@ struct Launch {
 
 }  // namespace
 
-// 16 rows where they hold every sequence's rows of a kv head: nothing is then
-// computed for absent rows
+// 16 rows where they hold every sequence's rows of a kv head: a tile then costs a
+// quarter of the multiply-adds
 int varlen_generic_rows(const VarlenParams &p) { return (long)p.max_q * (p.Hq / p.Hkv) <= 16 ? 16 : 64; }
 
 int varlen_max_grid(int path, const VarlenParams &p) {

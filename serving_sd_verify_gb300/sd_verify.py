@@ -448,18 +448,15 @@ def sd_latent_compress(queries, features, out, ws, stream=None):
 # rotary positions, paged cache, packed attention
 # --------------------------------------------------------------------------
 
-def _on_current_device(*ts):
-    """Every tensor (None left out) on the current CUDA device: the calls use
-    its stream and its fault word.  Returns the device's number."""
-    dev = -1
-    for t in ts:
-        if t is not None:
-            d = t.get_device()       # -1 for a CPU tensor
-            if d != dev or d < 0:
-                if dev >= 0 or d < 0:
-                    raise ValueError("all tensors must be CUDA tensors on the current device")
-                dev = d
-    if dev != torch.cuda.current_device():
+def _on_current_device(first, *others):
+    """Every tensor (None left out of `others`) on the current CUDA device: the
+    calls use its stream and its fault word.  Returns the device's number."""
+    dev = first.get_device()         # -1 for a CPU tensor
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+            break
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("all tensors must be CUDA tensors on the current device")
     return dev
 
@@ -475,19 +472,24 @@ def _stream_on(stream, dev) -> int:
 def _paged_cache(k_pages, v_pages, page_table, cu_q, kv_len):
     """(the C struct, sequences, Hkv, D) of a cache and the lengths that go with it."""
     shape, strides = k_pages.shape, k_pages.stride()
-    if len(shape) != 4 or shape != v_pages.shape or strides != v_pages.stride() or k_pages.dtype != v_pages.dtype:
+    if len(shape) != 4 or v_pages.stride() != strides or v_pages.shape != shape or v_pages.dtype != k_pages.dtype:
         raise ValueError("k_pages and v_pages are [pages, page_size, Hkv, D] of equal shape, strides and dtype")
-    if strides[3] != 1:
+    pages, page_size, Hkv, D = shape
+    sp, ss, sh, sd = strides
+    if sd != 1:
         raise ValueError("the D axis of the cache must be contiguous")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table is int32 [B, columns] with contiguous rows")
+    B, cols = page_table.shape
+    row, col = page_table.stride()
+    if col != 1:
         raise ValueError("page_table is int32 [B, columns] with contiguous rows")
     _i32_cuda(cu_q, kv_len)
-    B, cols = page_table.shape
     if kv_len.dim() != 1 or cu_q.dim() != 1 or kv_len.numel() != B or cu_q.numel() != B + 1:
         raise ValueError("cu_q is [B + 1], kv_len [B], and page_table has B rows")
-    cache = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), Strides(strides[0], strides[1], strides[2]),
-                       page_table.data_ptr(), page_table.stride(0), cols, shape[0], shape[1])
-    return cache, B, shape[2], shape[3]
+    cache = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), (sp, ss, sh), page_table.data_ptr(), row, cols, pages,
+                       page_size)
+    return cache, B, Hkv, D
 
 
 def sd_rotary_table(rot_dim, theta, scaling="none", factor=1.0, original_max=0, low=1.0, high=32.0):
@@ -534,7 +536,7 @@ def sd_rotary_append_paged(q, k, v, q_out, positions, turns, cu_q, kv_len, page_
     equal strides; positions int32 [N] or None; cu_q int32 [B + 1]; kv_len
     int32 [B]; page_table int32 [B, columns]; k_pages, v_pages [pages,
     page_size, Hkv, D]."""
-    dev = _on_current_device(q, k, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages)
+    dev = _on_current_device(k, q, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages)
     shape, strides = k.shape, k.stride()
     N, Hkv, D = shape
     lay = _rope_args(turns, positions, N, layout)
