@@ -497,8 +497,10 @@ typedef struct {
  *   positions  device int32 [N], or NULL: each token's cache position
  *   tokens of one call must not share a cache position (two sequences that
  *   share a page share only what was written before)
- * Rows from cu_q[B] on and all other slots are left as they were.  A token
- * whose position is negative (kv_len < q_len) is not written and sets bit 7. */
+ * Rows from cu_q[B] on and all other slots are left as they were.  Offsets are
+ * clamped as above; a length is not: a token whose position is negative
+ * (kv_len < q_len) or behind the table's last slot is not written, and every
+ * length that is none sets bit 7, that of a sequence without new tokens too. */
 sd_status sd_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, const void *k, const void *v,
                                  int64_t kv_tok, int64_t kv_head, void *q_out, const int32_t *positions,
                                  const uint64_t *turns, float magnitude, int rot_dim, sd_rope_layout layout,

@@ -80,12 +80,10 @@ __device__ long append_slot(const RopeParams &p, int n, int &pos) {
         if (p.cu[mid] <= n) lo = mid;
         else hi = mid - 1;
     }
-    const int a = p.cu[lo], e = p.cu[lo + 1];
-    if (n < a || n >= e) {      // behind the last sequence (or an offset that is no offset)
-        if (e > p.N || a < 0) set_fault(p.fault, FAULT_BAD_LENGTH);
-        return -2;
-    }
-    const long ps = (long)p.kv_len[lo] - (e - a) + (n - a);
+    // clamped as the attention clamps them, so that a bad offset puts its tokens where the attention looks
+    const int c0 = max(0, min(p.cu[lo], p.N)), c1 = max(c0, min(p.cu[lo + 1], p.N));
+    if (n < c0 || n >= c1) return -2;              // behind the last sequence
+    const long ps = (long)p.kv_len[lo] - (c1 - c0) + (n - c0);
     pos = (int)ps;
     if (ps < 0 || ps >= (long)p.table_cols * p.page_size) {
         set_fault(p.fault, FAULT_BAD_LENGTH);
@@ -98,6 +96,14 @@ __device__ long append_slot(const RopeParams &p, int n, int &pos) {
         return -1;
     }
     return (long)pg * p.pages.b + (long)((unsigned)ps - col * (unsigned)p.page_size) * p.pages.s;
+}
+
+// Sequence b's offsets and length, reported where they are none: by threads of
+// their own, since a token meets only its own sequence's.
+__device__ __forceinline__ void append_check(const RopeParams &p, int b) {
+    const int a = p.cu[b], e = p.cu[b + 1], len = p.kv_len[b];
+    if (a < 0 || a > p.N || e < a || e > p.N || len < 0 || (long)len > (long)p.table_cols * p.page_size)
+        set_fault(p.fault, FAULT_BAD_LENGTH);
 }
 
 // q and the remainder of a / b, in 32 bits where a fits (a 64-bit division is a
@@ -116,14 +122,20 @@ __device__ __forceinline__ long divide(long a, int b, int &rem) {
 // One thread: one chunk of a token for up to kHeads heads.  A chunk is NP
 // pairs (two vectors of V in the half layout, one in the interleaved), or V
 // elements past the rotated ones, which are copied.  V = 1: single elements.
-// Chunks of x and k come first, then the values' (copied whole).
+// Chunks of x and k come first, then the values' (copied whole).  Of an append,
+// the first `checks` CTAs look over the offsets and lengths instead.
 template <typename T, int V, bool kInter, bool kAppend>
 __global__ void __launch_bounds__(kRopeThreads, 6)
 rope_kernel(const RopeParams p, const int rot_chunks, const int chunks, const int groups, const int val_chunks,
-            const int val_groups, const long items, const long val_items) {
+            const int val_groups, const long items, const long val_items, const int checks) {
     constexpr int NP = kInter ? (V > 1 ? V / 2 : 1) : V;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long id = (long)blockIdx.x * kRopeThreads + threadIdx.x;
+    if (kAppend && (int)blockIdx.x < checks) {
+        const int b = (int)blockIdx.x * kRopeThreads + (int)threadIdx.x;
+        if (b < p.B) append_check(p, b);
+        return;
+    }
+    const long id = (long)((int)blockIdx.x - (kAppend ? checks : 0)) * kRopeThreads + threadIdx.x;
     const T *x = static_cast<const T *>(p.x);
     T *y = static_cast<T *>(p.y);
     if (id < items) {
@@ -231,7 +243,8 @@ cudaError_t launch_one(const RopeParams &p, cudaStream_t st) {
     const int val_chunks = p.D / V, val_groups = (p.Hk + kHeads - 1) / kHeads;
     const long items = (long)p.N * groups * chunks;
     const long val_items = kAppend ? (long)p.N * val_groups * val_chunks : 0;
-    const long blocks = (items + val_items + kRopeThreads - 1) / kRopeThreads;
+    const int checks = kAppend ? (p.B + kRopeThreads - 1) / kRopeThreads : 0;    // CTAs that look over the sequences
+    const long blocks = checks + (items + val_items + kRopeThreads - 1) / kRopeThreads;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
@@ -243,7 +256,7 @@ cudaError_t launch_one(const RopeParams &p, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, rope_kernel<T, V, kInter, kAppend>, p, rot_chunks, chunks, groups, val_chunks,
-                              val_groups, items, val_items);
+                              val_groups, items, val_items, checks);
 }
 
 template <typename T, int V>

@@ -1,0 +1,78 @@
+"""Guards of the paged-cache calls that well-formed input never meets: packed
+offsets that are none, against the reading the header gives them."""
+import pytest
+import torch
+
+from test_gpu_paged import BAD_LENGTH, Pool, S, _clean, check_rope, randn, rope_ref  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+# --------------------------------------------------------------------------
+# the append
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("positions", [False, True])
+@pytest.mark.parametrize("N,cu,kv,tokens", [
+    # `tokens`: first row, rows and first cache position of each sequence, offsets clamped to [0, N]
+    (8, [0, 50], [60], [(0, 8, 52)]),                              # past N
+    (8, [0, 4, 100], [20, 200], [(0, 4, 16), (4, 4, 196)]),
+    (8, [-3, 5], [20], [(0, 5, 15)]), (5, [-3, 5], [20], [(0, 5, 15)]),      # negative
+    (25, [0, 30, 21], [40, 50], [(0, 25, 15)]),                    # past N, then decreasing
+    (8, [0, 8, 4], [30, 30], [(0, 8, 22)]),                        # decreasing where no token looks
+])
+def test_append_clamps_offsets_and_reports_them(S, dtype, positions, N, cu, kv, tokens):
+    g = torch.Generator().manual_seed(N + len(cu))
+    Hq, Hkv, D, page, R = 3, 2, 64, 16, 64
+    pool = Pool(g, [208] * len(kv), page, Hkv, D, dtype, fill=0.25)
+    kp, vp, table = pool.cuda()
+    x = randn(g, N, Hq + 2 * Hkv, D, dtype=dtype)
+    dev = x.cuda()
+    turns = S.sd_rotary_table(R, 1e4)[0].cuda()
+    pos = torch.arange(N, dtype=torch.int32) * 5 + 3
+    qo = torch.full((N, Hq, D), 9.0, dtype=dtype, device="cuda")
+    S.sd_rotary_append_paged(dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:], qo, pos.cuda() if positions else None,
+                             turns, i32(*cu), i32(*kv), table, kp, vp)
+    torch.cuda.synchronize()
+    assert S.sd_fault_word() == BAD_LENGTH
+    kc, vc, qc = kp.cpu(), vp.cpu(), qo.cpu()
+    kept = torch.ones(kc.shape[:2], dtype=torch.bool)
+    mine = torch.zeros(N, dtype=torch.bool)
+    for b, (row, n, first) in enumerate(tokens):
+        rows, at = slice(row, row + n), torch.arange(first, first + n)
+        pg, sl = pool.table[b, at // page].long(), at % page
+        kept[pg, sl] = False
+        mine[rows] = True
+        turn = pos[rows] if positions else at
+        check_rope(kc[pg, sl], *rope_ref(x[rows, Hq:Hq + Hkv], turn, R, 1e4, "half"), dtype)
+        assert torch.equal(vc[pg, sl], x[rows, Hq + Hkv:])
+        if cu[-1] >= N or row + n <= cu[-1]:       # queries behind cu_q[B] stay
+            check_rope(qc[rows], *rope_ref(x[rows, :Hq], turn, R, 1e4, "half"), dtype)
+    assert bool((kc[kept] == 0.25).all()) and bool((vc[kept] == 0.25).all())
+    assert bool((qc[~mine] == 9.0).all())
+
+
+def test_append_reports_lengths_of_idle_sequences(S):
+    """Each sequence's length is looked over, by itself and among hundreds, its tokens present or not."""
+    g = torch.Generator().manual_seed(1)
+    for B in (1, 3, 129, 700):
+        pool = Pool(g, [16] * B, 16, 1, 64, torch.bfloat16, fill=0.25)
+        kp, vp, table = pool.cuda()
+        table.clamp_(min=0)
+        x = randn(g, 1, 1, 64, dtype=torch.bfloat16).cuda()
+        turns = S.sd_rotary_table(64, 1e4)[0].cuda()
+        cu = torch.zeros(B + 1, dtype=torch.int32)
+        cu[-1] = 1                                 # the last sequence's one token
+        for bad in (None, -1, 33):                 # two pages of 16 in the table
+            for at in {0, B // 2, B - 1}:
+                kv = torch.full((B,), 16, dtype=torch.int32)
+                if bad is not None:
+                    kv[at] = bad
+                S.sd_rotary_append_paged(None, x, x, None, None, turns, cu.cuda(), kv.cuda(), table, kp, vp)
+                torch.cuda.synchronize()
+                assert S.sd_fault_word() == (0 if bad is None else BAD_LENGTH)
