@@ -1007,7 +1007,7 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     if (!p.fault) return fail(SD_ERR_CUDA, "no CUDA device / fault word unavailable");
     varlen_units(p, path);
     p.line_shift = 0;
-    while (ldexp(varlen_line(p), -p.line_shift) > 2.1e9) ++p.line_shift;
+    while (ldexp(varlen_line(p), -p.line_shift) > (double)kVarlenLine) ++p.line_shift;
     if (p.fixed >> p.line_shift < 1)      // every unit keeps a length
         return fail(SD_ERR_UNSUPPORTED, "tokens times heads times keys exceed one call");
     p.min_share = std::max(1, p.min_share >> p.line_shift);

@@ -131,6 +131,7 @@ constexpr int kVarlenTcFixed = 448, kVarlenTcMinShare = 440, kVarlenTcGroup = 4;
 constexpr int kVarlenGenFixed = 64, kVarlenGenMinShare = 64, kVarlenGenGroup = 1;
 constexpr int kVarlenMaxKv = 1 << 26;   // keys of a sequence
 constexpr int kVarlenMaxGrid = 1024;
+constexpr long long kVarlenLine = 2100000000;   // the longest work line, after its shift
 bool varlen_tc_supported(const VarlenParams &p);
 int varlen_generic_rows(const VarlenParams &p);        // rows per unit of the CUDA-core kernel
 int varlen_max_grid(int path, const VarlenParams &p);  // its CTAs that are resident at once (0: none)

@@ -145,14 +145,19 @@ __device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const V
 
 // The share of CTA `c` (one full warp).  The code runs once per CTA, so it is
 // kept short: most of its time is instruction fetch.  The line's length stays
-// below 2^31 (the host picks line_shift by its bounds); offsets that are no
-// offsets could exceed it and then nothing is computed.
+// within kVarlenLine (the host picks line_shift by its bounds); offsets that are
+// no offsets (sequences that overlap) could exceed it and wrap the 32-bit sums,
+// so the same sum is held of the lengths' high bits, each shifted before it is
+// added, and where that is too large nothing is computed.
 // Up to 32 sequences a lane holds one each.  More go in blocks of 32 whose
 // lengths the lanes hold (32 blocks at a time), so that only the two blocks in
 // which the share begins and ends are read again.
 __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
     const int lane = threadIdx.x & 31;
     constexpr unsigned kAll = 0xffffffffu;
+    constexpr int kHigh = 8;
+    // what the shifts drop, 65,535 sequences' at most, does not carry a line past 2^31
+    static_assert(kVarlenLine + 65536ll * (1 << kHigh) < (1ll << 31), "prefix sums in 32 bits");
     VlPlan pl = {};
     VlSeq s = {};
     unsigned w = 0, total = 0, coarse = 0;
@@ -174,14 +179,15 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
         return e;
     };
     // the lengths of blocks s0 / 32 .. s0 / 32 + 31, one per lane
-    auto blocks = [&](int s0, bool report) {
+    auto blocks = [&](int s0, bool first) {
         unsigned mine = 0;
 #pragma unroll 4
         for (int k = 0; k < 32; ++k) {
             const int b0 = s0 + 32 * k;
             if (b0 >= p.B) break;
-            const unsigned t = __reduce_add_sync(kAll, read(b0 + lane, report));
+            const unsigned t = __reduce_add_sync(kAll, read(b0 + lane, first && c == 0));
             if (lane == k) mine = t;
+            if (first) coarse = min(coarse + __reduce_add_sync(kAll, w >> kHigh), 1u << 30);   // below 2^31
         }
         return mine;
     };
@@ -189,17 +195,16 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
     if (p.B <= 32) {
         held = read(lane, c == 0);
         total = __reduce_add_sync(kAll, held);
-        coarse = __reduce_add_sync(kAll, held >> 8);
+        coarse = __reduce_add_sync(kAll, held >> kHigh);
     } else {
 #pragma unroll 1
         for (int s0 = 0; s0 < p.B; s0 += 1024) {
-            held = blocks(s0, c == 0);
+            held = blocks(s0, true);
             total += __reduce_add_sync(kAll, held);
-            coarse = min(coarse + __reduce_add_sync(kAll, held >> 8), 1u << 30);
         }
     }
     pl.total = (int)total;
-    if (coarse >= (1u << 23) - 1024u) {
+    if (coarse > (unsigned)(kVarlenLine >> kHigh)) {
         if (c == 0 && lane == 0) set_fault(p.fault, FAULT_BAD_LENGTH);
         pl.total = 0;
     }

@@ -76,3 +76,38 @@ def test_append_reports_lengths_of_idle_sequences(S):
                 S.sd_rotary_append_paged(None, x, x, None, None, turns, cu.cuda(), kv.cuda(), table, kp, vp)
                 torch.cuda.synchronize()
                 assert S.sd_fault_word() == (0 if bad is None else BAD_LENGTH)
+
+
+# --------------------------------------------------------------------------
+# attention
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,path", [(torch.bfloat16, 2), (torch.bfloat16, 1), (torch.float32, 1)])
+def test_overlapping_sequences_past_the_work_line_are_refused(S, dtype, path):
+    """64 sequences, every other one all of 32,768 rows over 40,000 keys: far more work than a call's
+    line holds, and what 32 bits leave of its sum is not.  Nothing is computed; the next call on the
+    same workspace is exact."""
+    N, B, Hq, Hkv, D, page = 32768, 64, 64, 8, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(N, Hq, D, generator=g, device="cuda").to(dtype)
+    kp, vp = (torch.randn(8, page, Hkv, D, generator=g, device="cuda").to(dtype) for _ in range(2))
+    table = torch.arange(B * 625, device="cuda").remainder(8).to(torch.int32).view(B, 625)
+    out = torch.full((N, Hq, D), 7.0, dtype=dtype, device="cuda")
+    ws = S.workspace(S.sd_paged_attention_workspace_size(N, B, N, Hq, Hkv, D, 40000, S._dt(q)))
+    S.sd_set_attention_path(path)
+    args = (N, 40000, out, D ** -0.5, ws)
+    small = i32(*([0, 3] + [3] * (B - 2) + [10])), torch.full((B,), 300, dtype=torch.int32, device="cuda")
+    S.sd_paged_attention(q, kp, vp, table, *small, *args)
+    torch.cuda.synchronize()
+    good = out[:10].clone()
+    assert S.sd_fault_word() == 0 and not bool((good == 7.0).all())
+    out.fill_(7.0)
+    for causal in (False, True):
+        S.sd_paged_attention(q, kp, vp, table, i32(*([0, N] * (B // 2) + [0])),
+                             torch.full((B,), 40000, dtype=torch.int32, device="cuda"), *args, causal=causal)
+        torch.cuda.synchronize()
+        assert S.sd_fault_word() == BAD_LENGTH
+        assert bool((out == 7.0).all())
+    S.sd_paged_attention(q, kp, vp, table, *small, *args)
+    torch.cuda.synchronize()
+    assert S.sd_fault_word() == 0 and torch.equal(out[:10], good)
