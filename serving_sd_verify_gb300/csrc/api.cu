@@ -951,13 +951,16 @@ int varlen_grid(const VarlenParams &p, int cap) {
     return (int)std::max(1.0, std::min((double)std::min(cap, kVarlenMaxGrid), varlen_line(p) / p.min_share + 1.0));
 }
 
+// The counters' room is that of the largest grid: a workspace serves calls of
+// different grids one after the other, and what one leaves in its partials must
+// not lie where the next one counts.
 struct VarlenLayout {
     size_t ctr, o, ml, total;
 };
 VarlenLayout varlen_layout(int grid, int rows, int D) {
     VarlenLayout l;
     l.ctr = kHeader;
-    l.o = l.ctr + align_up((size_t)grid * 4, 256);
+    l.o = l.ctr + align_up((size_t)kVarlenMaxGrid * 4, 256);
     l.ml = l.o + align_up((size_t)2 * grid * rows * D * 4, 256);
     l.total = l.ml + align_up((size_t)2 * grid * rows * 8, 256);
     return l;

@@ -111,3 +111,48 @@ def test_overlapping_sequences_past_the_work_line_are_refused(S, dtype, path):
     S.sd_paged_attention(q, kp, vp, table, *small, *args)
     torch.cuda.synchronize()
     assert S.sd_fault_word() == 0 and torch.equal(out[:10], good)
+
+
+def counters(S, ws):
+    """The counters of a call's whole grid, which it leaves at zero."""
+    n = S.sd_last_attention_path()[1]
+    assert 1 <= n <= 1024
+    return ws[256:256 + 4 * n].view(torch.int32)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_calls_of_different_grids_share_a_workspace(S, D):
+    """One CTA, a few, and as many as there are, on both paths and in both types, one after the other on
+    one workspace: each as on a workspace of its own, with every counter of its grid back at zero."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    Hq, Hkv, page = 8, 2, 16
+    shapes = [([1], [1]), ([40, 3], [300, 20]), ([1, 16, 700, 2], [9000, 3000, 2000, 40]), ([2], [60]), ([1] * 90, [500] * 90)]
+    size = max(S.sd_paged_attention_workspace_size(sum(a), len(a), max(a), Hq, Hkv, D, max(b), t)
+               for a, b in shapes for t in (S.SD_BF16, S.SD_FP32))
+    shared = S.workspace(size)
+    calls = []
+    for dtype, path in ((torch.bfloat16, 2), (torch.bfloat16, 1), (torch.float32, 1)):
+        for q_lens, kv_lens in shapes:
+            n, B, cols = sum(q_lens), len(q_lens), -(-max(kv_lens) // page)
+            kp, vp = (torch.randn(cols + 5, page, Hkv, D, generator=g, device="cuda").to(dtype) for _ in range(2))
+            table = (torch.arange(B * cols, device="cuda") * 7).remainder(cols + 5).to(torch.int32).view(B, cols)
+            q = torch.randn(n, Hq, D, generator=g, device="cuda").to(dtype)
+            out = torch.empty_like(q)
+            cu = torch.tensor([0] + q_lens).cumsum(0).to(torch.int32).cuda()
+            args = (q, kp, vp, table, cu, i32(*kv_lens), max(q_lens), max(kv_lens), out, D ** -0.5)
+            own = S.workspace(size)
+            S.sd_set_attention_path(path)
+            S.sd_paged_attention(*args, own)
+            torch.cuda.synchronize()
+            assert not counters(S, own).any()
+            calls.append((path, args, out.clone()))
+    grids = set()
+    for path, args, want in calls + calls[::-1]:
+        S.sd_set_attention_path(path)
+        args[8].fill_(0)
+        S.sd_paged_attention(*args, shared)
+        torch.cuda.synchronize()
+        grids.add(S.sd_last_attention_path()[1])
+        assert torch.equal(args[8], want)
+        assert not shared[256:256 + 4 * 1024].any()
+    assert S.sd_fault_word() == 0 and min(grids) < 10 and max(grids) > 152

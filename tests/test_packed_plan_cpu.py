@@ -93,3 +93,13 @@ def test_random_batches_are_dealt_out_exactly(replay, seed):
                            shift=rng.choice([-1, -1, rng.randint(1, 8 if tensor else 6)])))
     for c, r in zip(cases, replay(cases)):
         assert r["what"] in ("ok", "refused") and r["fault"] == 0, (r, c[:120])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_counters_room_is_the_same_for_every_grid(D):
+    """A workspace holds 1,024 counters in front of the partials, whatever the call's grid: the rest of a
+    large call's is whole pairs of slots, 256 rows of D + 2 floats each (or four of 64)."""
+    from serving_sd_verify_gb300 import build, sd_verify
+    build.build()
+    size = sd_verify.sd_paged_attention_workspace_size(4096, 64, 4096, 28, 4, D, 65536)
+    assert (size - 256 - 4 * 1024) % (2 * 256 * (D + 2) * 4) == 0
