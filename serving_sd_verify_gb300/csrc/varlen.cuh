@@ -147,8 +147,8 @@ __device__ __forceinline__ VlPos vl_locate(const VarlenParams &p, int b, const V
 // kept short: most of its time is instruction fetch.  The line's length stays
 // within kVarlenLine (the host picks line_shift by its bounds); offsets that are
 // no offsets (sequences that overlap) could exceed it and wrap the 32-bit sums,
-// so the same sum is held of the lengths' high bits, each shifted before it is
-// added, and where that is too large nothing is computed.
+// so the lengths' high bits are summed as well, each shifted before it is added,
+// and where that is too large nothing is computed.
 // Up to 32 sequences a lane holds one each.  More go in blocks of 32 whose
 // lengths the lanes hold (32 blocks at a time), so that only the two blocks in
 // which the share begins and ends are read again.
@@ -179,15 +179,15 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
         return e;
     };
     // the lengths of blocks s0 / 32 .. s0 / 32 + 31, one per lane
-    auto blocks = [&](int s0, bool first) {
+    auto blocks = [&](int s0, bool report) {
         unsigned mine = 0;
 #pragma unroll 4
         for (int k = 0; k < 32; ++k) {
             const int b0 = s0 + 32 * k;
             if (b0 >= p.B) break;
-            const unsigned t = __reduce_add_sync(kAll, read(b0 + lane, first && c == 0));
+            const unsigned t = __reduce_add_sync(kAll, read(b0 + lane, report));
             if (lane == k) mine = t;
-            if (first) coarse = min(coarse + __reduce_add_sync(kAll, w >> kHigh), 1u << 30);   // below 2^31
+            coarse = min(coarse + (w >> kHigh), 1u << 26);     // this lane's sequences'
         }
         return mine;
     };
@@ -199,9 +199,10 @@ __device__ __forceinline__ VlPlan vl_plan(const VarlenParams &p, int c) {
     } else {
 #pragma unroll 1
         for (int s0 = 0; s0 < p.B; s0 += 1024) {
-            held = blocks(s0, true);
+            held = blocks(s0, c == 0);
             total += __reduce_add_sync(kAll, held);
         }
+        coarse = __reduce_add_sync(kAll, coarse);
     }
     pl.total = (int)total;
     if (coarse > (unsigned)(kVarlenLine >> kHigh)) {
