@@ -420,12 +420,22 @@ size_t sd_latent_compress_workspace_size(int frames, int N, int Cq, int d);
  *   SD_ROPE_YARN    SD_ROPE_PARTS, and the magnitude m = 0.1 ln(factor) + 1
  *                   ("YaRN: Efficient Context Window Extension of Large
  *                   Language Models"); m = 1 in every other kind
+ * The ramp of SD_ROPE_PARTS and SD_ROPE_YARN is that paper's, linear in a pair's
+ * turns.  Many models with "yarn" in their configuration were trained with
+ * another: linear in the pair's index i, between the (rounded) indices at which
+ * the turns are `high` and `low`.  Their blended frequencies differ (by tens of
+ * percent in the middle of the ramp); for such a model fill the words with its
+ * own w_i, as below.
  *
  * sd_rotary_table (host only; no GPU call) writes R/2 words, turns[i] =
- * round(2^64 frac(w_i / (2 pi))), and the magnitude.  The kernels multiply a
- * word by the position in 64-bit integers, which drops whole turns exactly:
- * the angle of any int32 position is right to position * 2^-54 turns plus
- * 2^-32, whatever its size.
+ * floor(2^64 frac(w_i / (2 pi))), and the magnitude.  The kernels take any
+ * words and multiply one by the position p in 64-bit integers, which drops whole
+ * turns exactly.  An angle is therefore right, at any int32 position, to
+ *   |p| (e w_i / (2 pi) + 2^-64) + 2^-28 + 2^-33 turns:
+ * e = 2^-49 is the fp64 arithmetic behind a word (theta, for SD_ROPE_NTK the
+ * stretched one, below 10^10; for SD_ROPE_PARTS and SD_ROPE_YARN
+ * 2^-49 (2 + factor low / (high - low))), 2^-28 the fp32 remainder within an
+ * eighth of a turn.
  * ------------------------------------------------------------------------ */
 typedef enum { SD_ROPE_HALF = 0, SD_ROPE_INTERLEAVED = 1 } sd_rope_layout;
 
@@ -523,7 +533,9 @@ sd_status sd_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, c
  *         softmax, one rounding at the end), overlapping no input; rows from
  *         cu_q[B] on are left as they were
  *   max_q, max_kv  host upper bounds of the sequences' new tokens and kv_len;
- *         N, max_q and max_kv at most 2^26
+ *         N, max_q and max_kv at most 2^26.  Bounds whose product
+ *         Hkv (N / tokens of a unit + B) max_kv passes 5e11 (1e11 on CUDA cores)
+ *         return SD_ERR_UNSUPPORTED
  *   query head h reads kv head h / (Hq / Hkv); Hq / Hkv <= 64; D in {64, 128}
  *   scale > 0, finite; B in [1, 65535]; all bases 16-byte aligned, all strides
  *   multiples of 16 bytes
@@ -532,8 +544,11 @@ sd_status sd_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, c
  * non-finite value of a later position of the same tile is not 0.
  * bf16 over pages of a multiple of 8 slots runs on the tensor cores: the softmax
  * weights enter the second product as one bf16 term, or, where max_q * Hq / Hkv
- * <= 128, as two (2^-16 of each weight).  fp32, and other page sizes, run on CUDA
- * cores.  sd_set_attention_path applies.  One launch.
+ * <= 128, as two (2^-16 of each weight).  max_q decides it for the whole call: a
+ * decoding sequence beside a long one, or under a loose max_q, gets one term, and
+ * a call that decodes or verifies only is better off with a tight bound.  fp32,
+ * and other page sizes, run on CUDA cores.  sd_set_attention_path applies.  One
+ * launch.
  * Deterministic: a call's result depends on its arguments alone.  How a
  * sequence's keys are divided, and with it the last bits, depends on the lengths
  * of the whole batch.
@@ -654,8 +669,9 @@ int sd_set_sample_path(int path);
 int sd_last_sample_path(void);
 
 /* Failure-detection test hook, process-wide.  The in-kernel barriers (the
- * tensor-core attention's merge of a unit's splits, the one-launch sampled
- * rule's grid and sequence barriers) wait for `extra_arrivals` more CTAs than
+ * tensor-core attention's merge of a unit's splits, the join of the packed
+ * attention's shared units, the one-launch sampled rule's grid and sequence
+ * barriers) wait for `extra_arrivals` more CTAs than
  * the grid has, giving up after `limit_ns` (0, or more than 2 s: 2 s, the
  * normal limit).  A call made meanwhile sets fault bit 3 (a bounded wait gave
  * up), returns with undefined outputs and leaves its counters zero, so the

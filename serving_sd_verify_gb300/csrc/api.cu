@@ -932,7 +932,7 @@ void varlen_units(VarlenParams &p, int path) {
     const int G = p.Hq / p.Hkv;
     p.rows = path >= 2 ? kVarlenTcRows : varlen_generic_rows(p);
     p.tb = path >= 2 ? 2 * (128 / G) : p.rows / G;
-    if (p.tb < 1) p.tb = 1;      // 64 rows, a group of at most 64
+    if (p.tb < 1) p.tb = 1;      // max_q = 0: 16 rows, whatever the group (and no units)
     p.fixed = path >= 2 ? kVarlenTcFixed : kVarlenGenFixed;
     p.group = path >= 2 ? kVarlenTcGroup : kVarlenGenGroup;
     p.min_share = path >= 2 ? kVarlenTcMinShare : kVarlenGenMinShare;

@@ -33,7 +33,7 @@ constexpr int kMaxHeadBytes = 512;  // bytes of one (position, kv head) row the 
 constexpr unsigned long long kBarrierWaitNs = 2000000000ull;   // an in-kernel barrier wait gives up after 2 s
 
 // Failure-detection test hook (sd_set_wait_test): the in-kernel barriers
-// (attention merge, one-launch sampled rule) wait for `extra` arrivals more
+// (attention merge, packed attention's join, one-launch sampled rule) wait for `extra` arrivals more
 // than exist, giving up after `limit_ns`.  {0, kBarrierWaitNs} normally.
 struct WaitTest {
     unsigned int extra;
