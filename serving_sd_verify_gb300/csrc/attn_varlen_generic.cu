@@ -12,7 +12,9 @@
 // them, and multiply-adds come two an instruction.  What bounds it: with 64 rows
 // the shared-memory reads that feed the FMA pipe (410 tokens of 64 heads over 544
 // keys, fp32: 394 us, 32 TFLOP/s), with 16 the latency of a tile's load, product
-// and softmax one after the other (16 rows of 4 heads over 527 keys: 16 us).
+// and softmax one after the other (16 rows of 4 heads over 527 keys: 14 to 18 us).
+// Causal fp32 prompts of 2,048 and 8,192 tokens, 28 / 4 heads of 128: 0.82 and 11.9
+// ms, 37 and 41 TFLOP/s.
 #include "varlen.cuh"
 
 #include <math.h>

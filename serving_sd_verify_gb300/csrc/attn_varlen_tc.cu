@@ -31,15 +31,19 @@
 // P_i overlays the first 64 columns of S_i (its second term, in the small form,
 // the others).
 //
-// Measured.  A causal prompt of 25,119 tokens (28 / 4 heads of 128) takes 2.81 ms,
-// 1.61 PFLOP/s sustained, 0.94 of what a large library product sustains on this
-// part: the tensor pipe and its power.  The products read Q and K from shared
+// Measured.  A causal prompt of 25,119 tokens (28 / 4 heads of 128) takes 2.88 to
+// 2.98 ms by the box's power, 1.52 to 1.57 PFLOP/s, 0.90 to 0.93 of what a large
+// library product sustains on this part: the tensor pipe and its power.  The
+// products read Q and K from shared
 // memory at its full rate, 128 bytes a clock, so a pair of tiles takes 2,300
 // clocks of the pipe instead of 2,050.  2,048 new tokens over 32,768 (64 / 8) take
-// 1.45 ms.  One token over 25,119 takes 20 us for its 51 MB: 7.6 us of memory
+// 1.49 ms.  One token over 25,119 takes 20.5 us for its 51 MB: 7.6 us of memory
 // time between 6 us of start (the plan, the page table, the first tile) and 6 us
-// of end (the last product, the join over 38 CTAs).  16 rows each of 8 sequences of
-// 4,096 to 32,768 take 54 us with pages of 64 slots, 58 with pages of 16 and 70 with
+// of end (the last product, the join over 38 CTAs).  One token each of 64 and 256
+// sequences over 4,000 keys takes 90 and 336 us with pages of 64 (floors of memory
+// 78 and 310), 102 and 373 with pages of 16; over 900 keys 44 and 137 (18 and 70).
+// 16 rows each of 8 sequences of
+// 4,096 to 32,768 take 55 us with pages of 64 slots, 58 with pages of 16 and 69 with
 // pages of 8: a copy costs about 40 clocks besides the 4 of each 128-byte row.
 // Short units are bound by what surrounds their tiles: about 9,000 clocks a unit
 // against 2,800 a tile.
