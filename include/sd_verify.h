@@ -584,6 +584,129 @@ sd_status sd_prompt_attention(const void *q, int64_t q_tok, int64_t q_head, cons
                               void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Norms of queries and keys, positions of several axes
+ *
+ * No counterpart in the method's pages beyond their target models' use of it:
+ * models that norm every head of their queries and keys before the rotary turn,
+ * and video models that give each token a time, a height and a width.  Per head
+ * (row of D elements):
+ *   u = w x / sqrt(mean(x^2) + eps)        (u = x where the weight is NULL)
+ *   y = u turned as by sd_rotary, pair i by positions[axis(i)] of its token
+ * in one pass: u is not rounded, y is rounded once.
+ *
+ * axis(i) of the R/2 pairs, with n axes that have pairs[0] .. pairs[n-1] of them
+ * (their sum is R/2):
+ *   SD_AXES_BLOCKS   the first pairs[0] pairs turn by axis 0, the next pairs[1]
+ *                    by axis 1, and so on
+ *   SD_AXES_STRIPES  pair i turns by axis a = i % n while i < n pairs[a], and by
+ *                    axis 0 otherwise
+ * `turns` holds one word per pair whatever its axis: sd_rotary_table's for one
+ * run of frequencies over all pairs, or, for frequencies that begin anew with
+ * each axis, the tables of 2 pairs[a] one after the other.
+ *
+ *   positions  device int32, axis a of token n at positions[a * pos_stride + n];
+ *              any value
+ *   axes       NULL: one axis
+ *   q, k       device [N, Hq, D] and [N, Hk, D], strides as for sd_rotary; q_out
+ *              and k_out with strides of their own, each its input itself (equal
+ *              pointers and strides) or overlapping no input.  Hk = 0: no keys
+ *   q_weight, k_weight  device [D] of the inputs' type, aligned to it, or NULL
+ *   eps        >= 0, finite
+ *   the rest as for sd_rotary
+ * Rows of non-finite values, and with eps = 0 rows of zeros, give NaN as the
+ * formula does; no other row is touched by them.
+ * ------------------------------------------------------------------------ */
+typedef enum { SD_AXES_BLOCKS = 0, SD_AXES_STRIPES = 1 } sd_axes_order;
+
+typedef struct {
+    int n;                  /* axes, 1 to 4 */
+    int pairs[4];           /* each >= 1 */
+    sd_axes_order order;
+} sd_rope_axes;
+
+sd_status sd_norm_rotary(const void *q, int64_t q_tok, int64_t q_head, void *q_out, int64_t qo_tok, int64_t qo_head,
+                         const void *k, int64_t k_tok, int64_t k_head, void *k_out, int64_t ko_tok, int64_t ko_head,
+                         const void *q_weight, const void *k_weight, float eps, const int32_t *positions,
+                         int64_t pos_stride, const sd_rope_axes *axes, const uint64_t *turns, float magnitude, int N,
+                         int Hq, int Hk, int D, int rot_dim, sd_rope_layout layout, sd_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A paged cache in 8 bits
+ *
+ * With scales, a cache's pages hold e4m3 codes (1 byte an element; the strides
+ * of sd_paged_cache count elements as ever) and every row -- one slot of one kv
+ * head -- of K and of V has an fp32 scale: the value is code * scale.
+ *   k, v   device fp32 [n_pages, Hkv, page_size] contiguous, 16-byte aligned
+ * A row x is written with m = max(max |x|, 2^-100) as scale = m / 448 (448 is the
+ * largest e4m3 value) and codes x (448 / m), in fp32 and to nearest: an element is
+ * off by 2^-4 of itself at most, and by 2^-10 scale where it is small.
+ * Rows are taken to be finite.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    float *k, *v;
+} sd_page_scales;
+
+/* sd_norm_rotary of q and k with the cache write of k and v (sd_rotary_append_paged
+ * with norms and axes): k is normed and turned in fp32 and goes into the cache in
+ * one rounding, v is copied or quantised.
+ *   positions  or NULL: every axis takes the token's cache position
+ *   scales     NULL: the pages hold `dtype`; else e4m3 with these scales
+ *   v          device [N, Hkv, D] with k's strides
+ * The rest as for sd_norm_rotary and sd_rotary_append_paged (q and q_out may be
+ * NULL; q_out contiguous), clamping and fault bits among it. */
+sd_status sd_norm_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, const void *k, const void *v,
+                                      int64_t kv_tok, int64_t kv_head, void *q_out, const void *q_weight,
+                                      const void *k_weight, float eps, const int32_t *positions, int64_t pos_stride,
+                                      const sd_rope_axes *axes, const uint64_t *turns, float magnitude, int rot_dim,
+                                      sd_rope_layout layout, const int32_t *cu_q, const int32_t *kv_len,
+                                      const sd_paged_cache *cache, const sd_page_scales *scales, int N, int B, int Hq,
+                                      int Hkv, int D, sd_dtype dtype, void *stream);
+
+/* sd_paged_attention over a cache in 8 bits: keys and values are code * scale.
+ * dtype is that of q and out.  Everything else as there; the workspace is
+ * sd_paged_attention's.
+ * bf16 over pages of a multiple of 8 slots runs on the tensor cores, in e4m3: q as
+ * the sum of two e4m3 terms (exact for elements above 2^-9 of their row's
+ * largest, off by 2^-18 of that largest below), the weights as two terms (2^-8 of
+ * each, or 2^-16 of the row's largest), fp32 sums.
+ * Scales of slots at and past kv_len[b] may hold anything; those inside a sequence
+ * are finite and not negative. */
+sd_status sd_paged_attention_e4m3(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,
+                                  const sd_page_scales *scales, const int32_t *cu_q, const int32_t *kv_len, int max_q,
+                                  int max_kv, void *out, int N, int B, int Hq, int Hkv, int D, sd_dtype dtype,
+                                  float scale, int causal, void *workspace, size_t workspace_bytes, void *stream);
+
+/* sd_verify_tree_attention over a paged cache: sequence b's new tokens cu_q[b] ..
+ * cu_q[b+1] are the nodes of its tree (any number up to 64, none among them), their
+ * K/V the last of its kv_len[b] cache positions.  Node i sees the positions before
+ * the tree, [0, kv_len[b] - q_len), and position kv_len[b] - q_len + k for every
+ * bit k < q_len set in tree_mask[cu_q[b] + i].  (With ctx_len as
+ * sd_verify_tree_attention counts it, kv_len = ctx_len + T - 1.)  A node that sees
+ * nothing gives zeros.
+ *   tree_mask  device uint64 [N], 8-byte aligned
+ *   scales     NULL: the pages hold `dtype`; else e4m3 with these scales
+ *   max_q      at most 64
+ * Everything else as for sd_paged_attention or sd_paged_attention_e4m3. */
+sd_status sd_paged_tree_attention(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,
+                                  const sd_page_scales *scales, const uint64_t *tree_mask, const int32_t *cu_q,
+                                  const int32_t *kv_len, int max_q, int max_kv, void *out, int N, int B, int Hq,
+                                  int Hkv, int D, sd_dtype dtype, float scale, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* sd_compact_tree_kv in a paged cache: for d = 1 .. n_accepted[b], position
+ * ctx_len[b]-1+d takes the row (every kv head, K and V, bit for bit, with its
+ * scales) of position ctx_len[b]-1+path[b*T+d-1].  All other slots keep theirs.
+ *   path       device int32 [B, T] (sd_accept_tree_greedy's)
+ *   scales     NULL: the pages hold `dtype`; else e4m3 with these scales
+ * A sequence whose path or count is out of range, or whose block (T positions from
+ * ctx_len[b]-1 on) passes the table, is skipped (fault bit 6), and so is one of
+ * which a moved row comes from or goes to a page outside the pool (bit 8).  The
+ * slots that rows move to must be no other sequence's of the call. */
+sd_status sd_compact_tree_paged(const sd_paged_cache *cache, const sd_page_scales *scales, const int32_t *ctx_len,
+                                const int32_t *path, const int32_t *n_accepted, int B, int T, int Hkv, int D,
+                                sd_dtype dtype, void *stream);
+
+/* ------------------------------------------------------------------------
  * Greedy acceptance without a caller workspace
  *
  * No counterpart in the method's pages: this is a convenience of the library.

@@ -984,12 +984,12 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     if (v != SD_OK) return v;
     if (p.N == 0) return SD_OK;
     if (!p.q || !p.k || !p.v || !p.cu || !p.out) return fail(SD_ERR_INVALID_ARG, "null tensor pointer");
-    const size_t es = esize(p.dt);
+    const size_t es = esize(p.dt), ces = p.k_scale ? 1 : es;
     if (!fix_strides(p.N, p.Hq, p.D, p.q_tok, p.q_head))
         return fail(SD_ERR_INVALID_ARG, "query strides must not overlap the D axis");
     if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.out))
         return fail(SD_ERR_INVALID_ARG, "tensor base addresses must be 16-byte aligned");
-    if ((p.q_tok * es) % 16 || (p.q_head * es) % 16 || (p.kv.s * es) % 16 || (p.kv.h * es) % 16)
+    if ((p.q_tok * es) % 16 || (p.q_head * es) % 16 || (p.kv.s * ces) % 16 || (p.kv.h * ces) % 16)
         return fail(SD_ERR_INVALID_ARG, "strides must be multiples of 16 bytes");
     if (!aligned_to(p.cu, 4)) return fail(SD_ERR_INVALID_ARG, "index arrays must be aligned to 4 bytes");
     p.max_q = std::min(p.max_q, p.N);
@@ -1049,7 +1049,157 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     return SD_OK;
 }
 
+sd_status check_scales(const sd_page_scales *s) {
+    if (s && (!s->k || !s->v)) return fail(SD_ERR_INVALID_ARG, "null scales");
+    if (s && (!aligned16(s->k) || !aligned16(s->v))) return fail(SD_ERR_INVALID_ARG, "scales must be 16-byte aligned");
+    return SD_OK;
+}
+
+// attention over a paged cache, as it is or in e4m3, of a tree's nodes or of tokens in a row
+sd_status run_paged(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,
+                    const sd_page_scales *scales, const uint64_t *tree, const int32_t *cu_q, const int32_t *kv_len,
+                    int max_q, int max_kv, void *out, int N, int B, int Hq, int Hkv, int D, sd_dtype dtype, float scale,
+                    int causal, void *workspace, size_t workspace_bytes, void *stream) {
+    VarlenParams p = {};
+    p.q = q; p.q_tok = (long)q_tok; p.q_head = (long)q_head;
+    p.cu = cu_q; p.kv_len = kv_len; p.out = out; p.tree = tree;
+    p.N = N; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.D = D;
+    p.max_q = max_q; p.max_kv = max_kv; p.causal = causal != 0; p.scale = scale; p.dt = dtype;
+    sd_status s = check_varlen(p);
+    if (s != SD_OK) return s;
+    s = check_cache(cache, B, cu_q, kv_len, Hkv, D, scales ? 1 : esize(dtype), 16, &p.kv);
+    if (s != SD_OK) return s;
+    s = check_scales(scales);
+    if (s != SD_OK) return s;
+    if (scales) { p.k_scale = scales->k; p.v_scale = scales->v; }
+    p.k = cache->k; p.v = cache->v;
+    p.table = cache->table; p.table_stride = (long)cache->table_stride; p.table_cols = cache->table_cols;
+    p.n_pages = cache->n_pages; p.page_size = cache->page_size;
+    return run_varlen(p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+// the axes of the pairs, two bits each
+sd_status pack_axes(NormRopeParams &p, const sd_rope_axes *axes) {
+    memset(p.axis, 0, sizeof p.axis);
+    if (!axes) return SD_OK;
+    if (axes->n < 1 || axes->n > 4) return fail(SD_ERR_INVALID_ARG, "1 to 4 axes");
+    if (axes->order != SD_AXES_BLOCKS && axes->order != SD_AXES_STRIPES)
+        return fail(SD_ERR_INVALID_ARG, "unknown order of the axes");
+    long sum = 0;
+    for (int a = 0; a < axes->n; ++a) {
+        if (axes->pairs[a] < 1) return fail(SD_ERR_INVALID_ARG, "every axis has at least one pair");
+        sum += axes->pairs[a];
+    }
+    if (sum != p.rot / 2) return fail(SD_ERR_INVALID_ARG, "the axes' pairs must add up to rot_dim / 2");
+    for (int i = 0, a = 0, end = axes->pairs[0]; i < p.rot / 2; ++i) {
+        int of = 0;
+        if (axes->order == SD_AXES_BLOCKS) {
+            while (i >= end) end += axes->pairs[++a];
+            of = a;
+        } else {
+            of = i % axes->n;
+            if (i >= axes->n * (long)axes->pairs[of]) of = 0;
+        }
+        p.axis[i >> 4] |= (uint32_t)of << (2 * (i & 15));
+    }
+    return SD_OK;
+}
+
+// what the calls with norms and axes share; `n_axes` positions per token where p.positions is given
+sd_status check_norm(NormRopeParams &p, sd_rope_layout layout, const sd_rope_axes *axes) {
+    RopeParams r = {};               // the limits are the plain rotary calls'
+    r.dt = p.dt; r.N = p.N; r.D = p.D; r.rot = p.rot; r.Hq = p.Hq; r.Hk = p.Hk; r.magnitude = p.magnitude;
+    r.turns = p.turns;
+    sd_status s = check_rope(r, layout);
+    if (s != SD_OK) return s;
+    if (!(p.eps >= 0.f) || !isfinite(p.eps)) return fail(SD_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+    const size_t es = esize(p.dt);
+    if (!aligned_to(p.wq, es) || !aligned_to(p.wk, es))
+        return fail(SD_ERR_INVALID_ARG, "weights must be aligned to their elements");
+    if (!aligned_to(p.positions, 4)) return fail(SD_ERR_INVALID_ARG, "index arrays must be aligned to 4 bytes");
+    if (p.positions && axes && axes->n > 1 && p.N > 1 && p.pos_stride < 1)
+        return fail(SD_ERR_INVALID_ARG, "pos_stride must be >= 1");
+    return pack_axes(p, axes);
+}
+
 }  // namespace
+
+sd_status sd_norm_rotary(const void *q, int64_t q_tok, int64_t q_head, void *q_out, int64_t qo_tok, int64_t qo_head,
+                         const void *k, int64_t k_tok, int64_t k_head, void *k_out, int64_t ko_tok, int64_t ko_head,
+                         const void *q_weight, const void *k_weight, float eps, const int32_t *positions,
+                         int64_t pos_stride, const sd_rope_axes *axes, const uint64_t *turns, float magnitude, int N,
+                         int Hq, int Hk, int D, int rot_dim, sd_rope_layout layout, sd_dtype dtype, void *stream) {
+    NormRopeParams p = {};
+    p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;
+    p.q_tok = (long)q_tok; p.q_head = (long)q_head; p.qo_tok = (long)qo_tok; p.qo_head = (long)qo_head;
+    p.k_tok = (long)k_tok; p.k_head = (long)k_head; p.ko_tok = (long)ko_tok; p.ko_head = (long)ko_head;
+    p.wq = q_weight; p.wk = k_weight; p.eps = eps;
+    p.positions = positions; p.pos_stride = (long)pos_stride; p.turns = turns; p.magnitude = magnitude;
+    p.N = N; p.Hq = Hq; p.Hk = Hk; p.D = D; p.rot = rot_dim; p.interleaved = layout == SD_ROPE_INTERLEAVED; p.dt = dtype;
+    if (Hq < 1 || Hk < 0) return fail(SD_ERR_INVALID_ARG, "Hq must be >= 1 and Hk >= 0");
+    sd_status s = check_norm(p, layout, axes);
+    if (s != SD_OK) return s;
+    if (N == 0) return SD_OK;
+    if (!q || !q_out || !positions || (Hk && (!k || !k_out))) return fail(SD_ERR_INVALID_ARG, "null tensor pointer");
+    if (!fix_strides(N, Hq, D, p.q_tok, p.q_head) || !fix_strides(N, Hq, D, p.qo_tok, p.qo_head) ||
+        (Hk && (!fix_strides(N, Hk, D, p.k_tok, p.k_head) || !fix_strides(N, Hk, D, p.ko_tok, p.ko_head))))
+        return fail(SD_ERR_INVALID_ARG, "strides must not overlap the D axis");
+    const size_t es = esize(dtype);
+    if (!aligned_to(q, es) || !aligned_to(q_out, es) || (Hk && (!aligned_to(k, es) || !aligned_to(k_out, es))))
+        return fail(SD_ERR_INVALID_ARG, "tensor base addresses must be aligned to their elements");
+    if ((q == q_out && (p.q_tok != p.qo_tok || p.q_head != p.qo_head)) ||
+        (Hk && k == k_out && (p.k_tok != p.ko_tok || p.k_head != p.ko_head)))
+        return fail(SD_ERR_INVALID_ARG, "in place, input and output must share strides");
+    const cudaError_t e = launch_norm_rope(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm and rotary launch");
+    return SD_OK;
+}
+
+sd_status sd_norm_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_head, const void *k, const void *v,
+                                      int64_t kv_tok, int64_t kv_head, void *q_out, const void *q_weight,
+                                      const void *k_weight, float eps, const int32_t *positions, int64_t pos_stride,
+                                      const sd_rope_axes *axes, const uint64_t *turns, float magnitude, int rot_dim,
+                                      sd_rope_layout layout, const int32_t *cu_q, const int32_t *kv_len,
+                                      const sd_paged_cache *cache, const sd_page_scales *scales, int N, int B, int Hq,
+                                      int Hkv, int D, sd_dtype dtype, void *stream) {
+    NormRopeParams p = {};
+    p.q = q; p.q_out = q_out; p.k = k; p.v = v;
+    p.q_tok = (long)q_tok; p.q_head = (long)q_head; p.qo_tok = (long)Hq * D; p.qo_head = D;
+    p.k_tok = (long)kv_tok; p.k_head = (long)kv_head;
+    p.wq = q_weight; p.wk = k_weight; p.eps = eps;
+    p.positions = positions; p.pos_stride = (long)pos_stride; p.turns = turns; p.magnitude = magnitude;
+    p.N = N; p.Hq = q ? Hq : 0; p.Hk = Hkv; p.D = D; p.rot = rot_dim;
+    p.interleaved = layout == SD_ROPE_INTERLEAVED; p.dt = dtype;
+    if ((q == nullptr) != (q_out == nullptr)) return fail(SD_ERR_INVALID_ARG, "q and q_out go together");
+    if ((q && Hq < 1) || Hkv < 1) return fail(SD_ERR_INVALID_ARG, "Hq and Hkv must be >= 1");
+    sd_status s = check_norm(p, layout, axes);
+    if (s != SD_OK) return s;
+    const size_t es = esize(dtype), ces = scales ? 1 : es;
+    s = check_cache(cache, B, cu_q, kv_len, Hkv, D, ces, ces, &p.pages);
+    if (s != SD_OK) return s;
+    s = check_scales(scales);
+    if (s != SD_OK) return s;
+    if (N == 0) return SD_OK;
+    if (!k || !v) return fail(SD_ERR_INVALID_ARG, "null tensor pointer");
+    if (q && !fix_strides(N, Hq, D, p.q_tok, p.q_head))
+        return fail(SD_ERR_INVALID_ARG, "query strides must not overlap the D axis");
+    if (!fix_strides(N, Hkv, D, p.k_tok, p.k_head))
+        return fail(SD_ERR_INVALID_ARG, "key and value strides must not overlap the D axis");
+    if (q == q_out && q && ((N > 1 && p.q_tok != p.qo_tok) || (Hq > 1 && p.q_head != p.qo_head)))
+        return fail(SD_ERR_INVALID_ARG, "in place, q must be contiguous");
+    if ((q && (!aligned_to(q, es) || !aligned_to(q_out, es))) || !aligned_to(k, es) || !aligned_to(v, es))
+        return fail(SD_ERR_INVALID_ARG, "tensor base addresses must be aligned to their elements");
+    if (scales) { p.k_scale = scales->k; p.v_scale = scales->v; }
+    p.cu = cu_q; p.kv_len = kv_len; p.B = B;
+    p.table = cache->table; p.table_stride = (long)cache->table_stride; p.table_cols = cache->table_cols;
+    p.n_pages = cache->n_pages; p.page_size = cache->page_size;
+    p.k_pages = cache->k; p.v_pages = cache->v;
+    p.fault = fault_ptr();
+    if (!p.fault) return fail(SD_ERR_CUDA, "no CUDA device / fault word unavailable");
+    const cudaError_t e = launch_norm_rope(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm, rotary and append launch");
+    return SD_OK;
+}
 
 sd_status sd_rotary(const void *x, int64_t x_tok, int64_t x_head, void *y, int64_t y_tok, int64_t y_head,
                     const int32_t *positions, const uint64_t *turns, float magnitude, int N, int H, int D,
@@ -1124,19 +1274,8 @@ sd_status sd_paged_attention(const void *q, int64_t q_tok, int64_t q_head, const
                              const int32_t *cu_q, const int32_t *kv_len, int max_q, int max_kv, void *out, int N,
                              int B, int Hq, int Hkv, int D, sd_dtype dtype, float scale, int causal,
                              void *workspace, size_t workspace_bytes, void *stream) {
-    VarlenParams p = {};
-    p.q = q; p.q_tok = (long)q_tok; p.q_head = (long)q_head;
-    p.cu = cu_q; p.kv_len = kv_len; p.out = out;
-    p.N = N; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.D = D;
-    p.max_q = max_q; p.max_kv = max_kv; p.causal = causal != 0; p.scale = scale; p.dt = dtype;
-    sd_status s = check_varlen(p);
-    if (s != SD_OK) return s;
-    s = check_cache(cache, B, cu_q, kv_len, Hkv, D, esize(dtype), 16, &p.kv);
-    if (s != SD_OK) return s;
-    p.k = cache->k; p.v = cache->v;
-    p.table = cache->table; p.table_stride = (long)cache->table_stride; p.table_cols = cache->table_cols;
-    p.n_pages = cache->n_pages; p.page_size = cache->page_size;
-    return run_varlen(p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    return run_paged(q, q_tok, q_head, cache, nullptr, nullptr, cu_q, kv_len, max_q, max_kv, out, N, B, Hq, Hkv, D, dtype,
+                     scale, causal, workspace, workspace_bytes, stream);
 }
 
 sd_status sd_prompt_attention(const void *q, int64_t q_tok, int64_t q_head, const void *k, const void *v,
@@ -1156,6 +1295,59 @@ sd_status sd_prompt_attention(const void *q, int64_t q_tok, int64_t q_head, cons
         return fail(SD_ERR_INVALID_ARG, "key and value strides must not overlap the D axis");
     p.kv.s = tok; p.kv.h = head;
     return run_varlen(p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+sd_status sd_paged_attention_e4m3(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,
+                                  const sd_page_scales *scales, const int32_t *cu_q, const int32_t *kv_len, int max_q,
+                                  int max_kv, void *out, int N, int B, int Hq, int Hkv, int D, sd_dtype dtype,
+                                  float scale, int causal, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!scales) return fail(SD_ERR_INVALID_ARG, "null scales");
+    return run_paged(q, q_tok, q_head, cache, scales, nullptr, cu_q, kv_len, max_q, max_kv, out, N, B, Hq, Hkv, D, dtype,
+                     scale, causal, workspace, workspace_bytes, stream);
+}
+
+sd_status sd_paged_tree_attention(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,
+                                  const sd_page_scales *scales, const uint64_t *tree_mask, const int32_t *cu_q,
+                                  const int32_t *kv_len, int max_q, int max_kv, void *out, int N, int B, int Hq,
+                                  int Hkv, int D, sd_dtype dtype, float scale, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    if (max_q > kMaxTreeT) return fail(SD_ERR_INVALID_ARG, "a tree has at most %d nodes: max_q", kMaxTreeT);
+    if (!tree_mask && N > 0) return fail(SD_ERR_INVALID_ARG, "null tree mask");
+    if (!aligned_to(tree_mask, 8)) return fail(SD_ERR_INVALID_ARG, "tree masks must be aligned to 8 bytes");
+    return run_paged(q, q_tok, q_head, cache, scales, tree_mask, cu_q, kv_len, max_q, max_kv, out, N, B, Hq, Hkv, D,
+                     dtype, scale, 0, workspace, workspace_bytes, stream);
+}
+
+sd_status sd_compact_tree_paged(const sd_paged_cache *cache, const sd_page_scales *scales, const int32_t *ctx_len,
+                                const int32_t *path, const int32_t *n_accepted, int B, int T, int Hkv, int D,
+                                sd_dtype dtype, void *stream) {
+    if (T < 1 || T > kMaxTreeT || Hkv < 1 || Hkv > 4096 || D < 1)
+        return fail(SD_ERR_INVALID_ARG, "need T in [1, 64], Hkv in [1, 4096] and D >= 1");
+    if (dtype != SD_BF16 && dtype != SD_FP32) return fail(SD_ERR_INVALID_ARG, "unknown dtype");
+    const size_t es = scales ? 1 : esize(dtype);
+    if (D > kMaxHeadBytes || (D * es) % 16 != 0 || D * es > (size_t)kMaxHeadBytes)
+        return fail(SD_ERR_UNSUPPORTED, "a (position, head) row must be a multiple of 16 bytes, at most 512");
+    CompactPagedParams p = {};
+    sd_strides st;
+    sd_status s = check_cache(cache, B, ctx_len, ctx_len, Hkv, D, es, 16, &st);
+    if (s != SD_OK) return s;
+    s = check_scales(scales);
+    if (s != SD_OK) return s;
+    if (!path || !n_accepted) return fail(SD_ERR_INVALID_ARG, "null tensor pointer");
+    if (!aligned_to(path, 4) || !aligned_to(n_accepted, 4))
+        return fail(SD_ERR_INVALID_ARG, "index arrays must be aligned to 4 bytes");
+    p.k = cache->k; p.v = cache->v;
+    p.page = (long)(st.b * es); p.slot = (long)(st.s * es); p.head = (long)(st.h * es);
+    if (scales) { p.k_scale = scales->k; p.v_scale = scales->v; }
+    p.table = cache->table; p.table_stride = (long)cache->table_stride; p.table_cols = cache->table_cols;
+    p.n_pages = cache->n_pages; p.page_size = cache->page_size;
+    p.ctx_len = ctx_len; p.path = path; p.n_acc = n_accepted;
+    p.B = B; p.T = T; p.Hkv = Hkv; p.row = (int)(D * es);
+    p.fault = fault_ptr();
+    if (!p.fault) return fail(SD_ERR_CUDA, "no CUDA device / fault word unavailable");
+    const cudaError_t e = launch_compact_tree_paged(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged tree compaction launch");
+    return SD_OK;
 }
 
 size_t sd_paged_attention_workspace_size(int N, int B, int max_q, int Hq, int Hkv, int D, int max_kv,

@@ -15,6 +15,7 @@
 // and softmax one after the other (16 rows of 4 heads over 527 keys: 14 to 18 us).
 // Causal fp32 prompts of 2,048 and 8,192 tokens, 28 / 4 heads of 128: 0.82 and 11.9
 // ms, 37 and 41 TFLOP/s.
+#include "e4m3.cuh"
 #include "varlen.cuh"
 
 #include <math.h>
@@ -43,21 +44,26 @@ template <int D, int R> struct GLay {
 // one that reads 64 keys of a row does too.
 __device__ __forceinline__ int key_at(int d, int key4) { return d * kGTile + ((key4 ^ ((d >> 2) & 15)) << 2); }
 
-// offset of key `key`'s row of the unit's kv head, or -1 for a bad page
-__device__ __forceinline__ long key_offset(const VarlenParams &p, const VlUnit &u, int key) {
+// offset of key `key`'s row of the unit's kv head, or -1 for a bad page; `scale_at` that of its scales
+__device__ __forceinline__ long key_offset(const VarlenParams &p, const VlUnit &u, int key, long &scale_at) {
     if (!p.table) return (long)(u.row0 - u.tok0 + key) * p.kv.s + (long)u.g * p.kv.h;
     const unsigned pi = p.page_log2 >= 0 ? (unsigned)key >> p.page_log2 : (unsigned)key / (unsigned)p.page_size;
     const int pg = __ldg(p.table + (long)u.b * p.table_stride + pi);
     if (pg < 0 || pg >= p.n_pages) { set_fault(p.fault, FAULT_BAD_PAGE); return -1; }
-    return (long)pg * p.kv.b + (long)(key - (int)pi * p.page_size) * p.kv.s + (long)u.g * p.kv.h;
+    const int slot = key - (int)pi * p.page_size;
+    scale_at = ((long)pg * p.Hkv + u.g) * p.page_size + slot;
+    return (long)pg * p.kv.b + (long)slot * p.kv.s + (long)u.g * p.kv.h;
 }
 
-template <typename T, int D, int R>
+// T: the queries' type, C: the cache's (T itself, or e4m3 codes with a scale per row)
+template <typename T, typename C, int D, int R>
 __global__ void __launch_bounds__(kGThreads, 2)
 attn_varlen_generic_kernel(const VarlenParams p) {
     using L = GLay<D, R>;
     constexpr int TM = R / 16, TN = D / 16;          // rows and output columns of a thread
     constexpr int VP = Elem<T>::kPerVec, VPR = D / VP;
+    constexpr int CP = Elem<C>::kPerVec, CPR = D / CP;
+    constexpr bool kScaled = sizeof(C) == 1;
     extern __shared__ float4 smem4[];
     float *Qs = reinterpret_cast<float *>(smem4);    // [D][R + 4]
     float *Ks = Qs + L::kQ;                          // [D][64], swizzled
@@ -99,10 +105,12 @@ attn_varlen_generic_kernel(const VarlenParams p) {
         }
         float o[TM][TN], m[TM], l[TM];
         int lim[TM];
+        uint64_t seen[TM];                             // of a tree: the block's slots that the row sees
 #pragma unroll
         for (int a = 0; a < TM; ++a) {
             const int r = ty * TM + a;
             lim[a] = r < rows ? vl_limit(p, u, u.tok0 + r / G) : 0;
+            seen[a] = p.tree && r < rows ? vl_tree_word(p, u, r / G) : 0;
             m[a] = -INFINITY;
             l[a] = 0.f;
 #pragma unroll
@@ -112,29 +120,39 @@ attn_varlen_generic_kernel(const VarlenParams p) {
             const int key0 = t * kGTile;
             __syncthreads();
             // a warp takes 8 vectors of 4 keys at a time
-            for (int i = tid >> 5; i < (kGTile / 4) * (VPR / 8); i += kGThreads / 32) {
-                const int kk = 4 * (i / (VPR / 8)) + ((tid >> 3) & 3), v = 8 * (i % (VPR / 8)) + (tid & 7);
-                float kf[VP], vf[VP];
-                const T *kp = nullptr, *vp = nullptr;
+            for (int i = tid >> 5; i < (kGTile / 4) * (CPR / 8); i += kGThreads / 32) {
+                const int kk = 4 * (i / (CPR / 8)) + ((tid >> 3) & 3), v = 8 * (i % (CPR / 8)) + (tid & 7);
+                float kf[CP], vf[CP];
+                const C *kp = nullptr, *vp = nullptr;
+                float ks = 1.f, vs = 1.f;
                 if (key0 + kk < u.kv) {
-                    const long at = key_offset(p, u, key0 + kk);
+                    long scale_at = 0;
+                    const long at = key_offset(p, u, key0 + kk, scale_at);
                     if (at >= 0) {
-                        kp = static_cast<const T *>(p.k) + at;
-                        vp = static_cast<const T *>(p.v) + at;
+                        kp = static_cast<const C *>(p.k) + at;
+                        vp = static_cast<const C *>(p.v) + at;
+                        if constexpr (kScaled) {
+                            ks = __ldg(p.k_scale + scale_at);
+                            vs = __ldg(p.v_scale + scale_at);
+                        }
                     }
                 }
                 if (kp) {
-                    Elem<T>::load_vec(kp + v * VP, kf);
-                    Elem<T>::load_vec(vp + v * VP, vf);
+                    Elem<C>::load_vec(kp + v * CP, kf);
+                    Elem<C>::load_vec(vp + v * CP, vf);
+                    if constexpr (kScaled) {
+#pragma unroll
+                        for (int e = 0; e < CP; ++e) { kf[e] *= ks; vf[e] *= vs; }
+                    }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) { kf[e] = 0.f; vf[e] = 0.f; }
+                    for (int e = 0; e < CP; ++e) { kf[e] = 0.f; vf[e] = 0.f; }
                 }
 #pragma unroll
-                for (int e = 0; e < VP; ++e) Ks[key_at(v * VP + e, kk >> 2) + (kk & 3)] = kf[e];
+                for (int e = 0; e < CP; ++e) Ks[key_at(v * CP + e, kk >> 2) + (kk & 3)] = kf[e];
 #pragma unroll
-                for (int e = 0; e < VP; e += 4)
-                    *reinterpret_cast<float4 *>(Vs + kk * D + v * VP + e) = make_float4(vf[e], vf[e + 1], vf[e + 2], vf[e + 3]);
+                for (int e = 0; e < CP; e += 4)
+                    *reinterpret_cast<float4 *>(Vs + kk * D + v * CP + e) = make_float4(vf[e], vf[e + 1], vf[e + 2], vf[e + 3]);
             }
             __syncthreads();
             float2 s2[TM][2];
@@ -168,7 +186,8 @@ attn_varlen_generic_kernel(const VarlenParams p) {
                 float mx = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if (key0 + 4 * tx + c >= lim[a]) s[a][c] = -INFINITY;
+                    const int key = key0 + 4 * tx + c;
+                    if (key >= lim[a] || (p.tree && key >= u.off && !(seen[a] >> (key - u.off) & 1))) s[a][c] = -INFINITY;
                     mx = fmaxf(mx, s[a][c]);
                 }
 #pragma unroll
@@ -248,7 +267,7 @@ attn_varlen_generic_kernel(const VarlenParams p) {
     for (int i = 0; i < ends.n; ++i) vl_join(p, ends.u[i], p.tb, 0, &join_flag, tid, kGThreads, 0);
 }
 
-template <typename T, int D, int R>
+template <typename T, typename C, int D, int R>
 int grid_of() {
     using L = GLay<D, R>;
     static std::atomic<int> per_sm[kMaxDevices];
@@ -256,9 +275,9 @@ int grid_of() {
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     if (dev >= 0 && dev < kMaxDevices) n = per_sm[dev].load(std::memory_order_acquire);
     if (n == 0) {
-        if (cudaFuncSetAttribute(attn_varlen_generic_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(attn_varlen_generic_kernel<T, C, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  L::kSmem) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_varlen_generic_kernel<T, D, R>, kGThreads,
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_varlen_generic_kernel<T, C, D, R>, kGThreads,
                                                           L::kSmem) != cudaSuccess)
             return 0;
         n = n < kVarlenGenPerSm ? n : kVarlenGenPerSm;
@@ -267,7 +286,7 @@ int grid_of() {
     return n * device_sm_count();
 }
 
-template <typename T, int D, int R>
+template <typename T, typename C, int D, int R>
 cudaError_t launch_gen(const VarlenParams &p, int grid, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -281,28 +300,28 @@ cudaError_t launch_gen(const VarlenParams &p, int grid, cudaStream_t st) {
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attn_varlen_generic_kernel<T, D, R>, p);
+    return cudaLaunchKernelEx(&cfg, attn_varlen_generic_kernel<T, C, D, R>, p);
 }
 
-template <typename F> auto dispatch(const VarlenParams &p, F f) {
+template <typename T, typename C, typename F> auto by_size(const VarlenParams &p, F f) {
     const bool big = varlen_generic_rows(p) == 64;
+    if (p.D == 128) return big ? f.template run<T, C, 128, 64>() : f.template run<T, C, 128, 16>();
+    return big ? f.template run<T, C, 64, 64>() : f.template run<T, C, 64, 16>();
+}
+template <typename F> auto dispatch(const VarlenParams &p, F f) {
     using bf = __nv_bfloat16;
-    if (p.dt == SD_BF16) {
-        if (p.D == 128) return big ? f.template run<bf, 128, 64>() : f.template run<bf, 128, 16>();
-        return big ? f.template run<bf, 64, 64>() : f.template run<bf, 64, 16>();
-    }
-    if (p.D == 128) return big ? f.template run<float, 128, 64>() : f.template run<float, 128, 16>();
-    return big ? f.template run<float, 64, 64>() : f.template run<float, 64, 16>();
+    if (p.k_scale) return p.dt == SD_BF16 ? by_size<bf, E4m3>(p, f) : by_size<float, E4m3>(p, f);
+    return p.dt == SD_BF16 ? by_size<bf, bf>(p, f) : by_size<float, float>(p, f);
 }
 
 struct GridOf {
-    template <typename T, int D, int R> int run() const { return grid_of<T, D, R>(); }
+    template <typename T, typename C, int D, int R> int run() const { return grid_of<T, C, D, R>(); }
 };
 struct Launch {
     const VarlenParams &p;
     int grid;
     cudaStream_t st;
-    template <typename T, int D, int R> cudaError_t run() const { return launch_gen<T, D, R>(p, grid, st); }
+    template <typename T, typename C, int D, int R> cudaError_t run() const { return launch_gen<T, C, D, R>(p, grid, st); }
 };
 
 }  // namespace

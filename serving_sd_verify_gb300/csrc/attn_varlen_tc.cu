@@ -975,6 +975,7 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
 
 bool varlen_tc_supported(const VarlenParams &p) {
     if (p.dt != SD_BF16 || (p.D != 64 && p.D != 128) || p.Hq / p.Hkv > kVarlenMaxGroup) return false;
+    if (p.k_scale || p.tree) return false;
     if (p.table && p.page_size % 8) return false;      // a copy's rows start on the swizzle's 8-row period
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;

@@ -110,6 +110,71 @@ __global__ void __launch_bounds__(kCompactThreads) compact_tree_kv_kernel(const 
     }
 }
 
+// The same in a paged cache: CTA (b, h), all rows read into registers before any
+// is written.  Thread d looks up where depth d + 1 comes from and goes to, so the
+// path, the table and the rows are three dependent reads in all, and what bounds
+// it is their latency.
+constexpr int kCompactPagedThreads = 256;
+constexpr int kCompactVecs = 2 * (kMaxTreeT - 1) * (kMaxHeadBytes / 16);       // K and V of a path
+constexpr int kCompactHeld = (kCompactVecs + kCompactPagedThreads - 1) / kCompactPagedThreads;
+__global__ void __launch_bounds__(kCompactPagedThreads) compact_tree_paged_kernel(const CompactPagedParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ long from[kMaxTreeT], to[kMaxTreeT];       // offsets of the rows, bytes
+    const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+    const int n = p.n_acc[b], c = p.ctx_len[b];
+    bool ok = n >= 0 && n <= p.T - 1 && c >= 1 && (long)c - 1 + p.T <= (long)p.table_cols * p.page_size;
+    bool pages = true;
+    float ks = 0.f, vs = 0.f;
+    long scale_to = 0;
+    if (ok && tid < n) {
+        const int node = p.path[(long)b * p.T + tid];
+        ok = node >= 1 && node < p.T;
+        if (ok) {
+            const int32_t *row = p.table + (long)b * p.table_stride;
+            const unsigned a = (unsigned)(c - 1 + node), z = (unsigned)(c + tid);   // below 2^31 + 64
+            const unsigned ac = a / (unsigned)p.page_size, zc = z / (unsigned)p.page_size;
+            const int pa = row[ac], pz = row[zc];
+            const int sa = (int)(a - ac * (unsigned)p.page_size), sz = (int)(z - zc * (unsigned)p.page_size);
+            pages = pa >= 0 && pa < p.n_pages && pz >= 0 && pz < p.n_pages;
+            from[tid] = (long)pa * p.page + (long)sa * p.slot + (long)h * p.head;
+            to[tid] = (long)pz * p.page + (long)sz * p.slot + (long)h * p.head;
+            if (p.k_scale && pages) {
+                const long at = ((long)pa * p.Hkv + h) * p.page_size + sa;
+                ks = p.k_scale[at];
+                vs = p.v_scale[at];
+                scale_to = ((long)pz * p.Hkv + h) * p.page_size + sz;
+            }
+        }
+    }
+    ok = __syncthreads_and(ok);
+    pages = __syncthreads_and(pages);
+    if (!ok || !pages) {
+        if (h == 0 && tid == 0) set_fault(p.fault, ok ? FAULT_BAD_PAGE : FAULT_BAD_COMMIT);
+        return;
+    }
+    const int vec = p.row / 16, half = n * vec;            // 16-byte words of a row, of K's rows
+    uint4 w[kCompactHeld];
+#pragma unroll
+    for (int k = 0; k < kCompactHeld; ++k) {
+        const int i = tid + k * kCompactPagedThreads;
+        if (i >= 2 * half) break;
+        const int j = i < half ? i : i - half;
+        w[k] = reinterpret_cast<const uint4 *>(static_cast<const char *>(i < half ? p.k : p.v) + from[j / vec])[j % vec];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kCompactHeld; ++k) {
+        const int i = tid + k * kCompactPagedThreads;
+        if (i >= 2 * half) break;
+        const int j = i < half ? i : i - half;
+        reinterpret_cast<uint4 *>(static_cast<char *>(i < half ? p.k : p.v) + to[j / vec])[j % vec] = w[k];
+    }
+    if (p.k_scale && tid < n) {
+        p.k_scale[scale_to] = ks;
+        p.v_scale[scale_to] = vs;
+    }
+}
+
 // A grid-stride copy of 16-byte vectors.  The stores cross the chip-to-host
 // link one by one, so a handful of CTAs per SM keep enough of them in flight;
 // for the few hundred KB of a step's results this ends sooner than a
@@ -155,6 +220,10 @@ cudaError_t launch_store_to_host(const HostStoreParams &p, int sm_count, cudaStr
 
 cudaError_t launch_compact_tree_kv(const CompactParams &p, cudaStream_t st) {
     return launch_pdl_cm(compact_tree_kv_kernel, dim3((unsigned)p.B, (unsigned)p.Hkv), dim3(kCompactThreads), st, p);
+}
+
+cudaError_t launch_compact_tree_paged(const CompactPagedParams &p, cudaStream_t st) {
+    return launch_pdl_cm(compact_tree_paged_kernel, dim3((unsigned)p.B, (unsigned)p.Hkv), dim3(kCompactPagedThreads), st, p);
 }
 
 }  // namespace sdv

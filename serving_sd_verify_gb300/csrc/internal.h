@@ -28,6 +28,7 @@ constexpr int kMaxT = 16;           // block rows (anchor + 15 proposals)
 constexpr int kMaxTreeT = 64;       // nodes of a draft tree (one 64-bit ancestor mask per node)
 constexpr int kTileKeys = 64;       // keys per tile of the CUDA-core attention kernel
 constexpr int kTcTileKeys = 128;    // keys per tile of the tensor-core attention kernel
+constexpr int kMaxHeadDim = 1024;   // elements of a head that the rotary calls take
 constexpr int kMaxHeadBytes = 512;  // bytes of one (position, kv head) row the tree compaction moves
 
 constexpr unsigned long long kBarrierWaitNs = 2000000000ull;   // an in-kernel barrier wait gives up after 2 s
@@ -100,7 +101,9 @@ struct VarlenParams {
     int N, B, Hq, Hkv, D;
     int max_q, max_kv, causal;
     float scale;
-    sd_dtype dt;
+    sd_dtype dt;                    // of q and out
+    const float *k_scale, *v_scale; // [n_pages, Hkv, page_size]: the pages hold e4m3 codes; null: dt
+    const uint64_t *tree;           // [N] which of its sequence's new tokens a token sees; null: as `causal` says
     int tb;                         // tokens per unit
     int tile_log2;                  // keys per tile: a power of two
     int line_shift;                 // the work line counts keys >> line_shift
@@ -161,6 +164,32 @@ struct RopeParams {
     unsigned int *fault;
 };
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t st);
+
+// The same with norms of the heads and positions of several axes; the cache as
+// it is, or in e4m3 with a scale per row.
+struct NormRopeParams {
+    const void *q, *k, *v;          // v: an append, else k goes to k_out
+    void *q_out, *k_out;
+    long q_tok, q_head, qo_tok, qo_head, k_tok, k_head, ko_tok, ko_head;   // elements; v as k
+    const void *wq, *wk;            // null: not normed
+    float eps;
+    const int32_t *positions;       // axis a of token n at a * pos_stride + n; null: the cache position (append only)
+    long pos_stride;
+    const uint64_t *turns;          // [rot / 2]
+    float magnitude;
+    uint32_t axis[kMaxHeadDim / 32];    // of pair i: 2 bits at 2 i
+    int N, Hq, Hk, D, rot, interleaved;
+    sd_dtype dt;
+    const int32_t *cu, *kv_len, *table;
+    int B;
+    long table_stride;
+    int table_cols, n_pages, page_size;
+    void *k_pages, *v_pages;
+    sd_strides pages;
+    float *k_scale, *v_scale;       // e4m3 pages; null: dt
+    unsigned int *fault;
+};
+cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t st);
 
 // kernel launchers: return the launch error (cudaSuccess when enqueued)
 cudaError_t launch_attn_generic(const AttnParams &p, cudaStream_t st);
@@ -288,6 +317,19 @@ struct CompactParams {
     unsigned int *fault;
 };
 cudaError_t launch_compact_tree_kv(const CompactParams &p, cudaStream_t st);
+
+struct CompactPagedParams {
+    void *k, *v;                    // pages, strides in bytes
+    long page, slot, head;
+    float *k_scale, *v_scale;       // or null
+    const int32_t *table;
+    long table_stride;
+    int table_cols, n_pages, page_size;
+    const int32_t *ctx_len, *path, *n_acc;
+    int B, T, Hkv, row;             // row: bytes of a (slot, head)
+    unsigned int *fault;
+};
+cudaError_t launch_compact_tree_paged(const CompactPagedParams &p, cudaStream_t st);
 
 // SpecFLASH latent compressor: out[i] = softmax(q . f[i]^T) . f[i] per frame i.
 constexpr int kLatentMaxQueries = 64;

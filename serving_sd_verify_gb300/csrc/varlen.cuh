@@ -327,6 +327,14 @@ __device__ __forceinline__ int vl_limit(const VarlenParams &p, const VlUnit &u, 
     return p.causal ? max(0, min(u.kv, u.off + i + 1)) : u.kv;
 }
 
+// Of a tree: bit k is set where the unit's token `i` sees the k-th of its
+// sequence's new tokens, at position off + k (the q = kv - off of them, at most 64).
+__device__ __forceinline__ uint64_t vl_tree_word(const VarlenParams &p, const VlUnit &u, int i) {
+    const int q = u.kv - u.off;
+    const uint64_t w = __ldg(reinterpret_cast<const unsigned long long *>(p.tree) + u.row0 + i);
+    return q < 64 ? w & ((1ull << q) - 1) : w;
+}
+
 // the units that CTA c shares with others (one full warp): the one its share
 // begins in the middle of, and the one it opens and leaves unfinished
 struct VlEnds {
