@@ -1033,7 +1033,8 @@ sd_status run_varlen(VarlenParams &p, void *ws, size_t ws_bytes, cudaStream_t st
     p.out32 = aligned_to(p.out, 32) && p.D * es % 32 == 0;
     for (;;) {
         p.inv_grid = 1.0f / (float)grid;
-        const cudaError_t e = path == 2 ? launch_varlen_tc(p, grid, st) : launch_varlen_generic(p, grid, st);
+        const cudaError_t e = path != 2 ? launch_varlen_generic(p, grid, st)
+                              : p.k_scale ? launch_varlen_tc8(p, grid, st) : launch_varlen_tc(p, grid, st);
         if (e == cudaErrorCooperativeLaunchTooLarge && grid > 1) {
             // a device that cannot hold that many CTAs at once (a partitioned one): any number serves
             (void)cudaGetLastError();

@@ -50,21 +50,12 @@
 //
 // Every wait is bounded; one that gives up sets the fault word, and the CTA
 // drains its copies and MMAs before it returns.
-#include "tcgen05.cuh"
-#include "varlen.cuh"
-
-#include <math.h>
-#include <atomic>
+#include "varlen_tc.cuh"
 
 namespace sdv {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;   // 216 * 256 + 72 * 128 = 168 * 384
-constexpr int kLaunchRegs = 168;
-static_assert(kSoftmaxRegs * 256 + kOtherRegs * 128 <= kLaunchRegs * kThreads, "register shares within the launch's");
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 16.0f;           // log2 units
 constexpr int kPFirst = 64;                 // keys of P announced first; P V of these runs while the others' weights are made
 
@@ -84,39 +75,6 @@ template <int D> struct Lay {
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
-struct Misc {
-    uint32_t tmem;
-    int abort_flag;
-    int join_flag;
-    int pad;
-    VlPlan plan;
-    VlEnds ends;
-};
-static_assert(sizeof(Misc) <= 512, "the misc area");
-
-struct RingPos {        // slot and phase of the next tile in a ring
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void step(int n) { if (++slot == n) { slot = 0; phase ^= 1u; } }
-};
-
-// mbar_wait, inlined: a call cannot be made where the warps' register counts differ
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned int *fault) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_timer();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (abort_flag && *abort_flag) return false;
-            if (global_timer() - t0 > kWaitLimitNs) {
-                if (abort_flag) *abort_flag = 1;
-                set_fault(fault, FAULT_WAIT_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-
 // K or V of 128 keys of the packed rows, or one page's 64 columns, with an L2 policy
 __device__ __forceinline__ void load_kv_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, uint64_t policy, int row,
                                            int g) {
@@ -135,33 +93,6 @@ __device__ __forceinline__ void load_kv_5d(uint32_t dst, const CUtensorMap *map,
         : "memory");
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13,"
-        " %14, %15}, [%16];"
-        : SDV_R8(0), SDV_R8(8)
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_bind16(uint32_t (&r)[16]) { asm volatile("" : SDV_W8(0), SDV_W8(8)); }
-
-__device__ __forceinline__ void store_32b(void *p, const uint32_t *v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
-// true in one lane of a converged warp, the same one each time
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-    return r != 0;
-}
-
 // kSmall: no sequence has more rows of a kv head than one tile holds (decoding,
 // block verification).  Those calls are bound by memory, so P goes into the
 // second product as two bf16 terms, to 2^-16 of each weight, and the second row
@@ -177,7 +108,8 @@ template <bool kSets> __device__ __forceinline__ constexpr int key_of(int c) {
     return kSets ? 16 * ((c & 63) >> 3) + 8 * (c >> 6) + (c & 7) : c;
 }
 enum From { kPacked, kPages, kPages16 };
-template <int D, From kFrom, bool kSmall>
+// kTree: a row sees of its sequence's new tokens those that its mask says.
+template <int D, From kFrom, bool kSmall, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const VarlenParams p, const int tpt, const int box) {
@@ -558,6 +490,7 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 const int tl = tr + (pair && w ? tpt : 0);             // token within the unit
                 const bool row_ok = tr < tpt && tl < u.ntok;
                 const int lim = row_ok ? vl_limit(p, u, u.tok0 + tl) : 0;
+                const uint64_t word = kTree && row_ok ? vl_tree_word(p, u, tl) : 0;
                 // rows this warp has to do anything for
                 const bool warp_live = __any_sync(0xffffffffu, row_ok);
                 float m_used = -INFINITY, l = 0.f;
@@ -598,7 +531,18 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_ld_bind(s[c]);
                         const int vis = lim - key0;                     // this row sees keys [0, vis) of the tile
-                        if (!__all_sync(0xffffffffu, vis >= 128 || !row_ok)) {
+                        if constexpr (kTree) {
+                            if (key0 + 128 > u.off) {                   // the tile holds nodes, or ends behind them
+                                const uint64_t seen[2] = {tree_seen(word, key0 - u.off), tree_seen(word, key0 + 64 - u.off)};
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) {
+                                        const int key = key_of<kSets>(32 * c + e);
+                                        if (!(seen[key >> 6] >> (key & 63) & 1)) s[c][e] = 0xff800000u;
+                                    }
+                            }
+                        } else if (!__all_sync(0xffffffffu, vis >= 128 || !row_ok)) {
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -876,19 +820,6 @@ attn_varlen_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn_vl() {
-    // looked up once; the initialisation of a function-local static is thread-safe
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess && q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-        return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-    }();
-    return fn;
-}
-
 bool encode_vl(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                const cuuint32_t *box) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn_vl();
@@ -899,13 +830,7 @@ bool encode_vl(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int page_box(int page_size) {       // slots per copy: the largest power of two that divides the page, up to 128
-    int b = 128;
-    while (page_size % b) b >>= 1;
-    return b;
-}
-
-template <int D, From kFrom, bool kSmall>
+template <int D, From kFrom, bool kSmall, bool kTree>
 cudaError_t configure() {
     // the shared-memory limit, and the registers that the warps share out
     static std::atomic<bool> done[kMaxDevices];
@@ -914,16 +839,16 @@ cudaError_t configure() {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, attn_varlen_tc_kernel<D, kFrom, kSmall>);
+    e = cudaFuncGetAttributes(&a, attn_varlen_tc_kernel<D, kFrom, kSmall, kTree>);
     if (e != cudaSuccess) return e;
     if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;   // setmaxnreg would wait for registers that are not there
-    e = cudaFuncSetAttribute(attn_varlen_tc_kernel<D, kFrom, kSmall>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_varlen_tc_kernel<D, kFrom, kSmall, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Lay<D>::kSmem);
     if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
     return e;
 }
 
-template <int D, From kFrom, bool kSmall>
+template <int D, From kFrom, bool kSmall, bool kTree = false>
 cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     const int G = p.Hq / p.Hkv, tpt = 128 / G;
     alignas(64) CUtensorMap mq, mk, mv;
@@ -952,7 +877,7 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
             if (!encode_vl(m, t, 4, dims, strides, box)) return cudaErrorInvalidValue;
         }
     }
-    cudaError_t e = configure<D, kFrom, kSmall>();
+    cudaError_t e = configure<D, kFrom, kSmall, kTree>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -968,14 +893,13 @@ cudaError_t launch_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kFrom, kSmall>, mq, mk, mv, p, tpt, box_rows);
+    return cudaLaunchKernelEx(&cfg, attn_varlen_tc_kernel<D, kFrom, kSmall, kTree>, mq, mk, mv, p, tpt, box_rows);
 }
 
 }  // namespace
 
 bool varlen_tc_supported(const VarlenParams &p) {
     if (p.dt != SD_BF16 || (p.D != 64 && p.D != 128) || p.Hq / p.Hkv > kVarlenMaxGroup) return false;
-    if (p.k_scale || p.tree) return false;
     if (p.table && p.page_size % 8) return false;      // a copy's rows start on the swizzle's 8-row period
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
@@ -994,10 +918,17 @@ bool varlen_tc_supported(const VarlenParams &p) {
 
 cudaError_t launch_varlen_tc(const VarlenParams &p, int grid, cudaStream_t st) {
     const bool small = p.max_q <= 128 / (p.Hq / p.Hkv);
+    const bool sets = p.D == 128 && p.table && page_box(p.page_size) == 16;
+    if (p.tree) {
+        if (sets)
+            return small ? launch_tc<128, kPages16, true, true>(p, grid, st) : launch_tc<128, kPages16, false, true>(p, grid, st);
+        if (p.D == 128)
+            return small ? launch_tc<128, kPages, true, true>(p, grid, st) : launch_tc<128, kPages, false, true>(p, grid, st);
+        return small ? launch_tc<64, kPages, true, true>(p, grid, st) : launch_tc<64, kPages, false, true>(p, grid, st);
+    }
     if (p.D == 128) {
         if (!p.table) return small ? launch_tc<128, kPacked, true>(p, grid, st) : launch_tc<128, kPacked, false>(p, grid, st);
-        if (page_box(p.page_size) == 16)
-            return small ? launch_tc<128, kPages16, true>(p, grid, st) : launch_tc<128, kPages16, false>(p, grid, st);
+        if (sets) return small ? launch_tc<128, kPages16, true>(p, grid, st) : launch_tc<128, kPages16, false>(p, grid, st);
         return small ? launch_tc<128, kPages, true>(p, grid, st) : launch_tc<128, kPages, false>(p, grid, st);
     }
     if (!p.table) return small ? launch_tc<64, kPacked, true>(p, grid, st) : launch_tc<64, kPacked, false>(p, grid, st);

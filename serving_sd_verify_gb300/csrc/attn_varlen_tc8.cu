@@ -1,0 +1,954 @@
+// Attention of packed new tokens over a paged cache in 8 bits (e4m3 codes with a
+// scale per row) on the tensor cores, for sm_103a: bf16 queries and outputs, pages
+// of a multiple of 8 slots, D of 64 or 128.
+//
+// The products run in e4m3 on the codes as they lie in the cache: no key or value is
+// ever widened, so a tile of 128 keys is 16 KB to copy and to read instead of 32.
+// With k_n, v_n the scales of key n, and for a unit (up to 256 query rows, as in
+// attn_varlen_tc.cu, whose tiles, streams and joins these are):
+//   S = (Q1 + Q2) K^T,  x_n = S_n k_n c,  m = max x,  P_n = exp2(x_n - m)
+//   l = sum P_n,  W_n = P_n v_n / v,  O = (W1 + W2) V,  out = O v / l
+//   Q: a row times a power of two that brings its largest element to [128, 256), as
+//     a first e4m3 term and, exactly, what that leaves: a bf16 element has 8 bits and
+//     each term holds 4, so the two are the element itself where it is above 2^-10
+//     of the row's largest, and off by 2^-18 of the largest where not.  c is that
+//     power's inverse times scale log2(e).
+//   v: the largest v_n of the stream's tiles so far; the weights of values that are
+//     small against others' are small.  Where it grows, O is rescaled as where m does.
+//   W: 64 W_n in two e4m3 terms, the top four bits and the nearest to the rest: off by
+//     2^-8 of itself, or by 2^-15 of the reference where it is small.  m moves where
+//     the maximum grows by more than 2^2 (2^16 in bf16), so 64 W_n stays below 448.
+// l takes P before any rounding.
+//
+// Warps as in attn_varlen_tc.cu, except that the softmax warps split and write Q
+// (thread = row, which keeps its power of two) and warp 2 reads the scales ahead and
+// hands them over in a ring of kScaleSlots tiles.
+// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [384,384+D); the
+// terms of W_i overlay columns 0-31 and 32-63 of S_i.
+//
+// Every wait is bounded; one that gives up sets the fault word, and the CTA
+// drains its copies and MMAs before it returns.
+#include "e4m3.cuh"
+#include "varlen_tc.cuh"
+
+namespace sdv {
+
+namespace {
+
+constexpr float kRescale8 = 2.0f;           // log2 units
+constexpr float kWeightScale = 64.0f;       // 64 * 2^kRescale8 <= 448
+constexpr int kScaleSlots = 4;
+
+// a tile's scales: K's, kWeightScale times V's against `ref`, which was `ratio` times that before this tile
+struct Scales {
+    float k[128], v[128];
+    float ratio, ref;
+    float pad[2];
+};
+
+struct Misc8 : Misc {
+    float vref[2];
+};
+static_assert(sizeof(Misc8) <= 512, "the misc area");
+
+template <int D> struct Lay8 {
+    static constexpr int kTile = 128 * D;                  // one term of Q, K or V: 128 rows of D bytes
+    static constexpr int kSlots = D == 128 ? 9 : 16;
+    static constexpr int kOffQ = 0;                        // two row tiles of two terms
+    static constexpr int kOffRing = 4 * kTile;
+    static constexpr int kMaxSlots = kSlots + 2;           // where no unit has a second row tile, its room too
+    static constexpr int kOffScale = kOffRing + kSlots * kTile;
+    static constexpr int kOffBar = kOffScale + kScaleSlots * (int)sizeof(Scales);
+    // full[max] empty[max] qfull drain sfull[2] pfull[2][2] ofull[2] ofree[2] scfull[] scempty[]
+    static constexpr int kBars = 2 * kMaxSlots + 2 + 2 + 4 + 2 + 2 + 2 * kScaleSlots;
+    static constexpr int kOffMl = kOffBar + 8 * kBars;     // [2][128] exchange between the streams
+    static constexpr int kOffMisc = kOffMl + 2 * 128 * 4;
+    static constexpr int kSmem = kOffMisc + 512 + 1024;    // + alignment slack
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+    static_assert(kOffBar % 16 == 0 && kOffMl % 16 == 0, "aligned parts");
+};
+
+// K or V of `box` slots of one page, with an L2 policy
+__device__ __forceinline__ void load_page(uint32_t dst, const CUtensorMap *map, uint32_t bar, uint64_t policy, int slot,
+                                          int g, int page) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(slot), "r"(g), "r"(page), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+// instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D, A K-major
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// descriptor of rows of D bytes in 8-row groups, swizzled within their D bytes
+template <int D> __device__ __forceinline__ uint64_t row_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)(8 * D / 16) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;       // 128-byte or 64-byte swizzle
+    return d;
+}
+// byte offset of 16-byte chunk c of row r in such a tile
+template <int D> __device__ __forceinline__ uint32_t row_off(int r, int c) {
+    return D == 128 ? sw128_off(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ float top_bits(float x) { return __uint_as_float(__float_as_uint(x) & 0xfff00000u); }
+
+// Row r of the Q tile at `tile` (the second term's tile behind the first's): part
+// `part` of its columns (halves, or all of them where parts is 2), in two terms.
+// Returns what the products have to be multiplied by.
+template <int D>
+__device__ __forceinline__ float put_query(const __nv_bfloat16 *q, uint8_t *tile, int r, int part, int parts) {
+    uint4 v[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+    uint32_t top = 0;                                  // the largest magnitudes, as pairs of bit patterns
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+        top = __vmaxu2(__vmaxu2(__vmaxu2(top, v[i].x & 0x7fff7fffu), __vmaxu2(v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu)),
+                       v[i].w & 0x7fff7fffu);
+    const int e = (int)(max(top & 0xffffu, top >> 16) >> 7);          // the largest element's biased exponent
+    const int ec = max(e, 8);                          // (rows below 2^-119 keep their order of size, not their last bits)
+    const float mul = __uint_as_float((uint32_t)(261 - ec) << 23);    // 2^(134 - ec): the largest to [2^7, 2^8)
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {                 // 16 elements, one chunk of each term
+        if (parts == 1 && i / (D / 32) != part) continue;
+        const uint32_t src[8] = {v[2 * i].x, v[2 * i].y, v[2 * i].z, v[2 * i].w,
+                                 v[2 * i + 1].x, v[2 * i + 1].y, v[2 * i + 1].z, v[2 * i + 1].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float f[4] = {__uint_as_float(src[2 * j] << 16) * mul, __uint_as_float(src[2 * j] & 0xffff0000u) * mul,
+                          __uint_as_float(src[2 * j + 1] << 16) * mul, __uint_as_float(src[2 * j + 1] & 0xffff0000u) * mul};
+            hi[j] = e4m3x4(f[0], f[1], f[2], f[3]);
+            const float4 h = from_e4m3x4(hi[j]);
+            lo[j] = e4m3x4(f[0] - h.x, f[1] - h.y, f[2] - h.z, f[3] - h.w);
+        }
+        *reinterpret_cast<uint4 *>(tile + row_off<D>(r, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(tile + 128 * D + row_off<D>(r, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    return e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ec - 7) << 23);
+}
+
+// kSmall: no sequence has more rows of a kv head than one tile holds: the second
+// row tile's room is ring slots.  kTree: a row sees of its sequence's new tokens
+// those that its mask says.
+template <int D, bool kSmall, bool kTree>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                       const VarlenParams p, const int tpt, const int box) {
+    using L = Lay8<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t base = (raw_u32 + 1023u) & ~1023u;
+    uint8_t *sbase = smem_raw + (base - raw_u32);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = (int)blockIdx.x;
+
+    const uint32_t sQ = base + L::kOffQ, sRing = base + L::kOffRing - (kSmall ? 2 * L::kTile : 0), bar0 = base + L::kOffBar;
+    constexpr int slots = kSmall ? L::kMaxSlots : L::kSlots;
+    auto full_bar = [&](int i) { return bar0 + 8u * i; };
+    auto empty_bar = [&](int i) { return bar0 + 8u * (L::kMaxSlots + i); };
+    const uint32_t bar1 = bar0 + 8u * (2 * L::kMaxSlots);
+    const uint32_t qfull_bar = bar1, drain_bar = bar1 + 8u;                  // Q written (8 warps); see the end
+    auto sfull_bar = [&](int i) { return bar1 + 8u * (2 + i); };             // S_i computed
+    auto pfull_bar = [&](int i, int h) { return bar1 + 8u * (4 + 2 * i + h); };   // half h of P_i written (4 warps)
+    auto ofull_bar = [&](int i) { return bar1 + 8u * (8 + i); };             // O_i complete for the unit
+    auto ofree_bar = [&](int i) { return bar1 + 8u * (10 + i); };            // O_i read out (4 warps)
+    auto scfull_bar = [&](int i) { return bar1 + 8u * (12 + i); };           // scales written
+    auto scempty_bar = [&](int i) { return bar1 + 8u * (12 + kScaleSlots + i); };   // and read (8 warps, or 4 twice)
+    Scales *scales = reinterpret_cast<Scales *>(sbase + L::kOffScale);
+    float *xrow = reinterpret_cast<float *>(sbase + L::kOffMl);      // [2][128]: one value per stream and row
+    Misc8 *misc = reinterpret_cast<Misc8 *>(sbase + L::kOffMisc);
+    volatile int *abort_flag = &misc->abort_flag;
+
+    if (tid == 0) {
+        for (int i = 0; i < L::kMaxSlots; ++i) { mbar_init(full_bar(i), 1); mbar_init(empty_bar(i), 1); }
+        mbar_init(qfull_bar, 8);
+        for (int i = 0; i < kScaleSlots; ++i) { mbar_init(scfull_bar(i), 1); mbar_init(scempty_bar(i), 8); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull_bar(i), 1);
+            mbar_init(pfull_bar(i, 0), 4);
+            mbar_init(pfull_bar(i, 1), 4);
+            mbar_init(ofull_bar(i), 1);
+            mbar_init(ofree_bar(i), 4);
+        }
+        misc->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&misc->tmem)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) {
+        const VlPlan q = vl_plan(p, cta);
+        vl_plan_store(q, &misc->plan);
+        // the producer goes straight on to its copies (it set up the barriers itself); the others wait for the plan
+        asm volatile("bar.arrive 15, %0;" ::"n"(kThreads) : "memory");
+    } else {
+        tc_fence_before();
+        named_sync(15, kThreads);
+        tc_fence_after();
+    }
+    const uint32_t tmem = warp == 0 ? 0u : misc->tmem;
+    const VlPlan &pl = misc->plan;
+    const int G = p.Hq / p.Hkv;
+
+    if (!pl.idle) {
+        if (warp < 4) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+            if (warp == 0) {
+                // ---------------------------------------------------------- TMA producer
+                // the whole warp: the lanes share a tile's page look-ups and copies
+                VlWalk walk(pl);
+                VlUnit u;
+                RingPos rp;
+                long loads = 0;
+                bool ok = true;
+                // K and V that one unit alone reads leave L2 first; what several units read stays as usual
+                uint64_t once, again;
+                asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+                asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
+                const int copies = 128 / box;          // of a tile
+                while (ok && walk.next(p, pl, u)) {
+                    const int n = u.t1 - u.t0;
+                    if (n <= 0) continue;
+                    const int la = kSmall || u.ntok <= tpt ? 2 : 1;
+                    const uint64_t policy = walk.s.nr == 1 ? once : again;
+                    const int32_t *trow = p.table + (long)u.b * p.table_stride;
+                    // the lane's page of tile t: looked up a tile ahead, first used (and checked) by its copy
+                    auto page_of = [&](int t) {
+                        const int key = t * 128 + (lane % copies) * box;
+                        return key < u.kv ? __ldg(trow + (p.page_log2 >= 0 ? key >> p.page_log2 : key / p.page_size)) : -1;
+                    };
+                    auto load_tile = [&](bool is_v, int t, int pg) {
+                        if (ok && loads >= slots)
+                            ok = wait_bar(empty_bar(rp.slot), rp.phase ^ 1u, abort_flag, p.fault);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) return;
+                        const uint32_t dst = sRing + rp.slot * L::kTile, bar = full_bar(rp.slot);
+                        const int boxes = min(copies, (u.kv - t * 128 + box - 1) / box);
+                        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * D));
+                        __syncwarp();
+                        if (lane < boxes) {
+                            const int key = t * 128 + lane * box;
+                            if (pg < 0 || pg >= p.n_pages) {      // read as zeros: the copy's fill
+                                set_fault(p.fault, FAULT_BAD_PAGE);
+                                pg = p.n_pages;
+                            }
+                            load_page(dst + lane * box * D, is_v ? &tmap_v : &tmap_k, bar, policy,
+                                      p.page_log2 >= 0 ? key & (p.page_size - 1) : key % p.page_size, u.g, pg);
+                        }
+                        rp.step(slots);
+                        ++loads;
+                    };
+                    int pk = page_of(u.t0), pv = pk;      // pages of the next K tile, of the V tile behind it
+                    int pk2 = 0;
+                    load_tile(false, u.t0, pk);
+                    if (n > 1) pk = page_of(u.t0 + 1);
+                    // V of tile j and K of tile j + la, in the order of use
+                    if (la == 2 && n > 1) {
+                        load_tile(false, u.t0 + 1, pk);
+                        pk2 = pk;
+                        if (n > 2) pk = page_of(u.t0 + 2);
+                    }
+                    for (int j = 0; ok && j < n; ++j) {
+                        load_tile(true, u.t0 + j, pv);
+                        if (la == 2) {
+                            pv = pk2;
+                            if (j + 2 < n) {
+                                load_tile(false, u.t0 + j + 2, pk);
+                                pk2 = pk;
+                                if (j + 3 < n) pk = page_of(u.t0 + j + 3);
+                            }
+                        } else if (j + 1 < n) {
+                            load_tile(false, u.t0 + j + 1, pk);
+                            pv = pk;
+                            if (j + 2 < n) pk = page_of(u.t0 + j + 2);
+                        }
+                    }
+                }
+                // the copies still in flight land before the CTA's shared memory goes
+                if (*abort_flag) {
+                    const int m = (int)min(loads, (long)slots);
+                    RingPos a = rp;
+                    for (int i = 0; i < m; ++i) {
+                        if (a.slot == 0) { a.slot = slots - 1; a.phase ^= 1u; } else --a.slot;
+                        wait_bar(full_bar(a.slot), a.phase, nullptr, p.fault);
+                    }
+                }
+            } else if (warp == 1) {
+                // ---------------------------------------------------------- MMA issuer
+                // the whole warp runs the loop and one elected lane issues: the descriptors are then the
+                // same in every lane for the compiler too and stay in uniform registers (issued from inside
+                // a one-lane branch, the products took twice as long: 4.49 ms against 3.10 for the
+                // 25,119-token prompt)
+                {
+                    const bool el = elect_one();
+                    VlWalk walk(pl);
+                    VlUnit u;
+                    RingPos rp;
+                    uint32_t qphase = 0, pphase[2] = {0, 0}, fphase[2] = {0, 0};
+                    bool used[2] = {false, false};
+                    bool ok = true;
+                    const uint32_t idS = idesc_e4m3(128, 128, false), idO = idesc_e4m3(128, D, true);
+                    auto wait_tile = [&]() {
+                        ok = ok && wait_bar(full_bar(rp.slot), rp.phase, abort_flag, p.fault);
+                        tc_fence_after();
+                    };
+                    // descriptors by their first tile's, moved on by whole 16-byte units: rows of D bytes, 8-row
+                    // groups 8 D bytes apart whatever the copies' size; the products take 32 of their columns
+                    // (Q, K) or 32 of their rows (V) at a time
+                    const uint64_t qd0 = row_desc<D>(sQ), kd0 = row_desc<D>(sRing);
+                    auto issue_s = [&](int i, int qt, int slot) {
+                        const uint64_t qd = qd0 + (uint64_t)(qt * (2 * L::kTile / 16)),
+                                       kd = kd0 + (uint64_t)(slot * (L::kTile / 16));
+                        if (el) {
+#pragma unroll
+                            for (int term = 0; term < 2; ++term)
+#pragma unroll
+                                for (int kk = 0; kk < D / 32; ++kk)
+                                    umma8_ss(tmem + 128u * i, qd + term * (L::kTile / 16) + 2 * kk, kd + 2 * kk, idS,
+                                             term + kk > 0 ? 1u : 0u);
+                            umma_commit(sfull_bar(i));
+                        }
+                    };
+                    auto issue_pv = [&](int i, int slot, bool first, int steps) {
+                        const uint64_t vd = kd0 + (uint64_t)(slot * (L::kTile / 16));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && wait_bar(pfull_bar(i, h), pphase[i], abort_flag, p.fault);
+                            if (!ok) return;
+                            tc_fence_after();
+                            if (el) {
+#pragma unroll
+                                for (int kk = 2 * h; kk < 2 * h + 2; ++kk) {
+                                    if (kSmall && kk >= steps) continue;
+#pragma unroll
+                                    for (int term = 0; term < 2; ++term)
+                                        umma8_ts(tmem + 256u + 128u * i, tmem + 128u * i + 32u * term + 8u * kk,
+                                                 vd + kk * (32 * D / 16), idO, (!first || kk + term > 0) ? 1u : 0u);
+                                }
+                            }
+                        }
+                        pphase[i] ^= 1u;
+                    };
+                    // O_i free for a new unit
+                    auto claim = [&](int i) {
+                        if (used[i]) {
+                            ok = ok && wait_bar(ofree_bar(i), fphase[i], abort_flag, p.fault);
+                            tc_fence_after();
+                            fphase[i] ^= 1u;
+                        }
+                        used[i] = true;
+                    };
+                    while (ok && walk.next(p, pl, u)) {
+                        const int n = u.t1 - u.t0;
+                        if (n <= 0) continue;
+                        const bool pair = !kSmall && u.ntok > tpt;
+                        // the small form's second products stop at the step of 32 that holds the last key
+                        auto steps = [&](int j) { return kSmall ? (u.kv - (u.t0 + j) * 128 + 31) >> 5 : 4; };
+                        ok = wait_bar(qfull_bar, qphase, abort_flag, p.fault);
+                        if (!ok) break;
+                        qphase ^= 1u;
+                        wait_tile();
+                        if (!ok) break;
+                        issue_s(0, 0, rp.slot);
+                        if (pair) issue_s(1, 1, rp.slot);
+                        if (el) umma_commit(empty_bar(rp.slot));
+                        rp.step(slots);
+                        if (pair) {
+                            for (int j = 0; ok && j < n; ++j) {
+                                wait_tile();
+                                if (!ok) break;
+                                const RingPos vp = rp;
+                                rp.step(slots);
+                                if (j == 0) claim(0);
+                                issue_pv(0, vp.slot, j == 0, 4);
+                                if (!ok) break;
+                                if (j + 1 < n) {
+                                    wait_tile();
+                                    if (!ok) break;
+                                    issue_s(0, 0, rp.slot);
+                                } else {
+                                    if (el) umma_commit(ofull_bar(0));
+                                }
+                                if (j == 0) claim(1);
+                                issue_pv(1, vp.slot, j == 0, 4);
+                                if (!ok) break;
+                                if (el) umma_commit(empty_bar(vp.slot));
+                                if (j + 1 < n) {
+                                    issue_s(1, 1, rp.slot);
+                                    if (el) umma_commit(empty_bar(rp.slot));
+                                    rp.step(slots);
+                                } else {
+                                    if (el) umma_commit(ofull_bar(1));
+                                }
+                            }
+                        } else {
+                            if (n > 1) {
+                                wait_tile();
+                                if (!ok) break;
+                                issue_s(1, 0, rp.slot);
+                                if (el) umma_commit(empty_bar(rp.slot));
+                                rp.step(slots);
+                            }
+                            for (int j = 0; ok && j < n; ++j) {
+                                const int i = j & 1;
+                                wait_tile();
+                                if (!ok) break;
+                                if (j < 2) claim(i);
+                                issue_pv(i, rp.slot, j < 2, steps(j));
+                                if (!ok) break;
+                                if (el) umma_commit(empty_bar(rp.slot));
+                                rp.step(slots);
+                                if (j + 2 < n) {
+                                    wait_tile();
+                                    if (!ok) break;
+                                    issue_s(i, 0, rp.slot);
+                                    if (el) umma_commit(empty_bar(rp.slot));
+                                    rp.step(slots);
+                                } else {
+                                    if (el) umma_commit(ofull_bar(i));
+                                }
+                            }
+                        }
+                    }
+                    if (!ok) *abort_flag = 1;
+                }
+                __syncwarp();
+            } else if (warp == 2) {
+                // ---------------------------------------------------------- scales
+                // a tile's K scales, and its V scales against the largest of the stream's so far: four keys a lane,
+                // pages looked up two tiles ahead and scales read one ahead
+                VlWalk walk(pl);
+                VlUnit u;
+                unsigned done = 0;
+                bool ok = true;
+                while (ok && walk.next(p, pl, u)) {
+                    const int n = u.t1 - u.t0;
+                    if (n <= 0) continue;
+                    const bool pair = !kSmall && u.ntok > tpt;
+                    const int32_t *trow = p.table + (long)u.b * p.table_stride;
+                    auto page_of = [&](int j) {
+                        const int key = (u.t0 + j) * 128 + 4 * lane;
+                        return j < n && key < u.kv ? __ldg(trow + (p.page_log2 >= 0 ? key >> p.page_log2 : key / p.page_size)) : -1;
+                    };
+                    float4 ks, vs;
+                    auto fetch = [&](int j, int pg) {
+                        ks = vs = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (pg >= 0 && pg < p.n_pages) {
+                            const int key = (u.t0 + j) * 128 + 4 * lane;
+                            const int in = p.page_log2 >= 0 ? key & (p.page_size - 1) : key % p.page_size;
+                            const long at = ((long)pg * p.Hkv + u.g) * p.page_size + in;
+                            ks = __ldg(reinterpret_cast<const float4 *>(p.k_scale + at));
+                            vs = __ldg(reinterpret_cast<const float4 *>(p.v_scale + at));
+                        }
+                    };
+                    float ref = 0.f, other = 0.f;          // of this tile's stream, and of the one in turn with it
+                    int pg = page_of(1);
+                    fetch(0, page_of(0));
+                    for (int j = 0; j < n; ++j, ++done) {
+                        float4 k4 = ks, v4 = vs;
+                        if (j + 1 < n) fetch(j + 1, pg);
+                        pg = page_of(j + 2);
+                        const int left = u.kv - (u.t0 + j) * 128 - 4 * lane;       // keys of the lane inside the sequence
+                        if (left < 4) {
+                            k4.w = v4.w = 0.f;
+                            if (left < 3) k4.z = v4.z = 0.f;
+                            if (left < 2) k4.y = v4.y = 0.f;
+                            if (left < 1) k4.x = v4.x = 0.f;
+                        }
+                        float top = fmaxf(max3(v4.x, v4.y, v4.z), v4.w);
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float grown = fmaxf(ref, top);
+                        const float ratio = ref == grown ? 1.f : __fdiv_rn(ref, grown);
+                        ref = grown;
+                        const unsigned slot = done % kScaleSlots;
+                        if (done >= kScaleSlots)
+                            ok = wait_bar(scempty_bar(slot), (done / kScaleSlots - 1) & 1u, abort_flag, p.fault);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        Scales &to = scales[slot];
+                        auto share = [&](float v) { return ref > 0.f ? kWeightScale * __fdiv_rn(v, ref) : 0.f; };
+                        reinterpret_cast<float4 *>(to.k)[lane] = k4;
+                        reinterpret_cast<float4 *>(to.v)[lane] = make_float4(share(v4.x), share(v4.y), share(v4.z), share(v4.w));
+                        if (lane == 0) { to.ratio = ratio; to.ref = ref; }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(scfull_bar(slot));
+                        if (!pair) { const float t = ref; ref = other; other = t; }
+                    }
+                }
+            } else if (warp == 3) {
+                vl_ends(p, pl, cta, &misc->ends);
+                asm volatile("bar.arrive 14, 288;" ::: "memory");
+            }
+        } else {
+            // -------------------------------------------------------------- softmax
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+            const int w = (warp - 4) >> 2;             // stream
+            const int r = (tid - 128) & 127;           // row of the tile = tensor-memory lane
+            const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t s_col = tmem + lane_off + 128u * w, o_col = tmem + lane_off + 256u + 128u * w;
+            const int tr = r / G;                      // token of the row within its tile
+            VlWalk walk(pl);
+            VlUnit u;
+            uint32_t sphase = 0, ophase0 = 0, ophase1 = 0;
+            bool have_ends = false;
+            unsigned ring = 0;                         // tiles that went through the ring before this unit
+            unsigned before = 0;                       // and key tiles
+            bool was_pair = false;
+            bool ok = true;
+            while (walk.next(p, pl, u)) {
+                const int n = u.t1 - u.t0;
+                const bool pair = !kSmall && u.ntok > tpt;
+                const int tl = tr + (pair && w ? tpt : 0);             // token within the unit
+                const bool row_ok = tr < tpt && tl < u.ntok;
+                const int lim = row_ok ? vl_limit(p, u, u.tok0 + tl) : 0;
+                const uint64_t word = kTree && row_ok ? vl_tree_word(p, u, tl) : 0;
+                // rows this warp has to do anything for
+                const bool warp_live = __any_sync(0xffffffffu, row_ok);
+                float m_used = -INFINITY, l = 0.f, vref = 0.f, qk = 0.f;
+                // Q in two e4m3 terms.  The tile's last readers are done: a stream's own products have been
+                // waited for, and where both write one tile behind a pair of them, they meet first.
+                if (!pair && was_pair) named_sync(2, 256);
+                was_pair = pair;
+                if (n > 0) {
+                    if (row_ok)
+                        qk = put_query<D>(static_cast<const __nv_bfloat16 *>(p.q) + (long)(u.row0 + tl) * p.q_tok +
+                                              (long)(u.g * G + (r - tr * G)) * p.q_head,
+                                          sbase + (sQ - base) + (pair && w ? 2 * L::kTile : 0), r, pair ? 0 : w, pair ? 2 : 1) *
+                             (p.scale * kLog2e);
+                    qk = qk < 0x1p-126f ? 0x1p-126f : qk;       // (NaN, a row that is not finite, stays)
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(qfull_bar);
+                }
+                const int step = pair ? 1 : 2, la = pair ? 1 : 2;
+                const int j0 = pair ? 0 : w;
+                for (int j = j0; j < n; j += step) {
+                    const int key0 = (u.t0 + j) * 128;
+                    ok = __all_sync(0xffffffffu, wait_bar(sfull_bar(w), sphase, abort_flag, p.fault)) && ok;
+                    sphase ^= 1u;
+                    tc_fence_after();
+                    if (key0 + 128 > u.kv && (!pair || w == 0)) {
+                        // slots past the sequence may hold anything, and 0 times that is not 0:
+                        // one stream, all its warps, clears those rows of the last V tile that its
+                        // product reads before that begins
+                        const int nk = min(la, n);
+                        const unsigned idx = ring + nk + j + min(j, n - nk);
+                        const int slot = (int)(idx % (unsigned)slots);
+                        ok = __all_sync(0xffffffffu, wait_bar(full_bar(slot), (idx / (unsigned)slots) & 1u,
+                                                               abort_flag, p.fault)) && ok;
+                        uint8_t *vt = sbase + (sRing - base) + slot * L::kTile;
+                        const int v0 = u.kv - key0, v1 = kSmall ? (v0 + 31) & ~31 : 128;
+                        for (int i = v0 * (D / 16) + r; i < v1 * (D / 16); i += 128)       // whole rows, in any order
+                            reinterpret_cast<uint4 *>(vt)[i] = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        // every warp's rows, before any arrival lets the product start
+                        named_sync(3 + w, 128);
+                    }
+                    const unsigned tile = before + j, sc = tile % kScaleSlots;
+                    ok = __all_sync(0xffffffffu, wait_bar(scfull_bar(sc), (tile / kScaleSlots) & 1u, abort_flag, p.fault)) && ok;
+                    const Scales &ts = scales[sc];
+                    const float ratio = ts.ratio;
+                    vref = ts.ref;
+                    if (warp_live) {
+                        uint32_t s[4][32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32_async(s_col + 32u * c, s[c]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld_bind(s[c]);
+                        // the keys' scales
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 f = reinterpret_cast<const float4 *>(ts.k)[8 * c + e / 4];
+                                const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                                            make_float2(f.x, f.y));
+                                const float2 y = __fmul2_rn(make_float2(__uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3])),
+                                                            make_float2(f.z, f.w));
+                                s[c][e] = __float_as_uint(x.x); s[c][e + 1] = __float_as_uint(x.y);
+                                s[c][e + 2] = __float_as_uint(y.x); s[c][e + 3] = __float_as_uint(y.y);
+                            }
+                        const int vis = lim - key0;                     // this row sees keys [0, vis) of the tile
+                        if constexpr (kTree) {
+                            if (key0 + 128 > u.off) {                   // the tile holds nodes, or ends behind them
+                                const uint64_t seen[2] = {tree_seen(word, key0 - u.off), tree_seen(word, key0 + 64 - u.off)};
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (!(seen[c >> 1] >> (32 * (c & 1) + e) & 1)) s[c][e] = 0xff800000u;
+                            }
+                        } else if (!__all_sync(0xffffffffu, vis >= 128 || !row_ok)) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (32 * c + e >= vis) s[c][e] = 0xff800000u;
+                        }
+                        const float2 qk2 = make_float2(qk, qk);
+                        float2 ls[2], nm2;
+                        uint32_t hi[16], lo[16];
+                        // weights of 32 keys from 4 `at`: 8 words of each term
+                        auto weights = [&](int at) {
+#pragma unroll
+                            for (int c = at; c < at + 8; ++c) {
+                                const uint32_t *src = s[c >> 3] + 4 * (c & 7);
+                                const float4 f = reinterpret_cast<const float4 *>(ts.v)[c];
+                                const float2 x = __ffma2_rn(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])), qk2, nm2);
+                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(src[2]), __uint_as_float(src[3])), qk2, nm2);
+                                const float2 p0 = make_float2(ex2(x.x), ex2(x.y)), p1 = make_float2(ex2(y.x), ex2(y.y));
+                                ls[0] = __fadd2_rn(ls[0], p0);
+                                ls[1] = __fadd2_rn(ls[1], p1);
+                                const float2 w0 = __fmul2_rn(p0, make_float2(f.x, f.y)), w1 = __fmul2_rn(p1, make_float2(f.z, f.w));
+                                // the first term: the top four bits; the second: what they leave, exact in fp32
+                                const float2 h0 = make_float2(top_bits(w0.x), top_bits(w0.y)), h1 = make_float2(top_bits(w1.x), top_bits(w1.y));
+                                hi[c & 15] = e4m3x4(h0.x, h0.y, h1.x, h1.y);
+                                lo[c & 15] = e4m3x4(w0.x - h0.x, w0.y - h0.y, w1.x - h1.x, w1.y - h1.y);
+                            }
+                        };
+                        float m4[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float m = max3(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]), __uint_as_float(s[i][2]));
+#pragma unroll
+                            for (int e = 3; e < 31; e += 2)
+                                m = max3(m, __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+                            m4[i] = fmaxf(m, __uint_as_float(s[i][31]));
+                        }
+                        const float tmax = qk * fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+                        const bool need = tmax > m_used + kRescale8;    // true at first while m_used = -inf
+                        float alpha = 1.f;
+                        if (need) {
+                            alpha = ex2(m_used - tmax);                 // 0 while nothing is held
+                            m_used = tmax;
+                        }
+                        if (j > j0 && __any_sync(0xffffffffu, need || ratio != 1.f)) {
+                            // S_j is complete, hence every earlier product of this stream too
+                            // (they were issued before it and complete in order)
+                            const float f = alpha * ratio;
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16_async(o_col + 16u * c, o);
+                                tmem_ld_wait();
+                                tmem_ld_bind16(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(o_col + 16u * c, o);
+                            }
+                        }
+                        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                        nm2 = make_float2(neg_m, neg_m);
+                        ls[0] = ls[1] = make_float2(0.f, 0.f);
+                        l *= alpha;
+                        // 64 keys' weights at a time, over the scores' first 64 columns: the first terms in
+                        // columns 0-31, the second in 32-63
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            weights(16 * h);
+                            weights(16 * h + 8);
+                            tmem_st16(s_col + 16u * h, hi);
+                            tmem_st16(s_col + 32u + 16u * h, lo);
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(pfull_bar(w, h));
+                        }
+                        if (lane == 0) mbar_arrive_n(scempty_bar(sc), pair ? 1 : 2);
+                        l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(pfull_bar(w, 0));
+                            mbar_arrive(pfull_bar(w, 1));
+                            mbar_arrive_n(scempty_bar(sc), pair ? 1 : 2);
+                        }
+                    }
+                }
+                // ---- end of the unit: this CTA's rows, normalised, or its part of them
+                const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+                const bool had0 = n > 0, had1 = pair ? n > 0 : n > 1;     // streams that hold anything
+                // A unit of two CTAs: the one that opens it has it last and keeps its part in tensor
+                // memory; the other had it first and left its part in the workspace long ago.  So one
+                // part is written and read instead of two (a batch of prompts shares about two units
+                // per CTA: 256 KB each way).  Units of more CTAs are joined at the end, by all of them.
+                const VlShared *sh = nullptr;
+                if (!whole) {
+                    if (!have_ends) asm volatile("bar.sync 14, 288;" ::: "memory");      // warp 3's answer
+                    have_ends = true;
+                    sh = misc->ends.u + (u.t0 > 0 ? 0 : misc->ends.n - 1);
+                }
+                const bool two = sh && sh->n == 2, keeper = two && u.t0 == 0;
+                const long slot = keeper ? 2L * sh->last : u.t0 == 0 ? 2L * cta + 1 : 2L * cta;
+                unsigned ticket = 0;
+                if (keeper) {
+                    if (tid == 128) {
+                        const bool got = vl_wait(p.ctr + sh->first, 1u + p.wt.extra, p.wt.limit_ns);
+                        if (!got) set_fault(p.fault, FAULT_WAIT_TIMEOUT);
+                        misc->join_flag = got;
+                        ticket = atomicAdd(p.ctr + sh->first, 1u);
+                    }
+                    named_sync(1, 256);
+                    if (tid == 128 && ticket == 1u) atomicExch(p.ctr + sh->first, 0u);
+                }
+                ring += 2 * max(n, 0);
+                before += max(n, 0);
+                float a0 = vref / kWeightScale, a1 = 0.f;
+                if (!pair) {
+                    // join the two streams of the one row tile: they exchange the row's maximum, then
+                    // its sum, and each takes half of the columns of both accumulators
+                    xrow[128 * w + r] = m_used;
+                    if (r == 0) misc->vref[w] = vref / kWeightScale;
+                    named_sync(1, 256);
+                    const float mo = xrow[128 * (w ^ 1) + r];
+                    const float m = fmaxf(m_used, mo), ref = m == -INFINITY ? 0.f : m;
+                    const float own = ex2(m_used - ref), other = ex2(mo - ref);
+                    l *= own;
+                    m_used = m;
+                    a0 = (w == 0 ? own : other) * misc->vref[0];
+                    a1 = (w == 0 ? other : own) * misc->vref[1];
+                    named_sync(2, 256);
+                    xrow[128 * w + r] = l;
+                    named_sync(1, 256);
+                    l += xrow[128 * (w ^ 1) + r];
+                }
+                // each warpgroup follows both barriers' phases; past the exchange above neither can be a unit behind
+                if (pair ? n > 0 && w == 0 : had0)
+                    ok = __all_sync(0xffffffffu, wait_bar(ofull_bar(0), ophase0, abort_flag, p.fault)) && ok;
+                if (pair ? n > 0 && w == 1 : had1)
+                    ok = __all_sync(0xffffffffu, wait_bar(ofull_bar(1), ophase1, abort_flag, p.fault)) && ok;
+                if (had0) ophase0 ^= 1u;
+                if (had1) ophase1 ^= 1u;
+                tc_fence_after();
+                if (warp_live) {
+                    const int c0 = pair ? 0 : w * (D / 64), c1 = pair ? D / 32 : c0 + D / 64;
+                    const uint32_t o0 = tmem + lane_off + 256u + (pair ? 128u * w : 0u);
+                    const long prow = 128 * (pair ? w : 0) + r;
+                    const long orow = (long)(u.row0 + tl) * p.Hq + u.g * G + (r - tr * G);
+                    const bool dead = n <= 0;
+                    float a2 = 0.f;                    // weight of the other CTA's part
+                    if (keeper && row_ok) {
+                        const float2 other = __ldcg(p.ml_part + slot * kVarlenTcRows + prow);
+                        const float m = fmaxf(m_used, other.x), ref = m == -INFINITY ? 0.f : m;
+                        const float f = ex2(m_used - ref);
+                        a0 *= f;
+                        a1 *= f;
+                        a2 = ex2(other.x - ref);
+                        l = l * f + a2 * other.y;
+                        if (!misc->join_flag) l = 0.f;
+                    }
+                    const bool write = whole || keeper;
+                    const float inv = write ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                    // (a loop, not unrolled: the code that runs once per unit is fetched once)
+#pragma unroll 1
+                    for (int c = c0; c < c1; ++c) {
+                        uint32_t o[32];
+                        if (!dead) {
+                            tmem_ld32_async(o0 + 32u * c, o);
+                            tmem_ld_wait();
+                            tmem_ld_bind(o);
+                        }
+                        float f[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = dead ? 0.f : __uint_as_float(o[e]) * (a0 * inv);
+                        if (!pair && had1) {
+                            tmem_ld32_async(o0 + 128u + 32u * c, o);
+                            tmem_ld_wait();
+                            tmem_ld_bind(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), a1 * inv, f[e]);
+                        }
+                        if (row_ok && ok) {
+                            float4 *part = reinterpret_cast<float4 *>(p.o_part) +
+                                           (slot * (D / 4) + 8 * c) * kVarlenTcRows + prow;
+                            if (keeper) {
+                                float4 v[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) v[e] = __ldcg(part + e * kVarlenTcRows);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    f[4 * e] = fmaf(v[e].x, a2 * inv, f[4 * e]);
+                                    f[4 * e + 1] = fmaf(v[e].y, a2 * inv, f[4 * e + 1]);
+                                    f[4 * e + 2] = fmaf(v[e].z, a2 * inv, f[4 * e + 2]);
+                                    f[4 * e + 3] = fmaf(v[e].w, a2 * inv, f[4 * e + 3]);
+                                }
+                            }
+                            if (write) {
+                                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + orow * D + 32 * c;
+                                uint32_t v[16];
+#pragma unroll
+                                for (int q = 0; q < 16; ++q) {
+                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
+                                    v[q] = *reinterpret_cast<const uint32_t *>(&b2);
+                                }
+                                // whole 32-byte sectors where the rows allow it
+                                if (p.out32) {
+                                    store_32b(dst, v);
+                                    store_32b(dst + 16, v + 8);
+                                } else {
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+                                        *reinterpret_cast<uint4 *>(dst + 8 * q) =
+                                            make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    __stcg(part + (e / 4) * kVarlenTcRows, make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]));
+                            }
+                        }
+                    }
+                    if (row_ok && !write && (pair || w == 0))
+                        __stcg(p.ml_part + slot * kVarlenTcRows + prow,
+                               make_float2(ok ? m_used : -INFINITY, ok ? l : 0.f));
+                }
+                if (two && !keeper) {
+                    // announced at once, for the CTA that keeps the other part; should that one have
+                    // given up waiting, the counter goes back to zero here
+                    named_sync(1, 256);
+                    if (tid == 128) {
+                        __threadfence();
+                        unsigned old;
+                        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p.ctr + sh->first)
+                                     : "memory");
+                        if (old == 1u) atomicExch(p.ctr + sh->first, 0u);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (pair) {
+                    if (lane == 0 && n > 0) mbar_arrive(ofree_bar(w));
+                } else {
+                    named_sync(2, 256);                // both warpgroups have read both accumulators
+                    if (lane == 0 && (w == 0 ? had0 : had1)) mbar_arrive(ofree_bar(w));
+                }
+            }
+            // the softmax warps (they hold the registers) join the shared units
+            if (!have_ends) asm volatile("bar.sync 14, 288;" ::: "memory");
+            const VlEnds &ends = misc->ends;
+            named_sync(1, 256);                        // every part of this CTA is written
+            if (tid - 128 < ends.n && ends.u[tid - 128].n > 2) vl_arrive(p, ends.u[tid - 128]);
+            for (int i = 0; i < ends.n; ++i)
+                if (ends.u[i].n > 2) vl_join(p, ends.u[i], tpt, 128, &misc->join_flag, tid - 128, 256, 1);
+        }
+    }
+
+    // every product has been waited for by a softmax warp (or the CTA aborted:
+    // then drain the pipe): free tensor memory
+    __syncthreads();
+    if (warp == 1 && lane == 0 && *abort_flag) {
+        mbar_init(drain_bar, 1);       // used here alone
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        umma_commit(drain_bar);
+        wait_bar(drain_bar, 0, nullptr, p.fault);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <int D, bool kSmall, bool kTree>
+cudaError_t configure8() {
+    // the shared-memory limit, and the registers that the warps share out
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, attn_varlen_tc8_kernel<D, kSmall, kTree>);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;   // setmaxnreg would wait for registers that are not there
+    e = cudaFuncSetAttribute(attn_varlen_tc8_kernel<D, kSmall, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Lay8<D>::kSmem);
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+template <int D, bool kSmall, bool kTree>
+cudaError_t launch_tc8(const VarlenParams &p, int grid, cudaStream_t st) {
+    const int tpt = 128 / (p.Hq / p.Hkv), box_rows = page_box(p.page_size);
+    alignas(64) CUtensorMap m[2];
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn_vl();
+    if (!fn) return cudaErrorInvalidValue;
+    for (int i = 0; i < 2; ++i) {       // (d, slot, kv head, page): a copy per page
+        const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.page_size, (cuuint64_t)p.Hkv, (cuuint64_t)p.n_pages};
+        const cuuint64_t strides[3] = {(cuuint64_t)p.kv.s, (cuuint64_t)p.kv.h, (cuuint64_t)p.kv.b};
+        const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
+        if (fn(&m[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(i ? p.v : p.k), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    cudaError_t e = configure8<D, kSmall, kTree>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Lay8<D>::kSmem;
+    cfg.stream = st;
+    // the CTAs of a shared unit wait for one another: a cooperative launch makes
+    // them resident together
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, attn_varlen_tc8_kernel<D, kSmall, kTree>, m[0], m[1], p, tpt, box_rows);
+}
+
+template <int D> cudaError_t launch_d(const VarlenParams &p, int grid, cudaStream_t st) {
+    const bool small = p.max_q <= 128 / (p.Hq / p.Hkv);
+    if (p.tree) return small ? launch_tc8<D, true, true>(p, grid, st) : launch_tc8<D, false, true>(p, grid, st);
+    return small ? launch_tc8<D, true, false>(p, grid, st) : launch_tc8<D, false, false>(p, grid, st);
+}
+
+}  // namespace
+
+cudaError_t launch_varlen_tc8(const VarlenParams &p, int grid, cudaStream_t st) {
+    return p.D == 128 ? launch_d<128>(p, grid, st) : launch_d<64>(p, grid, st);
+}
+
+}  // namespace sdv

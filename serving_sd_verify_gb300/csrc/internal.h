@@ -140,6 +140,7 @@ int varlen_generic_rows(const VarlenParams &p);        // rows per unit of the C
 int varlen_max_grid(int path, const VarlenParams &p);  // its CTAs that are resident at once (0: none)
 // grid <= varlen_max_grid(): the CTAs of a shared unit wait for one another
 cudaError_t launch_varlen_tc(const VarlenParams &p, int grid, cudaStream_t st);
+cudaError_t launch_varlen_tc8(const VarlenParams &p, int grid, cudaStream_t st);     // e4m3 pages
 cudaError_t launch_varlen_generic(const VarlenParams &p, int grid, cudaStream_t st);
 
 // Rotary positions, and with them the write of new keys and values to a paged
