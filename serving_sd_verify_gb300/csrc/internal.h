@@ -173,7 +173,7 @@ struct NormRopeParams {
     void *q_out, *k_out;
     long q_tok, q_head, qo_tok, qo_head, k_tok, k_head, ko_tok, ko_head;   // elements; v as k
     const void *wq, *wk;            // null: not normed
-    float eps;
+    float eps, inv_dim;             // 1 / D
     const int32_t *positions;       // axis a of token n at a * pos_stride + n; null: the cache position (append only)
     long pos_stride;
     const uint64_t *turns;          // [rot / 2]
