@@ -15,8 +15,8 @@
 //     power's inverse times scale log2(e).
 //   v: the largest v_n of the stream's tiles so far; the weights of values that are
 //     small against others' are small.  Where it grows, O is rescaled as where m does.
-//   W: 64 W_n in two e4m3 terms, the top four bits and the nearest to the rest: off by
-//     2^-8 of itself, or by 2^-15 of the reference where it is small.  m moves where
+//   W: 64 W_n in two e4m3 terms, the second what the first leaves: off by 2^-9 of
+//     itself, or by 2^-16 of the reference where it is small.  m moves where
 //     the maximum grows by more than 2^2 (2^16 in bf16), so 64 W_n stays below 448.
 // l takes P before any rounding.
 //
@@ -114,8 +114,6 @@ template <int D> __device__ __forceinline__ uint64_t row_desc(uint32_t saddr) {
 template <int D> __device__ __forceinline__ uint32_t row_off(int r, int c) {
     return D == 128 ? sw128_off(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
-
-__device__ __forceinline__ float top_bits(float x) { return __uint_as_float(__float_as_uint(x) & 0xfff00000u); }
 
 // Row r of the Q tile at `tile` (the second term's tile behind the first's): part
 // `part` of its columns (halves, or all of them where parts is 2), in two terms.
@@ -621,23 +619,37 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         const float2 qk2 = make_float2(qk, qk);
                         float2 ls[2], nm2;
                         uint32_t hi[16], lo[16];
-                        // weights of 32 keys from 4 `at`: 8 words of each term
-                        auto weights = [&](int at) {
+                        // weights of 32 keys, the scores' c-th 32 columns: 8 words of each term; step by step over
+                        // all of them, so that each step's latency is covered by the others' work
+                        auto weights = [&](int c, int to) {
+                            float2 x[16];
 #pragma unroll
-                            for (int c = at; c < at + 8; ++c) {
-                                const uint32_t *src = s[c >> 3] + 4 * (c & 7);
-                                const float4 f = reinterpret_cast<const float4 *>(ts.v)[c];
-                                const float2 x = __ffma2_rn(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])), qk2, nm2);
-                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(src[2]), __uint_as_float(src[3])), qk2, nm2);
-                                const float2 p0 = make_float2(ex2(x.x), ex2(x.y)), p1 = make_float2(ex2(y.x), ex2(y.y));
-                                ls[0] = __fadd2_rn(ls[0], p0);
-                                ls[1] = __fadd2_rn(ls[1], p1);
-                                const float2 w0 = __fmul2_rn(p0, make_float2(f.x, f.y)), w1 = __fmul2_rn(p1, make_float2(f.z, f.w));
-                                // the first term: the top four bits; the second: what they leave, exact in fp32
-                                const float2 h0 = make_float2(top_bits(w0.x), top_bits(w0.y)), h1 = make_float2(top_bits(w1.x), top_bits(w1.y));
-                                hi[c & 15] = e4m3x4(h0.x, h0.y, h1.x, h1.y);
-                                lo[c & 15] = e4m3x4(w0.x - h0.x, w0.y - h0.y, w1.x - h1.x, w1.y - h1.y);
+                            for (int e = 0; e < 16; ++e)
+                                x[e] = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), qk2, nm2);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) x[e] = make_float2(ex2(x[e].x), ex2(x[e].y));
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ls[e & 1] = __fadd2_rn(ls[e & 1], x[e]);
+                            __half2 v[16];
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float4 f = reinterpret_cast<const float4 *>(ts.v)[8 * c + e / 2];
+                                const float2 w0 = __fmul2_rn(x[e], make_float2(f.x, f.y)), w1 = __fmul2_rn(x[e + 1], make_float2(f.z, f.w));
+                                // (in f16, 2^-12 off; the first term's rest is exact there)
+                                v[e] = __floats2half2_rn(w0.x, w0.y);
+                                v[e + 1] = __floats2half2_rn(w1.x, w1.y);
                             }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) hi[to + e] = e4m3x4(v[2 * e], v[2 * e + 1]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                __half2 h0, h1;
+                                halves_of_e4m3x4(hi[to + e], h0, h1);
+                                v[2 * e] = __hsub2(v[2 * e], h0);
+                                v[2 * e + 1] = __hsub2(v[2 * e + 1], h1);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) lo[to + e] = e4m3x4(v[2 * e], v[2 * e + 1]);
                         };
                         float m4[4];
 #pragma unroll
@@ -678,8 +690,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         // columns 0-31, the second in 32-63
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            weights(16 * h);
-                            weights(16 * h + 8);
+                            weights(2 * h, 0);
+                            weights(2 * h + 1, 8);
                             tmem_st16(s_col + 16u * h, hi);
                             tmem_st16(s_col + 32u + 16u * h, lo);
                             tmem_st_wait();
