@@ -51,6 +51,14 @@ struct Misc8 : Misc {
 };
 static_assert(sizeof(Misc8) <= 512, "the misc area");
 
+// a softmax warp's place in its CTA's units
+struct Walk8 {
+    VlWalk walk;
+    VlUnit u;
+    int more;
+};
+constexpr int kSoftmaxWarps = 8;
+
 template <int D> struct Lay8 {
     static constexpr int kTile = 128 * D;                  // one term of Q, K or V: 128 rows of D bytes
     static constexpr int kSlots = D == 128 ? 9 : 16;
@@ -63,7 +71,8 @@ template <int D> struct Lay8 {
     static constexpr int kBars = 2 * kMaxSlots + 2 + 2 + 4 + 2 + 2 + 2 * kScaleSlots;
     static constexpr int kOffMl = kOffBar + 8 * kBars;     // [2][128] exchange between the streams
     static constexpr int kOffMisc = kOffMl + 2 * 128 * 4;
-    static constexpr int kSmem = kOffMisc + 512 + 1024;    // + alignment slack
+    static constexpr int kOffWalk = kOffMisc + 512;
+    static constexpr int kSmem = kOffWalk + kSoftmaxWarps * (int)sizeof(Walk8) + 1024;    // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     static_assert(kOffBar % 16 == 0 && kOffMl % 16 == 0, "aligned parts");
 };
@@ -517,15 +526,23 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t s_col = tmem + lane_off + 128u * w, o_col = tmem + lane_off + 256u + 128u * w;
             const int tr = r / G;                      // token of the row within its tile
-            VlWalk walk(pl);
-            VlUnit u;
+            // The walk and its unit lie in shared memory, a copy for each warp that its first lane moves on:
+            // registers they would hold are spilled within the tiles' loop, to L2 (shared memory leaves L1
+            // little).
+            Walk8 &wk = reinterpret_cast<Walk8 *>(sbase + L::kOffWalk)[warp - 4];
+            if (lane == 0) wk.walk = VlWalk(pl);
+            const VlUnit &u = wk.u;
             uint32_t sphase = 0, ophase0 = 0, ophase1 = 0;
             bool have_ends = false;
             unsigned ring = 0;                         // tiles that went through the ring before this unit
             unsigned before = 0;                       // and key tiles
             bool was_pair = false;
             bool ok = true;
-            while (walk.next(p, pl, u)) {
+            for (;;) {
+                __syncwarp();
+                if (lane == 0) wk.more = wk.walk.next(p, pl, wk.u);
+                __syncwarp();
+                if (!wk.more) break;
                 const int n = u.t1 - u.t0;
                 const bool pair = !kSmall && u.ntok > tpt;
                 const int tl = tr + (pair && w ? tpt : 0);             // token within the unit

@@ -9,6 +9,7 @@ the shared library has not been built, loading fails loudly.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -504,14 +505,15 @@ def _paged_cache(k_pages, v_pages, page_table, cu_q, kv_len):
     sp, ss, sh, sd = strides
     if sd != 1:
         raise ValueError("the D axis of the cache must be contiguous")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+    cells = page_table.shape
+    if page_table.dtype != torch.int32 or len(cells) != 2:
         raise ValueError("page_table is int32 [B, columns] with contiguous rows")
-    B, cols = page_table.shape
+    B, cols = cells
     row, col = page_table.stride()
     if col != 1:
         raise ValueError("page_table is int32 [B, columns] with contiguous rows")
     _i32_cuda(cu_q, kv_len)
-    if kv_len.dim() != 1 or kv_len.numel() != B or (cu_q is not None and (cu_q.dim() != 1 or cu_q.numel() != B + 1)):
+    if kv_len.shape != (B,) or (cu_q is not None and cu_q.shape != (B + 1,)):
         raise ValueError("cu_q is [B + 1], kv_len [B], and page_table has B rows")
     cache = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), (sp, ss, sh), page_table.data_ptr(), row, cols, pages,
                        page_size)
@@ -636,34 +638,41 @@ def sd_prompt_attention(q, k, v, cu_seqlens, max_len, out, scale, ws, causal=Tru
 # norms, positions of several axes, the 8-bit cache, trees over pages
 # --------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=64)
+def _axes_struct(axes, order):
+    code = ROPE_AXES.get(order)
+    if code is None:
+        raise ValueError(f"axes_order is one of {sorted(ROPE_AXES)}")
+    if not 1 <= len(axes) <= 4:
+        raise ValueError("axes are the pairs of 1 to 4 axes, rot_dim / 2 in all")
+    return RopeAxes(len(axes), axes, code)
+
+
 def _axes_arg(axes, order, half):
     """The C struct of `axes`, the pairs of each (None: one axis); and their number."""
     if axes is None:
         return None, 1
-    code = ROPE_AXES.get(order)
-    if code is None:
-        raise ValueError(f"axes_order is one of {sorted(ROPE_AXES)}")
-    n = len(axes)
-    if not 1 <= n <= 4 or sum(axes) != half:
+    axes = tuple(axes)
+    if sum(axes) != half:
         raise ValueError("axes are the pairs of 1 to 4 axes, rot_dim / 2 in all")
-    return RopeAxes(n, tuple(axes), code), n
+    return _axes_struct(axes, order), len(axes)
 
 
 def _axes_positions(positions, n_axes, N):
     """(pointer, stride between axes) of int32 [N] or [axes, N] positions."""
     if positions is None:
         return None, 0
-    shape = positions.shape
-    if positions.dtype != torch.int32 or shape[-1:] != (N,) or (N > 1 and positions.stride(-1) != 1) or \
-            shape[:-1] != (() if n_axes == 1 and len(shape) == 1 else (n_axes,)):
+    shape, strides = positions.shape, positions.stride()
+    if positions.dtype != torch.int32 or not (shape == (n_axes, N) or (n_axes == 1 and shape == (N,))) or \
+            (N > 1 and strides[-1] != 1):
         raise ValueError("positions is int32 [axes, N] (or [N] for one axis) with contiguous rows")
-    return positions.data_ptr(), positions.stride(0) if len(shape) == 2 else 0
+    return positions.data_ptr(), strides[0]
 
 
 def _norm_weight(w, D, dtype):
     if w is None:
         return None
-    if w.shape != (D,) or w.dtype != dtype or (D > 1 and w.stride(0) != 1):
+    if w.shape != (D,) or w.dtype != dtype or (D > 1 and w.stride() != (1,)):
         raise ValueError("norm weights are contiguous [D] of the rows' dtype")
     return w.data_ptr()
 
@@ -677,10 +686,27 @@ def _page_scales(k_scale, v_scale, k_pages, dtype):
     pages, page_size, Hkv, _ = k_pages.shape
     if k_pages.dtype != torch.float8_e4m3fn:
         raise ValueError("pages with scales are float8_e4m3fn")
-    for s in (k_scale, v_scale):
-        if s is None or s.dtype != torch.float32 or s.shape != (pages, Hkv, page_size) or not s.is_contiguous():
-            raise ValueError("k_scale and v_scale are contiguous fp32 [pages, Hkv, page_size]")
+    want = (pages, Hkv, page_size)
+    if k_scale is None or v_scale is None or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or \
+            k_scale.shape != want or v_scale.shape != want or not (k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("k_scale and v_scale are contiguous fp32 [pages, Hkv, page_size]")
     return PageScales(k_scale.data_ptr(), v_scale.data_ptr())
+
+
+_device_of = torch.Tensor.get_device
+
+
+def _one_device(tensors):
+    """As _on_current_device, of a tuple without None."""
+    found = set(map(_device_of, tensors))
+    dev = found.pop()
+    if found or dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("all tensors must be CUDA tensors on the current device")
+    return dev
+
+
+def _present(*tensors):
+    return tuple(t for t in tensors if t is not None)
 
 
 def sd_norm_rotary(q, q_out, k, k_out, positions, turns, q_weight=None, k_weight=None, eps=1e-6, axes=None,
@@ -688,30 +714,35 @@ def sd_norm_rotary(q, q_out, k, k_out, positions, turns, q_weight=None, k_weight
     """q, q_out [N, Hq, D] and k, k_out [N, Hk, D] (or both None), D contiguous; an
     output may be its input.  positions int32 [axes, N], or [N] for one axis; axes:
     the pairs of each (None: one axis); weights [D] or None (not normed)."""
-    dev = _on_current_device(q, q_out, k, k_out, positions, turns, q_weight, k_weight)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if positions is None:
+        raise ValueError("positions is int32 [axes, N] (or [N] for one axis) with contiguous rows")
+    dev = _one_device((q, q_out, positions, turns) + _present(k, k_out, q_weight, k_weight))
     shape, dtype = q.shape, q.dtype
     N, Hq, D = shape
     lay = _rope_args(turns, None, N, layout)
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out go together")
-    qs, qo = q.stride(), q_out.stride()
-    if q_out.shape != shape or q_out.dtype != dtype or qs[2] != 1 or qo[2] != 1:
+    qt, qh, qd = q.stride()
+    ot, oh, od = q_out.stride()
+    if q_out.shape != shape or q_out.dtype != dtype or qd != 1 or od != 1:
         raise ValueError("q and q_out are [N, Hq, D] of one dtype with contiguous last axes")
-    Hk, kp, ks, kop, ko = 0, None, (0, 0), None, (0, 0)
+    Hk = kt = kh = lt = lh = 0
+    kp = lp = None
     if k is not None:
-        ks, ko, Hk = k.stride(), k_out.stride(), k.shape[1]
-        if k.shape != (N, Hk, D) or k_out.shape != k.shape or k.dtype != dtype or k_out.dtype != dtype or \
-                ks[2] != 1 or ko[2] != 1:
+        ks = k.shape
+        kt, kh, kd = k.stride()
+        lt, lh, ld = k_out.stride()
+        Hk = ks[1]
+        if ks != (N, Hk, D) or k_out.shape != ks or k.dtype != dtype or k_out.dtype != dtype or kd != 1 or ld != 1:
             raise ValueError("k and k_out are [N, Hk, D] of q's dtype with contiguous last axes")
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    ax, n_axes = _axes_arg(axes, axes_order, turns.numel())
-    if positions is None:
-        raise ValueError("positions is int32 [axes, N] (or [N] for one axis) with contiguous rows")
+        kp, lp = k.data_ptr(), k_out.data_ptr()
+    half = turns.numel()
+    ax, n_axes = _axes_arg(axes, axes_order, half)
     pos, pos_stride = _axes_positions(positions, n_axes, N)
-    _check(load().sd_norm_rotary(q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), qo[0], qo[1], kp, ks[0], ks[1], kop, ko[0],
-                                 ko[1], _norm_weight(q_weight, D, dtype), _norm_weight(k_weight, D, dtype), eps, pos,
-                                 pos_stride, ax, turns.data_ptr(), magnitude, N, Hq, Hk, D, 2 * turns.numel(), lay,
-                                 _dt(q), _stream_on(stream, dev)))
+    _check(load().sd_norm_rotary(q.data_ptr(), qt, qh, q_out.data_ptr(), ot, oh, kp, kt, kh, lp, lt, lh,
+                                 _norm_weight(q_weight, D, dtype), _norm_weight(k_weight, D, dtype), eps, pos, pos_stride,
+                                 ax, turns.data_ptr(), magnitude, N, Hq, Hk, D, 2 * half, lay, _dt(q),
+                                 _stream_on(stream, dev)))
 
 
 def sd_norm_rotary_append_paged(q, k, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages,
@@ -720,8 +751,10 @@ def sd_norm_rotary_append_paged(q, k, v, q_out, positions, turns, cu_q, kv_len, 
     """As sd_rotary_append_paged with norms and axes (sd_norm_rotary); positions None:
     every axis takes the cache position.  With k_scale and v_scale (fp32 [pages, Hkv,
     page_size]) the pages are float8_e4m3fn."""
-    dev = _on_current_device(k, q, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages, k_scale,
-                             v_scale, q_weight, k_weight)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    dev = _one_device((k, v, turns, cu_q, kv_len, page_table, k_pages, v_pages) +
+                      _present(q, q_out, positions, k_scale, v_scale, q_weight, k_weight))
     shape, strides, dtype = k.shape, k.stride(), k.dtype
     N, Hkv, D = shape
     lay = _rope_args(turns, None, N, layout)
@@ -731,38 +764,43 @@ def sd_norm_rotary_append_paged(q, k, v, q_out, positions, turns, cu_q, kv_len, 
     if heads != Hkv or dim != D:
         raise ValueError("pages and new rows share heads and head dimension")
     scales = _page_scales(k_scale, v_scale, k_pages, dtype)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
     Hq = qt = qh = 0
+    qp = op = None
     if q is not None:
-        Hq = q.shape[1]
+        qs = q.shape
+        Hq = qs[1]
         qt, qh, qd = q.stride()
-        if q.shape != (N, Hq, D) or q_out.shape != q.shape or qd != 1 or not q_out.is_contiguous() or \
-                q.dtype != dtype or q_out.dtype != dtype:
+        if qs != (N, Hq, D) or q_out.shape != qs or qd != 1 or not q_out.is_contiguous() or q.dtype != dtype or \
+                q_out.dtype != dtype:
             raise ValueError("q and q_out are [N, Hq, D] of k's dtype; q_out contiguous")
-    ax, n_axes = _axes_arg(axes, axes_order, turns.numel())
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    half = turns.numel()
+    ax, n_axes = _axes_arg(axes, axes_order, half)
     pos, pos_stride = _axes_positions(positions, n_axes, N)
     _check(load().sd_norm_rotary_append_paged(
-        _p(q), qt, qh, k.data_ptr(), v.data_ptr(), strides[0], strides[1], _p(q_out), _norm_weight(q_weight, D, dtype),
-        _norm_weight(k_weight, D, dtype), eps, pos, pos_stride, ax, turns.data_ptr(), magnitude, 2 * turns.numel(), lay,
+        qp, qt, qh, k.data_ptr(), v.data_ptr(), strides[0], strides[1], op, _norm_weight(q_weight, D, dtype),
+        _norm_weight(k_weight, D, dtype), eps, pos, pos_stride, ax, turns.data_ptr(), magnitude, 2 * half, lay,
         cu_q.data_ptr(), kv_len.data_ptr(), cache, scales, N, B, Hq, Hkv, D, _dt(k), _stream_on(stream, dev)))
 
 
 def _query_rows(q, out, dim):
+    """(N, Hq, D, strides) of queries whose output is contiguous."""
+    shape = q.shape
     qt, qh, qd = q.stride()
-    if out.shape != q.shape or not out.is_contiguous() or qd != 1 or dim != q.shape[2] or q.dtype != out.dtype:
+    if out.shape != shape or not out.is_contiguous() or qd != 1 or dim != shape[2] or q.dtype != out.dtype:
         raise ValueError("q, out and pages share D; out is contiguous [N, Hq, D] of q's dtype")
-    return qt, qh
+    return *shape, qt, qh
 
 
 def sd_paged_attention_e4m3(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_q, kv_len, max_q, max_kv, out, scale,
                             ws, causal=True, stream=None):
     """As sd_paged_attention over float8_e4m3fn pages with k_scale and v_scale, fp32
     [pages, Hkv, page_size]; ws of sd_paged_attention_workspace_size."""
-    dev = _on_current_device(q, k_pages, v_pages, k_scale, v_scale, page_table, cu_q, kv_len, out, ws)
-    N, Hq, D = q.shape
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale are contiguous fp32 [pages, Hkv, page_size]")
+    dev = _one_device((q, k_pages, v_pages, k_scale, v_scale, page_table, cu_q, kv_len, out, ws))
     cache, B, Hkv, dim = _paged_cache(k_pages, v_pages, page_table, cu_q, kv_len)
-    qt, qh = _query_rows(q, out, dim)
+    N, Hq, D, qt, qh = _query_rows(q, out, dim)
     scales = _page_scales(k_scale, v_scale, k_pages, None)
     _check(load().sd_paged_attention_e4m3(q.data_ptr(), qt, qh, cache, scales, cu_q.data_ptr(), kv_len.data_ptr(), max_q,
                                           max_kv, out.data_ptr(), N, B, Hq, Hkv, D, _dt(q), scale, 1 if causal else 0,
@@ -774,10 +812,9 @@ def sd_paged_tree_attention(q, k_pages, v_pages, page_table, tree_mask, cu_q, kv
     """Attention of drafted trees over a paged cache of q's dtype, or float8_e4m3fn with
     scales: tree_mask int64 [N], bit k of a node's word: it sees its tree's node k;
     max_q <= 64; the rest as sd_paged_attention."""
-    dev = _on_current_device(q, k_pages, v_pages, page_table, tree_mask, cu_q, kv_len, out, ws, k_scale, v_scale)
-    N, Hq, D = q.shape
+    dev = _one_device((q, k_pages, v_pages, page_table, tree_mask, cu_q, kv_len, out, ws) + _present(k_scale, v_scale))
     cache, B, Hkv, dim = _paged_cache(k_pages, v_pages, page_table, cu_q, kv_len)
-    qt, qh = _query_rows(q, out, dim)
+    N, Hq, D, qt, qh = _query_rows(q, out, dim)
     scales = _page_scales(k_scale, v_scale, k_pages, q.dtype)
     if tree_mask.dtype != torch.int64 or tree_mask.shape != (N,) or not tree_mask.is_contiguous():
         raise ValueError("tree_mask is contiguous int64 [N] (one 64-bit mask word per node)")
@@ -790,16 +827,15 @@ def sd_compact_tree_paged(k_pages, v_pages, page_table, ctx_len, path, n_accepte
                           stream=None):
     """As sd_compact_tree_kv in a paged cache (float8_e4m3fn pages with their scales, or
     bf16 / fp32): page_table int32 [B, columns], ctx_len and n_accepted int32 [B], path int32 [B, T]."""
-    dev = _on_current_device(k_pages, v_pages, page_table, ctx_len, path, n_accepted, k_scale, v_scale)
-    _i32_cuda(path, n_accepted)
-    if path.dim() != 2 or ctx_len.dim() != 1 or path.shape[0] != ctx_len.numel() or n_accepted.numel() != ctx_len.numel():
-        raise ValueError("path is [B, T], ctx_len and n_accepted are [B]")
+    dev = _one_device((k_pages, v_pages, page_table, ctx_len, path, n_accepted) + _present(k_scale, v_scale))
     cache, B, Hkv, D = _paged_cache(k_pages, v_pages, page_table, None, ctx_len)
-    quantised = k_scale is not None or v_scale is not None
+    _i32_cuda(path, n_accepted)
+    T = path.shape[-1]
+    if path.shape != (B, T) or n_accepted.numel() != B:
+        raise ValueError("path is [B, T], ctx_len and n_accepted are [B]")
     scales = _page_scales(k_scale, v_scale, k_pages, k_pages.dtype)
-    _check(load().sd_compact_tree_paged(cache, scales, ctx_len.data_ptr(), path.data_ptr(), n_accepted.data_ptr(), B,
-                                        path.shape[1], Hkv, D, SD_BF16 if quantised else _dt(k_pages),
-                                        _stream_on(stream, dev)))
+    _check(load().sd_compact_tree_paged(cache, scales, ctx_len.data_ptr(), path.data_ptr(), n_accepted.data_ptr(), B, T,
+                                        Hkv, D, _dt(k_pages) if scales is None else SD_BF16, _stream_on(stream, dev)))
 
 
 def sd_set_projector_path(path: int) -> int:
