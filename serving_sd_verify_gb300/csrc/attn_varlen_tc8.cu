@@ -87,6 +87,10 @@ __device__ __forceinline__ void load_page(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), SDV_S8(0)
+                 : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
@@ -160,14 +164,21 @@ __device__ __forceinline__ float put_query(const __nv_bfloat16 *q, uint8_t *tile
     return e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ec - 7) << 23);
 }
 
-// kSmall: no sequence has more rows of a kv head than one tile holds: the second
-// row tile's room is ring slots.  kTree: a row sees of its sequence's new tokens
-// those that its mask says.
-template <int D, bool kSmall, bool kTree>
+// kRows: what one unit holds.  kPairs: up to 256 rows.  kSmall: no sequence has more
+// rows of a kv head than one tile holds, and the second row tile's room is ring
+// slots.  kQuad: none has more than 32 (decoding).  Four copies of the rows then lie
+// in the tile's four quarters, and the warp of a quarter sees to 32 of a tile's 128
+// keys: its copies' weights of the others are zero, each copy has a maximum and a sum
+// of its own, and the copies are joined as the streams are.  One warp of a stream
+// would work through 128 keys otherwise, and three sleep.
+// kTree: a row sees of its sequence's new tokens those that its mask says.
+enum Rows8 { kPairs, kSmall8, kQuad8 };
+template <int D, Rows8 kRows, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const VarlenParams p, const int tpt, const int box) {
     using L = Lay8<D>;
+    constexpr bool kSmall = kRows != kPairs, kQuad = kRows == kQuad8;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t base = (raw_u32 + 1023u) & ~1023u;
@@ -525,7 +536,9 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             const int r = (tid - 128) & 127;           // row of the tile = tensor-memory lane
             const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t s_col = tmem + lane_off + 128u * w, o_col = tmem + lane_off + 256u + 128u * w;
-            const int tr = r / G;                      // token of the row within its tile
+            const int quarter = warp & 3;
+            const int ur = kQuad ? lane : r;           // row of the unit's tile
+            const int tr = ur / G;                     // and its token
             // The walk and its unit lie in shared memory, a copy for each warp that its first lane moves on:
             // registers they would hold are spilled within the tiles' loop, to L2 (shared memory leaves L1
             // little).
@@ -559,7 +572,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 if (n > 0) {
                     if (row_ok)
                         qk = put_query<D>(static_cast<const __nv_bfloat16 *>(p.q) + (long)(u.row0 + tl) * p.q_tok +
-                                              (long)(u.g * G + (r - tr * G)) * p.q_head,
+                                              (long)(u.g * G + (ur - tr * G)) * p.q_head,
                                           sbase + (sQ - base) + (pair && w ? 2 * L::kTile : 0), r, pair ? 0 : w, pair ? 2 : 1) *
                              (p.scale * kLog2e);
                     qk = qk < 0x1p-126f ? 0x1p-126f : qk;       // (NaN, a row that is not finite, stays)
@@ -596,7 +609,94 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     const Scales &ts = scales[sc];
                     const float ratio = ts.ratio;
                     vref = ts.ref;
-                    if (warp_live) {
+                    if constexpr (kQuad) {
+                        uint32_t s[32];
+                        tmem_ld32_async(s_col + 32u * quarter, s);
+                        tmem_ld_wait();
+                        tmem_ld_bind(s);
+                        const int from = key0 + 32 * quarter;
+                        uint32_t seen = 0xffffffffu;
+                        if constexpr (kTree) {
+                            seen = (uint32_t)tree_seen(word, from - u.off);
+                        } else {
+                            const int vis = lim - from;
+                            if (vis < 32) seen = vis <= 0 ? 0u : (1u << vis) - 1u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 f = reinterpret_cast<const float4 *>(ts.k)[8 * quarter + e / 4];
+                            s[e] = __float_as_uint(__uint_as_float(s[e]) * f.x);
+                            s[e + 1] = __float_as_uint(__uint_as_float(s[e + 1]) * f.y);
+                            s[e + 2] = __float_as_uint(__uint_as_float(s[e + 2]) * f.z);
+                            s[e + 3] = __float_as_uint(__uint_as_float(s[e + 3]) * f.w);
+                        }
+                        if (!__all_sync(0xffffffffu, seen == 0xffffffffu || !row_ok)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1)) s[e] = 0xff800000u;
+                        }
+                        float m = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+                        float m2 = fmaxf(__uint_as_float(s[3]), __uint_as_float(s[31]));
+#pragma unroll
+                        for (int e = 4; e < 16; e += 2) m = max3(m, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+#pragma unroll
+                        for (int e = 16; e < 30; e += 2) m2 = max3(m2, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                        const float tmax = qk * max3(m, m2, __uint_as_float(s[30]));
+                        const bool need = row_ok && tmax > m_used + kRescale8;
+                        float alpha = 1.f;
+                        if (need) {
+                            alpha = ex2(m_used - tmax);
+                            m_used = tmax;
+                        }
+                        if (j > j0 && __any_sync(0xffffffffu, need || ratio != 1.f)) {
+                            const float f = alpha * ratio;
+                            uint32_t o[D / 32][32];
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) tmem_ld32_async(o_col + 32u * c, o[c]);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                tmem_ld_bind(o[c]);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[c][e] = __float_as_uint(__uint_as_float(o[c][e]) * f);
+                                tmem_st32(o_col + 32u * c, o[c]);
+                            }
+                        }
+                        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                        float ls[2] = {0.f, 0.f};
+                        uint32_t hi[8], lo[8];
+                        const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                        for (int c = 0; c < 4; ++c)
+                            if (c != quarter) {
+                                tmem_st8(s_col + 8u * c, none);
+                                tmem_st8(s_col + 32u + 8u * c, none);
+                            }
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) {
+                            const float4 f = reinterpret_cast<const float4 *>(ts.v)[8 * quarter + g];
+                            float x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[e] = ex2(fmaf(__uint_as_float(s[4 * g + e]), qk, neg_m));
+                            ls[0] += x[0] + x[2];
+                            ls[1] += x[1] + x[3];
+                            const __half2 v0 = __floats2half2_rn(x[0] * f.x, x[1] * f.y), v1 = __floats2half2_rn(x[2] * f.z, x[3] * f.w);
+                            __half2 h0, h1;
+                            hi[g] = e4m3x4(v0, v1);
+                            halves_of_e4m3x4(hi[g], h0, h1);
+                            lo[g] = e4m3x4(__hsub2(v0, h0), __hsub2(v1, h1));
+                        }
+                        tmem_st8(s_col + 8u * quarter, hi);
+                        tmem_st8(s_col + 32u + 8u * quarter, lo);
+                        l = l * alpha + (ls[0] + ls[1]);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(pfull_bar(w, 0));
+                            mbar_arrive(pfull_bar(w, 1));
+                            mbar_arrive_n(scempty_bar(sc), 2);
+                        }
+                    } else if (warp_live) {
                         uint32_t s[4][32];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_ld32_async(s_col + 32u * c, s[c]);
@@ -764,7 +864,12 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     if (r == 0) misc->vref[w] = vref / kWeightScale;
                     named_sync(1, 256);
                     const float mo = xrow[128 * (w ^ 1) + r];
-                    const float m = fmaxf(m_used, mo), ref = m == -INFINITY ? 0.f : m;
+                    float m = fmaxf(m_used, mo);
+                    if (kQuad) {                       // and of the other copies
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) m = fmaxf(m, xrow[32 * c + lane]);
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
                     const float own = ex2(m_used - ref), other = ex2(mo - ref);
                     l *= own;
                     m_used = m;
@@ -773,7 +878,13 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     named_sync(2, 256);
                     xrow[128 * w + r] = l;
                     named_sync(1, 256);
-                    l += xrow[128 * (w ^ 1) + r];
+                    if (kQuad) {
+                        l = 0.f;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) l += xrow[32 * c + lane];
+                    } else {
+                        l += xrow[128 * (w ^ 1) + r];
+                    }
                 }
                 // each warpgroup follows both barriers' phases; past the exchange above neither can be a unit behind
                 if (pair ? n > 0 && w == 0 : had0)
@@ -786,8 +897,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 if (warp_live) {
                     const int c0 = pair ? 0 : w * (D / 64), c1 = pair ? D / 32 : c0 + D / 64;
                     const uint32_t o0 = tmem + lane_off + 256u + (pair ? 128u * w : 0u);
-                    const long prow = 128 * (pair ? w : 0) + r;
-                    const long orow = (long)(u.row0 + tl) * p.Hq + u.g * G + (r - tr * G);
+                    const long prow = 128 * (pair ? w : 0) + ur;
+                    const long orow = (long)(u.row0 + tl) * p.Hq + u.g * G + (ur - tr * G);
                     const bool dead = n <= 0;
                     float a2 = 0.f;                    // weight of the other CTA's part
                     if (keeper && row_ok) {
@@ -802,6 +913,53 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     }
                     const bool write = whole || keeper;
                     const float inv = write ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                    if constexpr (kQuad) {
+                        // 16 columns at a time: the copies' shares meet in the room of Q (its last product is
+                        // done), and the warp of a quarter sums and writes four of the columns
+                        float4 *meet = reinterpret_cast<float4 *>(sbase + (sQ - base)) + w * (4 * 4 * 32);
+#pragma unroll 1
+                        for (int c = w * (D / 32); c < (w + 1) * (D / 32); ++c) {
+                            float f[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) f[e] = 0.f;
+                            uint32_t o[16];
+                            if (!dead) {
+                                tmem_ld16_async(o0 + 16u * c, o);
+                                tmem_ld_wait();
+                                tmem_ld_bind16(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) f[e] = __uint_as_float(o[e]) * a0;
+                            }
+                            if (had1) {
+                                tmem_ld16_async(o0 + 128u + 16u * c, o);
+                                tmem_ld_wait();
+                                tmem_ld_bind16(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) f[e] = fmaf(__uint_as_float(o[e]), a1, f[e]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                meet[(quarter * 4 + e) * 32 + lane] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                            named_sync(3 + w, 128);
+                            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 y = meet[(e * 4 + quarter) * 32 + lane];
+                                x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                            }
+                            named_sync(3 + w, 128);    // read, before the next columns go there
+                            if (row_ok && ok) {
+                                float4 *at = reinterpret_cast<float4 *>(p.o_part) + (slot * (D / 4) + 4 * c + quarter) * kVarlenTcRows + prow;
+                                if (keeper) {
+                                    const float4 y = __ldcg(at);
+                                    x.x = fmaf(y.x, a2, x.x); x.y = fmaf(y.y, a2, x.y);
+                                    x.z = fmaf(y.z, a2, x.z); x.w = fmaf(y.w, a2, x.w);
+                                }
+                                if (write) vl_store4(p, orow, 4 * c + quarter, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+                                else __stcg(at, x);
+                            }
+                        }
+                    } else
                     // (a loop, not unrolled: the code that runs once per unit is fetched once)
 #pragma unroll 1
                     for (int c = c0; c < c1; ++c) {
@@ -861,7 +1019,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             }
                         }
                     }
-                    if (row_ok && !write && (pair || w == 0))
+                    if (row_ok && !write && (pair || w == 0) && (!kQuad || quarter == 0))
                         __stcg(p.ml_part + slot * kVarlenTcRows + prow,
                                make_float2(ok ? m_used : -INFINITY, ok ? l : 0.f));
                 }
@@ -916,7 +1074,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int D, bool kSmall, bool kTree>
+template <int D, Rows8 kRows, bool kTree>
 cudaError_t configure8() {
     // the shared-memory limit, and the registers that the warps share out
     static std::atomic<bool> done[kMaxDevices];
@@ -925,16 +1083,16 @@ cudaError_t configure8() {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
     cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, attn_varlen_tc8_kernel<D, kSmall, kTree>);
+    e = cudaFuncGetAttributes(&a, attn_varlen_tc8_kernel<D, kRows, kTree>);
     if (e != cudaSuccess) return e;
     if (a.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;   // setmaxnreg would wait for registers that are not there
-    e = cudaFuncSetAttribute(attn_varlen_tc8_kernel<D, kSmall, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_varlen_tc8_kernel<D, kRows, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Lay8<D>::kSmem);
     if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
     return e;
 }
 
-template <int D, bool kSmall, bool kTree>
+template <int D, Rows8 kRows, bool kTree>
 cudaError_t launch_tc8(const VarlenParams &p, int grid, cudaStream_t st) {
     const int tpt = 128 / (p.Hq / p.Hkv), box_rows = page_box(p.page_size);
     alignas(64) CUtensorMap m[2];
@@ -949,7 +1107,7 @@ cudaError_t launch_tc8(const VarlenParams &p, int grid, cudaStream_t st) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    cudaError_t e = configure8<D, kSmall, kTree>();
+    cudaError_t e = configure8<D, kRows, kTree>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -965,13 +1123,16 @@ cudaError_t launch_tc8(const VarlenParams &p, int grid, cudaStream_t st) {
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attn_varlen_tc8_kernel<D, kSmall, kTree>, m[0], m[1], p, tpt, box_rows);
+    return cudaLaunchKernelEx(&cfg, attn_varlen_tc8_kernel<D, kRows, kTree>, m[0], m[1], p, tpt, box_rows);
 }
 
+template <int D, bool kTree> cudaError_t launch_rows8(const VarlenParams &p, int grid, cudaStream_t st) {
+    const int G = p.Hq / p.Hkv;
+    if (p.max_q * G <= 32) return launch_tc8<D, kQuad8, kTree>(p, grid, st);
+    return p.max_q <= 128 / G ? launch_tc8<D, kSmall8, kTree>(p, grid, st) : launch_tc8<D, kPairs, kTree>(p, grid, st);
+}
 template <int D> cudaError_t launch_d(const VarlenParams &p, int grid, cudaStream_t st) {
-    const bool small = p.max_q <= 128 / (p.Hq / p.Hkv);
-    if (p.tree) return small ? launch_tc8<D, true, true>(p, grid, st) : launch_tc8<D, false, true>(p, grid, st);
-    return small ? launch_tc8<D, true, false>(p, grid, st) : launch_tc8<D, false, false>(p, grid, st);
+    return p.tree ? launch_rows8<D, true>(p, grid, st) : launch_rows8<D, false>(p, grid, st);
 }
 
 }  // namespace

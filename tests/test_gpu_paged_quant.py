@@ -208,6 +208,20 @@ def test_long_caches_are_shared_among_ctas(S, dtype, path, q_lens, kv_lens):
                  quantised=quantised)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(28, 4, 128), (8, 8, 64), (32, 1, 128), (16, 1, 64), (4, 2, 128)])
+def test_few_rows(S, Hq, Hkv, D):
+    """At most 32 rows of a kv head: decoding, a few drafted tokens, small trees; short and shared among many CTAs."""
+    n = max(1, 32 // (Hq // Hkv))
+    g = torch.Generator().manual_seed(Hq)
+    for q_lens, kv_lens in (([n], [n]), ([1, n, 0, 1], [1, 130, 7, 64]), ([1] * 9, [31, 32, 33, 127, 128, 129, 160, 161, 300]),
+                            ([n, 1], [9000, 5000])):
+        for page in (8, 64):
+            case(S, q_lens, kv_lens, Hq, Hkv, D, torch.bfloat16, page, seed=n)
+            assert S.sd_last_attention_path()[0] == 2
+        case(S, q_lens, kv_lens, Hq, Hkv, D, torch.bfloat16, 16, seed=n, causal=False)
+        case(S, q_lens, kv_lens, Hq, Hkv, D, torch.bfloat16, 16, seed=n, tree=True)
+
+
 @pytest.mark.parametrize("path", [1, 0])
 def test_sharp_weights_and_uneven_rows(S, path):
     """Scores of +-60, and rows whose scales differ by many powers of two."""
