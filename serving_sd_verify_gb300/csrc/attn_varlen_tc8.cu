@@ -51,13 +51,16 @@ struct Misc8 : Misc {
 };
 static_assert(sizeof(Misc8) <= 512, "the misc area");
 
-// a softmax warp's place in its CTA's units
-struct Walk8 {
-    VlWalk walk;
+// The CTA's units, worked out by warp 3 ahead of everyone (each role's own walk would be on its way at
+// every unit, and four copies of its code in the instruction cache).  Softmax warps read theirs here
+// throughout: registers it would hold are spilled within the tiles' loop, to L2 (shared memory leaves
+// L1 little).
+struct Unit8 {
     VlUnit u;
-    int more;
+    int more;           // 0: the last unit was the one before
+    int alone;          // its sequence's only unit of a kv head
 };
-constexpr int kSoftmaxWarps = 8;
+constexpr int kUnitSlots = 4, kUnitReaders = 3 + 8;      // warps 0 to 2, and the softmax warps
 
 template <int D> struct Lay8 {
     static constexpr int kTile = 128 * D;                  // one term of Q, K or V: 128 rows of D bytes
@@ -67,12 +70,12 @@ template <int D> struct Lay8 {
     static constexpr int kMaxSlots = kSlots + 2;           // where no unit has a second row tile, its room too
     static constexpr int kOffScale = kOffRing + kSlots * kTile;
     static constexpr int kOffBar = kOffScale + kScaleSlots * (int)sizeof(Scales);
-    // full[max] empty[max] qfull drain sfull[2] pfull[2][2] ofull[2] ofree[2] scfull[] scempty[]
-    static constexpr int kBars = 2 * kMaxSlots + 2 + 2 + 4 + 2 + 2 + 2 * kScaleSlots;
+    // full[max] empty[max] qfull drain sfull[2] pfull[2][2] ofull[2] ofree[2] scfull[] scempty[] ufull[] uempty[]
+    static constexpr int kBars = 2 * kMaxSlots + 2 + 2 + 4 + 2 + 2 + 2 * kScaleSlots + 2 * kUnitSlots;
     static constexpr int kOffMl = kOffBar + 8 * kBars;     // [2][128] exchange between the streams
     static constexpr int kOffMisc = kOffMl + 2 * 128 * 4;
-    static constexpr int kOffWalk = kOffMisc + 512;
-    static constexpr int kSmem = kOffWalk + kSoftmaxWarps * (int)sizeof(Walk8) + 1024;    // + alignment slack
+    static constexpr int kOffUnits = kOffMisc + 512;
+    static constexpr int kSmem = kOffUnits + kUnitSlots * (int)sizeof(Unit8) + 1024;    // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     static_assert(kOffBar % 16 == 0 && kOffMl % 16 == 0, "aligned parts");
 };
@@ -128,32 +131,31 @@ template <int D> __device__ __forceinline__ uint32_t row_off(int r, int c) {
     return D == 128 ? sw128_off(r, c) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// Row r of the Q tile at `tile` (the second term's tile behind the first's): part
-// `part` of its columns (halves, or all of them where parts is 2), in two terms.
+// Row r of the Q tile at `tile` (the second term's tile behind the first's): the
+// part-th of `parts` equal shares of its columns, in two terms.
 // Returns what the products have to be multiplied by.
 template <int D>
 __device__ __forceinline__ float put_query(const __nv_bfloat16 *q, uint8_t *tile, int r, int part, int parts) {
-    uint4 v[D / 8];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(q) + i);
     uint32_t top = 0;                                  // the largest magnitudes, as pairs of bit patterns
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-        top = __vmaxu2(__vmaxu2(__vmaxu2(top, v[i].x & 0x7fff7fffu), __vmaxu2(v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu)),
-                       v[i].w & 0x7fff7fffu);
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+        top = __vmaxu2(__vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu)),
+                       v.w & 0x7fff7fffu);
+    }
     const int e = (int)(max(top & 0xffffu, top >> 16) >> 7);          // the largest element's biased exponent
     const int ec = max(e, 8);                          // (rows below 2^-119 keep their order of size, not their last bits)
     const float mul = __uint_as_float((uint32_t)(261 - ec) << 23);    // 2^(134 - ec): the largest to [2^7, 2^8)
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {                 // 16 elements, one chunk of each term
-        if (parts == 1 && i / (D / 32) != part) continue;
-        const uint32_t src[8] = {v[2 * i].x, v[2 * i].y, v[2 * i].z, v[2 * i].w,
-                                 v[2 * i + 1].x, v[2 * i + 1].y, v[2 * i + 1].z, v[2 * i + 1].w};
+    const int per = (D / 16) / parts;                  // chunks of 16 elements, read again from L1
+#pragma unroll 1
+    for (int i = part * per; i < (part + 1) * per; ++i) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(q) + 2 * i), b = __ldg(reinterpret_cast<const uint4 *>(q) + 2 * i + 1);
+        const uint32_t src[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float f[4] = {__uint_as_float(src[2 * j] << 16) * mul, __uint_as_float(src[2 * j] & 0xffff0000u) * mul,
-                          __uint_as_float(src[2 * j + 1] << 16) * mul, __uint_as_float(src[2 * j + 1] & 0xffff0000u) * mul};
+            const float f[4] = {__uint_as_float(src[2 * j] << 16) * mul, __uint_as_float(src[2 * j] & 0xffff0000u) * mul,
+                                __uint_as_float(src[2 * j + 1] << 16) * mul, __uint_as_float(src[2 * j + 1] & 0xffff0000u) * mul};
             hi[j] = e4m3x4(f[0], f[1], f[2], f[3]);
             const float4 h = from_e4m3x4(hi[j]);
             lo[j] = e4m3x4(f[0] - h.x, f[1] - h.y, f[2] - h.z, f[3] - h.w);
@@ -198,6 +200,19 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     auto ofree_bar = [&](int i) { return bar1 + 8u * (10 + i); };            // O_i read out (4 warps)
     auto scfull_bar = [&](int i) { return bar1 + 8u * (12 + i); };           // scales written
     auto scempty_bar = [&](int i) { return bar1 + 8u * (12 + kScaleSlots + i); };   // and read (8 warps, or 4 twice)
+    auto ufull_bar = [&](int i) { return bar1 + 8u * (12 + 2 * kScaleSlots + i); };
+    auto uempty_bar = [&](int i) { return bar1 + 8u * (12 + 2 * kScaleSlots + kUnitSlots + i); };
+    Unit8 *units = reinterpret_cast<Unit8 *>(sbase + L::kOffUnits);
+    // The next unit, false behind the last.  Every warp goes through all of them, whatever it gave up:
+    // these waits end because the others' do.
+    int uslot = 0;
+    uint32_t uphase = 0;
+    auto next_unit = [&]() { return wait_bar(ufull_bar(uslot), uphase, nullptr, p.fault) && units[uslot].more != 0; };
+    auto done_unit = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(uempty_bar(uslot));
+        if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
+    };
     Scales *scales = reinterpret_cast<Scales *>(sbase + L::kOffScale);
     float *xrow = reinterpret_cast<float *>(sbase + L::kOffMl);      // [2][128]: one value per stream and row
     Misc8 *misc = reinterpret_cast<Misc8 *>(sbase + L::kOffMisc);
@@ -206,6 +221,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     if (tid == 0) {
         for (int i = 0; i < L::kMaxSlots; ++i) { mbar_init(full_bar(i), 1); mbar_init(empty_bar(i), 1); }
         mbar_init(qfull_bar, 8);
+        for (int i = 0; i < kUnitSlots; ++i) { mbar_init(ufull_bar(i), 1); mbar_init(uempty_bar(i), kUnitReaders); }
         for (int i = 0; i < kScaleSlots; ++i) { mbar_init(scfull_bar(i), 1); mbar_init(scempty_bar(i), 8); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sfull_bar(i), 1);
@@ -245,8 +261,6 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             if (warp == 0) {
                 // ---------------------------------------------------------- TMA producer
                 // the whole warp: the lanes share a tile's page look-ups and copies
-                VlWalk walk(pl);
-                VlUnit u;
                 RingPos rp;
                 long loads = 0;
                 bool ok = true;
@@ -255,11 +269,13 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
                 asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
                 const int copies = 128 / box;          // of a tile
-                while (ok && walk.next(p, pl, u)) {
+                while (next_unit()) {
+                    const VlUnit u = units[uslot].u;
+                    const uint64_t policy = units[uslot].alone ? once : again;
+                    done_unit();
                     const int n = u.t1 - u.t0;
-                    if (n <= 0) continue;
+                    if (n <= 0 || !ok) continue;
                     const int la = kSmall || u.ntok <= tpt ? 2 : 1;
-                    const uint64_t policy = walk.s.nr == 1 ? once : again;
                     const int32_t *trow = p.table + (long)u.b * p.table_stride;
                     // the lane's page of tile t: looked up a tile ahead, first used (and checked) by its copy
                     auto page_of = [&](int t) {
@@ -330,8 +346,6 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 // 25,119-token prompt)
                 {
                     const bool el = elect_one();
-                    VlWalk walk(pl);
-                    VlUnit u;
                     RingPos rp;
                     uint32_t qphase = 0, pphase[2] = {0, 0}, fphase[2] = {0, 0};
                     bool used[2] = {false, false};
@@ -387,17 +401,18 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         }
                         used[i] = true;
                     };
-                    while (ok && walk.next(p, pl, u)) {
+                    while (next_unit()) {
+                        const VlUnit u = units[uslot].u;
+                        done_unit();
                         const int n = u.t1 - u.t0;
-                        if (n <= 0) continue;
+                        if (n <= 0 || !ok) continue;
                         const bool pair = !kSmall && u.ntok > tpt;
                         // the small form's second products stop at the step of 32 that holds the last key
                         auto steps = [&](int j) { return kSmall ? (u.kv - (u.t0 + j) * 128 + 31) >> 5 : 4; };
                         ok = wait_bar(qfull_bar, qphase, abort_flag, p.fault);
-                        if (!ok) break;
                         qphase ^= 1u;
                         wait_tile();
-                        if (!ok) break;
+                        if (!ok) continue;
                         issue_s(0, 0, rp.slot);
                         if (pair) issue_s(1, 1, rp.slot);
                         if (el) umma_commit(empty_bar(rp.slot));
@@ -433,7 +448,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         } else {
                             if (n > 1) {
                                 wait_tile();
-                                if (!ok) break;
+                                if (!ok) continue;
                                 issue_s(1, 0, rp.slot);
                                 if (el) umma_commit(empty_bar(rp.slot));
                                 rp.step(slots);
@@ -459,20 +474,19 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             }
                         }
                     }
-                    if (!ok) *abort_flag = 1;
                 }
                 __syncwarp();
             } else if (warp == 2) {
                 // ---------------------------------------------------------- scales
                 // a tile's K scales, and its V scales against the largest of the stream's so far: four keys a lane,
                 // pages looked up two tiles ahead and scales read one ahead
-                VlWalk walk(pl);
-                VlUnit u;
                 unsigned done = 0;
                 bool ok = true;
-                while (ok && walk.next(p, pl, u)) {
+                while (next_unit()) {
+                    const VlUnit u = units[uslot].u;
+                    done_unit();
                     const int n = u.t1 - u.t0;
-                    if (n <= 0) continue;
+                    if (n <= 0 || !ok) continue;
                     const bool pair = !kSmall && u.ntok > tpt;
                     const int32_t *trow = p.table + (long)u.b * p.table_stride;
                     auto page_of = [&](int j) {
@@ -526,8 +540,30 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     }
                 }
             } else if (warp == 3) {
-                vl_ends(p, pl, cta, &misc->ends);
-                asm volatile("bar.arrive 14, 288;" ::: "memory");
+                VlWalk walk(pl);
+                bool more = true;
+                for (int i = 0; more; ++i) {
+                    if (i == kUnitSlots) {         // (the first units go out first)
+                        vl_ends(p, pl, cta, &misc->ends);
+                        asm volatile("bar.arrive 14, 288;" ::: "memory");
+                    }
+                    VlUnit u;
+                    more = walk.next(p, pl, u);
+                    if (i >= kUnitSlots) wait_bar(uempty_bar(uslot), uphase ^ 1u, nullptr, p.fault);
+                    Unit8 &to = units[uslot];
+                    if (lane == 0) {
+                        to.u = u;
+                        to.more = more;
+                        to.alone = walk.s.nr == 1;
+                        mbar_arrive(ufull_bar(uslot));
+                    }
+                    __syncwarp();
+                    if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
+                    if (!more && i < kUnitSlots) {
+                        vl_ends(p, pl, cta, &misc->ends);
+                        asm volatile("bar.arrive 14, 288;" ::: "memory");
+                    }
+                }
             }
         } else {
             // -------------------------------------------------------------- softmax
@@ -539,23 +575,14 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             const int quarter = warp & 3;
             const int ur = kQuad ? lane : r;           // row of the unit's tile
             const int tr = ur / G;                     // and its token
-            // The walk and its unit lie in shared memory, a copy for each warp that its first lane moves on:
-            // registers they would hold are spilled within the tiles' loop, to L2 (shared memory leaves L1
-            // little).
-            Walk8 &wk = reinterpret_cast<Walk8 *>(sbase + L::kOffWalk)[warp - 4];
-            if (lane == 0) wk.walk = VlWalk(pl);
-            const VlUnit &u = wk.u;
             uint32_t sphase = 0, ophase0 = 0, ophase1 = 0;
             bool have_ends = false;
             unsigned ring = 0;                         // tiles that went through the ring before this unit
             unsigned before = 0;                       // and key tiles
             bool was_pair = false;
             bool ok = true;
-            for (;;) {
-                __syncwarp();
-                if (lane == 0) wk.more = wk.walk.next(p, pl, wk.u);
-                __syncwarp();
-                if (!wk.more) break;
+            while (next_unit()) {
+                const VlUnit &u = units[uslot].u;
                 const int n = u.t1 - u.t0;
                 const bool pair = !kSmall && u.ntok > tpt;
                 const int tl = tr + (pair && w ? tpt : 0);             // token within the unit
@@ -573,7 +600,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     if (row_ok)
                         qk = put_query<D>(static_cast<const __nv_bfloat16 *>(p.q) + (long)(u.row0 + tl) * p.q_tok +
                                               (long)(u.g * G + (ur - tr * G)) * p.q_head,
-                                          sbase + (sQ - base) + (pair && w ? 2 * L::kTile : 0), r, pair ? 0 : w, pair ? 2 : 1) *
+                                          sbase + (sQ - base) + (pair && w ? 2 * L::kTile : 0), r, pair ? 0 : w, pair ? 1 : 2) *
                              (p.scale * kLog2e);
                     qk = qk < 0x1p-126f ? 0x1p-126f : qk;       // (NaN, a row that is not finite, stays)
                     fence_proxy_async_smem();
@@ -1043,6 +1070,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     named_sync(2, 256);                // both warpgroups have read both accumulators
                     if (lane == 0 && (w == 0 ? had0 : had1)) mbar_arrive(ofree_bar(w));
                 }
+                done_unit();
             }
             // the softmax warps (they hold the registers) join the shared units
             if (!have_ends) asm volatile("bar.sync 14, 288;" ::: "memory");
