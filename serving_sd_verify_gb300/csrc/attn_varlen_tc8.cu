@@ -23,8 +23,11 @@
 // Warps as in attn_varlen_tc.cu, except that the softmax warps split and write Q
 // (thread = row, which keeps its power of two) and warp 2 reads the scales ahead and
 // hands them over in a ring of kScaleSlots tiles.
-// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [384,384+D); the
-// terms of W_i overlay columns 0-31 and 32-63 of S_i.
+// Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [384,384+D).  A
+// tile's scores come in two parts of 64 keys, whose weights go over the first 32 of
+// their 64 columns: while a stream's softmax has one part, the tensor pipe adds the
+// other's weights to O and makes the next tile's scores there, so that a warp does not
+// wait for its own products (2,048 over 32,768: of 5,400 clocks a pair of tiles 2,300).
 //
 // Every wait is bounded; one that gives up sets the fault word, and the CTA
 // drains its copies and MMAs before it returns.
@@ -70,8 +73,8 @@ template <int D> struct Lay8 {
     static constexpr int kMaxSlots = kSlots + 2;           // where no unit has a second row tile, its room too
     static constexpr int kOffScale = kOffRing + kSlots * kTile;
     static constexpr int kOffBar = kOffScale + kScaleSlots * (int)sizeof(Scales);
-    // full[max] empty[max] qfull drain sfull[2] pfull[2][2] ofull[2] ofree[2] scfull[] scempty[] ufull[] uempty[]
-    static constexpr int kBars = 2 * kMaxSlots + 2 + 2 + 4 + 2 + 2 + 2 * kScaleSlots + 2 * kUnitSlots;
+    // full[max] empty[max] qfull drain sfull[2][2] pfull[2][2] ofull[2] ofree[2] oadd[2] scfull[] scempty[] ufull[] uempty[]
+    static constexpr int kBars = 2 * kMaxSlots + 2 + 4 + 4 + 2 + 2 + 2 + 2 * kScaleSlots + 2 * kUnitSlots;
     static constexpr int kOffMl = kOffBar + 8 * kBars;     // [2][128] exchange between the streams
     static constexpr int kOffMisc = kOffMl + 2 * 128 * 4;
     static constexpr int kOffUnits = kOffMisc + 512;
@@ -181,6 +184,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                        const VarlenParams p, const int tpt, const int box) {
     using L = Lay8<D>;
     constexpr bool kSmall = kRows != kPairs, kQuad = kRows == kQuad8;
+    constexpr int kSubs = kQuad ? 1 : 2;               // parts of a tile's keys that go around by themselves
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t base = (raw_u32 + 1023u) & ~1023u;
@@ -194,14 +198,15 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     auto empty_bar = [&](int i) { return bar0 + 8u * (L::kMaxSlots + i); };
     const uint32_t bar1 = bar0 + 8u * (2 * L::kMaxSlots);
     const uint32_t qfull_bar = bar1, drain_bar = bar1 + 8u;                  // Q written (8 warps); see the end
-    auto sfull_bar = [&](int i) { return bar1 + 8u * (2 + i); };             // S_i computed
-    auto pfull_bar = [&](int i, int h) { return bar1 + 8u * (4 + 2 * i + h); };   // half h of P_i written (4 warps)
-    auto ofull_bar = [&](int i) { return bar1 + 8u * (8 + i); };             // O_i complete for the unit
-    auto ofree_bar = [&](int i) { return bar1 + 8u * (10 + i); };            // O_i read out (4 warps)
-    auto scfull_bar = [&](int i) { return bar1 + 8u * (12 + i); };           // scales written
-    auto scempty_bar = [&](int i) { return bar1 + 8u * (12 + kScaleSlots + i); };   // and read (8 warps, or 4 twice)
-    auto ufull_bar = [&](int i) { return bar1 + 8u * (12 + 2 * kScaleSlots + i); };
-    auto uempty_bar = [&](int i) { return bar1 + 8u * (12 + 2 * kScaleSlots + kUnitSlots + i); };
+    auto sfull_bar = [&](int i, int h) { return bar1 + 8u * (2 + 2 * i + h); };   // part h of S_i computed
+    auto pfull_bar = [&](int i, int h) { return bar1 + 8u * (6 + 2 * i + h); };   // part h of W_i written (4 warps)
+    auto ofull_bar = [&](int i) { return bar1 + 8u * (10 + i); };            // O_i complete for the unit
+    auto ofree_bar = [&](int i) { return bar1 + 8u * (12 + i); };            // O_i read out (4 warps)
+    auto oadd_bar = [&](int i) { return bar1 + 8u * (14 + i); };             // one more part added to O_i
+    auto scfull_bar = [&](int i) { return bar1 + 8u * (16 + i); };           // scales written
+    auto scempty_bar = [&](int i) { return bar1 + 8u * (16 + kScaleSlots + i); };   // and read (8 warps, or 4 twice)
+    auto ufull_bar = [&](int i) { return bar1 + 8u * (16 + 2 * kScaleSlots + i); };
+    auto uempty_bar = [&](int i) { return bar1 + 8u * (16 + 2 * kScaleSlots + kUnitSlots + i); };
     Unit8 *units = reinterpret_cast<Unit8 *>(sbase + L::kOffUnits);
     // The next unit, false behind the last.  Every warp goes through all of them, whatever it gave up:
     // these waits end because the others' do.
@@ -224,9 +229,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
         for (int i = 0; i < kUnitSlots; ++i) { mbar_init(ufull_bar(i), 1); mbar_init(uempty_bar(i), kUnitReaders); }
         for (int i = 0; i < kScaleSlots; ++i) { mbar_init(scfull_bar(i), 1); mbar_init(scempty_bar(i), 8); }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(sfull_bar(i), 1);
-            mbar_init(pfull_bar(i, 0), 4);
-            mbar_init(pfull_bar(i, 1), 4);
+            for (int h = 0; h < 2; ++h) { mbar_init(sfull_bar(i, h), 1); mbar_init(pfull_bar(i, h), 4); }
+            mbar_init(oadd_bar(i), 1);
             mbar_init(ofull_bar(i), 1);
             mbar_init(ofree_bar(i), 4);
         }
@@ -350,47 +354,51 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     uint32_t qphase = 0, pphase[2] = {0, 0}, fphase[2] = {0, 0};
                     bool used[2] = {false, false};
                     bool ok = true;
-                    const uint32_t idS = idesc_e4m3(128, 128, false), idO = idesc_e4m3(128, D, true);
-                    auto wait_tile = [&]() {
+                    const uint32_t idS = idesc_e4m3(128, 128 / kSubs, false), idO = idesc_e4m3(128, D, true);
+                    // the next tile of the ring: its slot
+                    auto take = [&]() {
                         ok = ok && wait_bar(full_bar(rp.slot), rp.phase, abort_flag, p.fault);
                         tc_fence_after();
+                        const int slot = rp.slot;
+                        rp.step(slots);
+                        return slot;
                     };
                     // descriptors by their first tile's, moved on by whole 16-byte units: rows of D bytes, 8-row
                     // groups 8 D bytes apart whatever the copies' size; the products take 32 of their columns
                     // (Q, K) or 32 of their rows (V) at a time
                     const uint64_t qd0 = row_desc<D>(sQ), kd0 = row_desc<D>(sRing);
-                    auto issue_s = [&](int i, int qt, int slot) {
+                    // part h of S_i from row tile qt and the K tile in `slot`
+                    auto issue_s = [&](int i, int qt, int slot, int h) {
                         const uint64_t qd = qd0 + (uint64_t)(qt * (2 * L::kTile / 16)),
-                                       kd = kd0 + (uint64_t)(slot * (L::kTile / 16));
+                                       kd = kd0 + (uint64_t)(slot * (L::kTile / 16) + h * (64 * D / 16));
                         if (el) {
 #pragma unroll
                             for (int term = 0; term < 2; ++term)
 #pragma unroll
                                 for (int kk = 0; kk < D / 32; ++kk)
-                                    umma8_ss(tmem + 128u * i, qd + term * (L::kTile / 16) + 2 * kk, kd + 2 * kk, idS,
+                                    umma8_ss(tmem + 128u * i + 64u * h, qd + term * (L::kTile / 16) + 2 * kk, kd + 2 * kk, idS,
                                              term + kk > 0 ? 1u : 0u);
-                            umma_commit(sfull_bar(i));
+                            umma_commit(sfull_bar(i, h));
                         }
                     };
-                    auto issue_pv = [&](int i, int slot, bool first, int steps) {
-                        const uint64_t vd = kd0 + (uint64_t)(slot * (L::kTile / 16));
+                    // W_i V for part h of the V tile in `slot`
+                    auto issue_pv = [&](int i, int slot, bool first, int steps, int h) {
+                        const uint64_t vd = kd0 + (uint64_t)(slot * (L::kTile / 16) + h * (64 * D / 16));
+                        ok = ok && wait_bar(pfull_bar(i, h), pphase[i], abort_flag, p.fault);
+                        if (!ok) return;
+                        tc_fence_after();
+                        if (el) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            ok = ok && wait_bar(pfull_bar(i, h), pphase[i], abort_flag, p.fault);
-                            if (!ok) return;
-                            tc_fence_after();
-                            if (el) {
+                            for (int kk = 0; kk < 4 / kSubs; ++kk) {
+                                if (kSmall && kk + 2 * h >= steps) continue;
 #pragma unroll
-                                for (int kk = 2 * h; kk < 2 * h + 2; ++kk) {
-                                    if (kSmall && kk >= steps) continue;
-#pragma unroll
-                                    for (int term = 0; term < 2; ++term)
-                                        umma8_ts(tmem + 256u + 128u * i, tmem + 128u * i + 32u * term + 8u * kk,
-                                                 vd + kk * (32 * D / 16), idO, (!first || kk + term > 0) ? 1u : 0u);
-                                }
+                                for (int term = 0; term < 2; ++term)
+                                    umma8_ts(tmem + 256u + 128u * i, tmem + 128u * i + 64u * h + 32u / kSubs * term + 8u * kk,
+                                             vd + kk * (32 * D / 16), idO, (!first || kk + term > 0) ? 1u : 0u);
                             }
+                            if (kSubs > 1) umma_commit(oadd_bar(i));
                         }
-                        pphase[i] ^= 1u;
+                        if (h == kSubs - 1) pphase[i] ^= 1u;
                     };
                     // O_i free for a new unit
                     auto claim = [&](int i) {
@@ -411,67 +419,46 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         auto steps = [&](int j) { return kSmall ? (u.kv - (u.t0 + j) * 128 + 31) >> 5 : 4; };
                         ok = wait_bar(qfull_bar, qphase, abort_flag, p.fault);
                         qphase ^= 1u;
-                        wait_tile();
+                        // Both parts of the first tiles' scores; then, as each part's weights come, their product and
+                        // the same part of the stream's next tile: a stream's other part is with its softmax meanwhile.
+                        int kt[2], vt[2] = {0, 0};
+                        kt[0] = kt[1] = take();
+                        if (!pair && n > 1) kt[1] = take();
                         if (!ok) continue;
-                        issue_s(0, 0, rp.slot);
-                        if (pair) issue_s(1, 1, rp.slot);
-                        if (el) umma_commit(empty_bar(rp.slot));
-                        rp.step(slots);
-                        if (pair) {
-                            for (int j = 0; ok && j < n; ++j) {
-                                wait_tile();
-                                if (!ok) break;
-                                const RingPos vp = rp;
-                                rp.step(slots);
-                                if (j == 0) claim(0);
-                                issue_pv(0, vp.slot, j == 0, 4);
-                                if (!ok) break;
-                                if (j + 1 < n) {
-                                    wait_tile();
-                                    if (!ok) break;
-                                    issue_s(0, 0, rp.slot);
-                                } else {
-                                    if (el) umma_commit(ofull_bar(0));
+#pragma unroll
+                        for (int h = 0; h < kSubs; ++h) {
+                            issue_s(0, 0, kt[0], h);
+                            if (pair || n > 1) issue_s(1, pair ? 1 : 0, kt[1], h);
+                        }
+                        if (el) {
+                            umma_commit(empty_bar(kt[0]));
+                            if (!pair && n > 1) umma_commit(empty_bar(kt[1]));
+                        }
+                        const int step = pair ? 1 : 2;
+                        for (int jj = 0; ok && jj < n; jj += step) {
+#pragma unroll
+                            for (int h = 0; h < kSubs; ++h)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const int j = pair ? jj : jj + i;
+                                    if (!ok || j >= n) continue;
+                                    const bool fetch = h == 0 && (!pair || i == 0), last = h == kSubs - 1 && (!pair || i == 1);
+                                    if (fetch) vt[i] = take();
+                                    const int v = vt[pair ? 0 : i];
+                                    if (jj == 0 && h == 0) claim(i);
+                                    issue_pv(i, v, jj == 0 && h == 0, steps(j), h);
+                                    if (!ok) continue;
+                                    if (last && el) umma_commit(empty_bar(v));
+                                    if (j + step < n) {
+                                        if (fetch) kt[i] = take();
+                                        if (!ok) continue;
+                                        const int k = kt[pair ? 0 : i];
+                                        issue_s(i, pair ? i : 0, k, h);
+                                        if (last && el) umma_commit(empty_bar(k));
+                                    } else if (h == kSubs - 1) {
+                                        if (el) umma_commit(ofull_bar(i));
+                                    }
                                 }
-                                if (j == 0) claim(1);
-                                issue_pv(1, vp.slot, j == 0, 4);
-                                if (!ok) break;
-                                if (el) umma_commit(empty_bar(vp.slot));
-                                if (j + 1 < n) {
-                                    issue_s(1, 1, rp.slot);
-                                    if (el) umma_commit(empty_bar(rp.slot));
-                                    rp.step(slots);
-                                } else {
-                                    if (el) umma_commit(ofull_bar(1));
-                                }
-                            }
-                        } else {
-                            if (n > 1) {
-                                wait_tile();
-                                if (!ok) continue;
-                                issue_s(1, 0, rp.slot);
-                                if (el) umma_commit(empty_bar(rp.slot));
-                                rp.step(slots);
-                            }
-                            for (int j = 0; ok && j < n; ++j) {
-                                const int i = j & 1;
-                                wait_tile();
-                                if (!ok) break;
-                                if (j < 2) claim(i);
-                                issue_pv(i, rp.slot, j < 2, steps(j));
-                                if (!ok) break;
-                                if (el) umma_commit(empty_bar(rp.slot));
-                                rp.step(slots);
-                                if (j + 2 < n) {
-                                    wait_tile();
-                                    if (!ok) break;
-                                    issue_s(i, 0, rp.slot);
-                                    if (el) umma_commit(empty_bar(rp.slot));
-                                    rp.step(slots);
-                                } else {
-                                    if (el) umma_commit(ofull_bar(i));
-                                }
-                            }
                         }
                     }
                 }
@@ -579,6 +566,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             bool have_ends = false;
             unsigned ring = 0;                         // tiles that went through the ring before this unit
             unsigned before = 0;                       // and key tiles
+            uint32_t added = 0;                        // parts added to this stream's accumulator, announced by oadd
             bool was_pair = false;
             bool ok = true;
             while (next_unit()) {
@@ -611,8 +599,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 const int j0 = pair ? 0 : w;
                 for (int j = j0; j < n; j += step) {
                     const int key0 = (u.t0 + j) * 128;
-                    ok = __all_sync(0xffffffffu, wait_bar(sfull_bar(w), sphase, abort_flag, p.fault)) && ok;
-                    sphase ^= 1u;
+                    ok = __all_sync(0xffffffffu, wait_bar(sfull_bar(w, 0), sphase, abort_flag, p.fault)) && ok;
                     tc_fence_after();
                     if (key0 + 128 > u.kv && (!pair || w == 0)) {
                         // slots past the sequence may hold anything, and 0 times that is not 0:
@@ -720,140 +707,123 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(pfull_bar(w, 0));
-                            mbar_arrive(pfull_bar(w, 1));
                             mbar_arrive_n(scempty_bar(sc), 2);
                         }
-                    } else if (warp_live) {
-                        uint32_t s[4][32];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32_async(s_col + 32u * c, s[c]);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld_bind(s[c]);
-                        // the keys' scales
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 f = reinterpret_cast<const float4 *>(ts.k)[8 * c + e / 4];
-                                const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
-                                                            make_float2(f.x, f.y));
-                                const float2 y = __fmul2_rn(make_float2(__uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3])),
-                                                            make_float2(f.z, f.w));
-                                s[c][e] = __float_as_uint(x.x); s[c][e + 1] = __float_as_uint(x.y);
-                                s[c][e + 2] = __float_as_uint(y.x); s[c][e + 3] = __float_as_uint(y.y);
-                            }
-                        const int vis = lim - key0;                     // this row sees keys [0, vis) of the tile
-                        if constexpr (kTree) {
-                            if (key0 + 128 > u.off) {                   // the tile holds nodes, or ends behind them
-                                const uint64_t seen[2] = {tree_seen(word, key0 - u.off), tree_seen(word, key0 + 64 - u.off)};
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                                    for (int e = 0; e < 32; ++e)
-                                        if (!(seen[c >> 1] >> (32 * (c & 1) + e) & 1)) s[c][e] = 0xff800000u;
-                            }
-                        } else if (!__all_sync(0xffffffffu, vis >= 128 || !row_ok)) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (32 * c + e >= vis) s[c][e] = 0xff800000u;
-                        }
-                        const float2 qk2 = make_float2(qk, qk);
-                        float2 ls[2], nm2;
-                        uint32_t hi[16], lo[16];
-                        // weights of 32 keys, the scores' c-th 32 columns: 8 words of each term; step by step over
-                        // all of them, so that each step's latency is covered by the others' work
-                        auto weights = [&](int c, int to) {
-                            float2 x[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                x[e] = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), qk2, nm2);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) x[e] = make_float2(ex2(x[e].x), ex2(x[e].y));
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) ls[e & 1] = __fadd2_rn(ls[e & 1], x[e]);
-                            __half2 v[16];
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                const float4 f = reinterpret_cast<const float4 *>(ts.v)[8 * c + e / 2];
-                                const float2 w0 = __fmul2_rn(x[e], make_float2(f.x, f.y)), w1 = __fmul2_rn(x[e + 1], make_float2(f.z, f.w));
-                                // (in f16, 2^-12 off; the first term's rest is exact there)
-                                v[e] = __floats2half2_rn(w0.x, w0.y);
-                                v[e + 1] = __floats2half2_rn(w1.x, w1.y);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) hi[to + e] = e4m3x4(v[2 * e], v[2 * e + 1]);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                __half2 h0, h1;
-                                halves_of_e4m3x4(hi[to + e], h0, h1);
-                                v[2 * e] = __hsub2(v[2 * e], h0);
-                                v[2 * e + 1] = __hsub2(v[2 * e + 1], h1);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) lo[to + e] = e4m3x4(v[2 * e], v[2 * e + 1]);
-                        };
-                        float m4[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float m = max3(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]), __uint_as_float(s[i][2]));
-#pragma unroll
-                            for (int e = 3; e < 31; e += 2)
-                                m = max3(m, __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
-                            m4[i] = fmaxf(m, __uint_as_float(s[i][31]));
-                        }
-                        const float tmax = qk * fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-                        const bool need = tmax > m_used + kRescale8;    // true at first while m_used = -inf
-                        float alpha = 1.f;
-                        if (need) {
-                            alpha = ex2(m_used - tmax);                 // 0 while nothing is held
-                            m_used = tmax;
-                        }
-                        if (j > j0 && __any_sync(0xffffffffu, need || ratio != 1.f)) {
-                            // S_j is complete, hence every earlier product of this stream too
-                            // (they were issued before it and complete in order)
-                            const float f = alpha * ratio;
+                    } else {
+                        // 64 keys at a time
 #pragma unroll 1
-                            for (int c = 0; c < D / 16; ++c) {
-                                uint32_t o[16];
-                                tmem_ld16_async(o_col + 16u * c, o);
-                                tmem_ld_wait();
-                                tmem_ld_bind16(o);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st16(o_col + 16u * c, o);
+                        for (int h = 0; h < 2; ++h, ++added) {
+                            if (h) {
+                                ok = __all_sync(0xffffffffu, wait_bar(sfull_bar(w, 1), sphase, abort_flag, p.fault)) && ok;
+                                tc_fence_after();
                             }
-                        }
-                        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-                        nm2 = make_float2(neg_m, neg_m);
-                        ls[0] = ls[1] = make_float2(0.f, 0.f);
-                        l *= alpha;
-                        // 64 keys' weights at a time, over the scores' first 64 columns: the first terms in
-                        // columns 0-31, the second in 32-63
+                            if (warp_live) {
+                                const uint32_t at = s_col + 64u * h;
+                                uint32_t s[2][32];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            weights(2 * h, 0);
-                            weights(2 * h + 1, 8);
-                            tmem_st16(s_col + 16u * h, hi);
-                            tmem_st16(s_col + 32u + 16u * h, lo);
-                            tmem_st_wait();
+                                for (int c = 0; c < 2; ++c) tmem_ld32_async(at + 32u * c, s[c]);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) tmem_ld_bind(s[c]);
+                                // the keys' scales
+                                const float4 *ks = reinterpret_cast<const float4 *>(ts.k) + 16 * h, *vs = reinterpret_cast<const float4 *>(ts.v) + 16 * h;
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 4) {
+                                        const float4 f = ks[8 * c + e / 4];
+                                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                                                    make_float2(f.x, f.y));
+                                        const float2 y = __fmul2_rn(make_float2(__uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3])),
+                                                                    make_float2(f.z, f.w));
+                                        s[c][e] = __float_as_uint(x.x); s[c][e + 1] = __float_as_uint(x.y);
+                                        s[c][e + 2] = __float_as_uint(y.x); s[c][e + 3] = __float_as_uint(y.y);
+                                    }
+                                const int from = key0 + 64 * h;
+                                uint64_t seen = ~0ull;
+                                if constexpr (kTree) {                  // nodes among the keys, or what lies behind them
+                                    seen = tree_seen(word, from - u.off);
+                                } else {
+                                    const int vis = lim - from;         // this row sees the first `vis` of the keys
+                                    if (vis < 64) seen = vis <= 0 ? 0ull : (1ull << vis) - 1;
+                                }
+                                if (!__all_sync(0xffffffffu, seen == ~0ull || !row_ok)) {
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e)
+                                            if (!(seen >> (32 * c + e) & 1)) s[c][e] = 0xff800000u;
+                                }
+                                float m4[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t *x = s[i >> 1] + 16 * (i & 1);
+                                    float m = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+#pragma unroll
+                                    for (int e = 3; e < 15; e += 2) m = max3(m, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                                    m4[i] = fmaxf(m, __uint_as_float(x[15]));
+                                }
+                                const float tmax = qk * fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+                                const bool need = row_ok && tmax > m_used + kRescale8;    // true at first while m_used = -inf
+                                float alpha = 1.f;
+                                if (need) {
+                                    alpha = ex2(m_used - tmax);         // 0 while nothing is held
+                                    m_used = tmax;
+                                }
+                                const float f = h ? alpha : alpha * ratio;
+                                if ((j > j0 || h) && __any_sync(0xffffffffu, f != 1.f)) {
+                                    // the part before this one has to be in O: the others are, their products went
+                                    // out before this part's scores and complete in order
+                                    ok = __all_sync(0xffffffffu, wait_bar(oadd_bar(w), (added - 1) & 1u, abort_flag, p.fault)) && ok;
+                                    tc_fence_after();
+#pragma unroll 1
+                                    for (int c = 0; c < D / 32; ++c) {
+                                        uint32_t o[32];
+                                        tmem_ld32_async(o_col + 32u * c, o);
+                                        tmem_ld_wait();
+                                        tmem_ld_bind(o);
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                        tmem_st32(o_col + 32u * c, o);
+                                    }
+                                }
+                                const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                                const float2 qk2 = make_float2(qk, qk), nm2 = make_float2(neg_m, neg_m);
+                                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                                // the weights go over scores that have been read: the first terms in the part's
+                                // columns 0-15, the second in 16-31
+                                uint32_t hi[16], lo[16];
+#pragma unroll
+                                for (int g = 0; g < 16; ++g) {
+                                    const uint32_t *x = s[g >> 3] + 4 * (g & 7);
+                                    const float4 y = vs[g];
+                                    const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), qk2, nm2);
+                                    const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), qk2, nm2);
+                                    const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y)), p1 = make_float2(ex2(x1.x), ex2(x1.y));
+                                    ls[0] = __fadd2_rn(ls[0], p0);
+                                    ls[1] = __fadd2_rn(ls[1], p1);
+                                    const float2 w0 = __fmul2_rn(p0, make_float2(y.x, y.y)), w1 = __fmul2_rn(p1, make_float2(y.z, y.w));
+                                    // (in f16, 2^-12 off; the first term's rest is exact there)
+                                    const __half2 v0 = __floats2half2_rn(w0.x, w0.y), v1 = __floats2half2_rn(w1.x, w1.y);
+                                    __half2 h0, h1;
+                                    hi[g] = e4m3x4(v0, v1);
+                                    halves_of_e4m3x4(hi[g], h0, h1);
+                                    lo[g] = e4m3x4(__hsub2(v0, h0), __hsub2(v1, h1));
+                                }
+                                tmem_st16(at, hi);
+                                tmem_st16(at + 16u, lo);
+                                l = l * alpha + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
+                                tmem_st_wait();
+                            }
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(pfull_bar(w, h));
-                        }
-                        if (lane == 0) mbar_arrive_n(scempty_bar(sc), pair ? 1 : 2);
-                        l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(pfull_bar(w, 0));
-                            mbar_arrive(pfull_bar(w, 1));
-                            mbar_arrive_n(scempty_bar(sc), pair ? 1 : 2);
+                            if (lane == 0) {
+                                mbar_arrive(pfull_bar(w, h));
+                                if (h) mbar_arrive_n(scempty_bar(sc), pair ? 1 : 2);
+                            }
                         }
                     }
+                    sphase ^= 1u;
                 }
                 // ---- end of the unit: this CTA's rows, normalised, or its part of them
                 const bool whole = u.t0 == 0 && u.t1 == u.tiles;
