@@ -419,20 +419,52 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         auto steps = [&](int j) { return kSmall ? (u.kv - (u.t0 + j) * 128 + 31) >> 5 : 4; };
                         ok = wait_bar(qfull_bar, qphase, abort_flag, p.fault);
                         qphase ^= 1u;
+                        if constexpr (kQuad) {         // (88 us for 64 sequences of one token; the loops below with one part 95)
+                            int k = take();
+                            if (!ok) continue;
+                            issue_s(0, 0, k, 0);
+                            if (el) umma_commit(empty_bar(k));
+                            if (n > 1) {
+                                k = take();
+                                if (!ok) continue;
+                                issue_s(1, 0, k, 0);
+                                if (el) umma_commit(empty_bar(k));
+                            }
+                            for (int j = 0; ok && j < n; ++j) {
+                                const int i = j & 1, v = take();
+                                if (!ok) break;
+                                if (j < 2) claim(i);
+                                issue_pv(i, v, j < 2, steps(j), 0);
+                                if (!ok) break;
+                                if (el) umma_commit(empty_bar(v));
+                                if (j + 2 < n) {
+                                    k = take();
+                                    if (!ok) break;
+                                    issue_s(i, 0, k, 0);
+                                    if (el) umma_commit(empty_bar(k));
+                                } else {
+                                    if (el) umma_commit(ofull_bar(i));
+                                }
+                            }
+                            continue;
+                        }
                         // Both parts of the first tiles' scores; then, as each part's weights come, their product and
                         // the same part of the stream's next tile: a stream's other part is with its softmax meanwhile.
                         int kt[2], vt[2] = {0, 0};
                         kt[0] = kt[1] = take();
-                        if (!pair && n > 1) kt[1] = take();
                         if (!ok) continue;
 #pragma unroll
                         for (int h = 0; h < kSubs; ++h) {
                             issue_s(0, 0, kt[0], h);
-                            if (pair || n > 1) issue_s(1, pair ? 1 : 0, kt[1], h);
+                            if (pair) issue_s(1, 1, kt[0], h);
                         }
-                        if (el) {
-                            umma_commit(empty_bar(kt[0]));
-                            if (!pair && n > 1) umma_commit(empty_bar(kt[1]));
+                        if (el) umma_commit(empty_bar(kt[0]));
+                        if (!pair && n > 1) {
+                            kt[1] = take();
+                            if (!ok) continue;
+#pragma unroll
+                            for (int h = 0; h < kSubs; ++h) issue_s(1, 0, kt[1], h);
+                            if (el) umma_commit(empty_bar(kt[1]));
                         }
                         const int step = pair ? 1 : 2;
                         for (int jj = 0; ok && jj < n; jj += step) {
