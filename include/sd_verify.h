@@ -613,8 +613,9 @@ sd_status sd_prompt_attention(const void *q, int64_t q_tok, int64_t q_head, cons
  *   q_weight, k_weight  device [D] of the inputs' type, aligned to it, or NULL
  *   eps        >= 0, finite
  *   the rest as for sd_rotary
- * Rows of non-finite values, and with eps = 0 rows of zeros, give NaN as the
- * formula does; no other row is touched by them.
+ * The squares are summed in fp32 (elements up to about 1e18).  Rows of non-finite
+ * values, and with eps = 0 rows of zeros, give NaN as the formula does; no other
+ * row is touched by them.
  * ------------------------------------------------------------------------ */
 typedef enum { SD_AXES_BLOCKS = 0, SD_AXES_STRIPES = 1 } sd_axes_order;
 
@@ -667,8 +668,9 @@ sd_status sd_norm_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_he
  * sd_paged_attention's.
  * bf16 over pages of a multiple of 8 slots runs on the tensor cores, in e4m3: q as
  * the sum of two e4m3 terms (exact for elements above 2^-9 of their row's
- * largest, off by 2^-18 of that largest below), the weights as two terms (2^-8 of
- * each, or 2^-16 of the row's largest), fp32 sums.
+ * largest, off by 2^-18 of that largest below), a weight times its value's scale as
+ * two terms (off by 2^-9 of itself, or by 2^-16 of the row's largest weight times
+ * the largest scale so far where that is more), fp32 sums.
  * Scales of slots at and past kv_len[b] may hold anything; those inside a sequence
  * are finite and not negative. */
 sd_status sd_paged_attention_e4m3(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,

@@ -197,6 +197,22 @@ def test_append(S, dtype, layout, quantised, Hq, Hkv, D, R, page, axes, order):
     assert S.sd_fault_word() == 0
 
 
+def test_values_are_copied_bit_for_bit(S):
+    """Into a cache of their own type every bit pattern goes as it is, NaNs and their payloads among them."""
+    for dtype, it, D in ((torch.bfloat16, torch.int16, 128), (torch.bfloat16, torch.int16, 30), (torch.float32, torch.int32, 64)):
+        g = torch.Generator().manual_seed(D)
+        info = torch.iinfo(it)
+        bits = torch.randint(info.min, info.max, (64, 2, D), generator=g, dtype=it)
+        v = bits.view(dtype).cuda()
+        k = torch.zeros_like(v)
+        kp, vp = (torch.zeros(5, 16, 2, D, dtype=dtype, device="cuda") for _ in range(2))
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+        S.sd_norm_rotary_append_paged(None, k, v, None, None, S.sd_rotary_table(2, 1e4)[0].cuda(), i32([0, 64]), i32([64]),
+                                      i32([[3, 1, 0, 4]]), kp, vp)
+        assert torch.equal(vp[[3, 1, 0, 4]].view(it).view(64, 2, D).cpu(), bits)
+    assert S.sd_fault_word() == 0
+
+
 def test_append_of_rows_of_zeros_and_tiny_ones(S):
     """A row of zeros gets codes of zero and the smallest scale; one of 2^-90 keeps its relative precision."""
     D = 64

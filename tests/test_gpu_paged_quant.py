@@ -476,3 +476,39 @@ def test_a_tree_is_drafted_verified_and_committed(S, quantised):
     top = float(rows[:, Hq + Hkv:].abs().max())
     assert float((got - ref).abs().max()) <= 4 * 2.0 ** -8 * top
     assert S.sd_fault_word() == 0
+
+
+@pytest.mark.parametrize("quantised", [True, False])
+def test_pools_past_32_bit_offsets(S, quantised):
+    """Pages whose offsets, in elements and in scales' bytes, pass 2^32: the same bits as in a pool of three."""
+    g = torch.Generator().manual_seed(30)
+    Hq, Hkv, D, page, n = 32, 8, 128, 128, 300
+    far = 36000 if quantised else 33100
+    dt = torch.uint8 if quantised else torch.bfloat16
+    x = torch.randn(n, Hq + 2 * Hkv, D, generator=g).bfloat16().cuda()
+    turns = S.sd_rotary_table(D, 1e6)[0].cuda()
+    path = torch.full((1, 40), -1, dtype=torch.int32)
+    path[0, :3] = i32([4, 9, 30])
+    results = []
+    for pages, ids in ((3, [2, 0, 1]), (far, [far - 1, 1, far - 2])):
+        kp, vp = (torch.empty(pages, page, Hkv, D, dtype=dt, device="cuda") for _ in range(2))
+        sc = [torch.empty(pages, Hkv, page, device="cuda") for _ in range(2)] if quantised else [None, None]
+        if quantised:
+            kp, vp = kp.view(torch.float8_e4m3fn), vp.view(torch.float8_e4m3fn)
+        table = i32([ids]).cuda()
+        q = torch.empty(n, Hq, D, dtype=torch.bfloat16, device="cuda")
+        S.sd_norm_rotary_append_paged(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], q, None, turns, i32([0, n]).cuda(), i32([n]).cuda(),
+                                      table, kp, vp, *sc)
+        S.sd_compact_tree_paged(kp, vp, table, i32([n - 39]).cuda(), path.cuda(), i32([3]).cuda(), *sc)
+        outs = []
+        for forced in (0, 1):
+            S.sd_set_attention_path(forced)
+            out = torch.empty(40, Hq, D, dtype=torch.bfloat16, device="cuda")
+            ws = S.workspace(S.sd_paged_attention_workspace_size(40, 1, 40, Hq, Hkv, D, n))
+            words = signed([(1 << 40) - 1] * 40).cuda()
+            S.sd_paged_tree_attention(q[-40:], kp, vp, table, words, i32([0, 40]).cuda(), i32([n]).cuda(), 40, n, out, D ** -0.5, ws, *sc)
+            outs.append(out)
+        rows = [(t.view(torch.uint8) if quantised else t)[ids] for t in (kp, vp)]
+        results.append(outs + [r.flatten(0, 1)[:n] for r in rows] + ([s[ids].transpose(1, 2).flatten(0, 1)[:n] for s in sc] if quantised else []))
+        del kp, vp, sc
+    assert all(torch.equal(a, b) for a, b in zip(*results)) and S.sd_fault_word() == 0
