@@ -2,6 +2,8 @@
 
 Each .cu under csrc/ is compiled in parallel to an object in _build/, then
 linked with the static CUDA runtime into serving_sd_verify_gb300/libsdverify.so.
+Beside them g++ compiles csrc/fast_calls.cpp, the Python binding's short way
+into the library, against the installed torch to _fast_calls.so.
 The library links no libcuda: the one driver entry point it needs (tensor-map
 encoding) is fetched at run time through the runtime's driver-entry-point
 query, so the .so also loads on machines without a GPU driver.
@@ -12,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsdverify.so")
+FAST = os.path.join(PKG, "_fast_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-I", os.path.join(ROOT, "include")]
@@ -36,15 +40,32 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return sources() + [os.path.join(CSRC, "fast_calls.cpp")] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         [os.path.join(ROOT, "include", "sd_verify.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(FAST)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(FAST))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _build_fast() -> None:
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(root, "lib")
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(a for d in inc for a in ("-isystem", d)), os.path.join(CSRC, "fast_calls.cpp"), "-o", tmp, "-L" + lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib, "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for fast_calls.cpp:\n{r.stderr}")
+    os.replace(tmp, FAST)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
@@ -66,7 +87,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        fast = ex.submit(_build_fast)
         objs = list(ex.map(compile_one, sources()))
+        fast.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

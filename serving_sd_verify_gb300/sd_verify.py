@@ -10,12 +10,15 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsdverify.so")
+FAST_PATH = os.path.join(_HERE, "_fast_calls.so")
 
 SD_OK, SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED, SD_ERR_WORKSPACE, SD_ERR_CUDA = range(5)
 SD_BF16, SD_FP32 = 0, 1
@@ -70,6 +73,7 @@ class RopeAxes(ctypes.Structure):
 
 
 _lib = None
+_fast = None        # fast_calls.cpp: the short way of the calls that use it
 _vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 
 
@@ -78,8 +82,8 @@ def load():
     global _lib
     if _lib is not None:
         return _lib
-    if not os.path.exists(LIB_PATH):
-        raise RuntimeError(f"{LIB_PATH} is missing: run serving_sd_verify_gb300.build.build() "
+    if not (os.path.exists(LIB_PATH) and os.path.exists(FAST_PATH)):
+        raise RuntimeError(f"{LIB_PATH} or {FAST_PATH} is missing: run serving_sd_verify_gb300.build.build() "
                            "(nvcc, sm_103a) first; there is no CPU fallback")
     lib = ctypes.CDLL(LIB_PATH)
     lib.sd_verify_attention.argtypes = [_vp, _vp, _vp, Strides, _vp, _i, _vp, _i, _i, _i, _i, _i, _i,
@@ -187,6 +191,12 @@ def load():
     lib.sd_last_projector_path.argtypes = []
     lib.sd_last_projector_path.restype = _i
     _lib = lib
+    global _fast
+    loader = importlib.machinery.ExtensionFileLoader("_fast_calls", FAST_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fast_calls", loader))
+    loader.exec_module(module)
+    module.bind(LIB_PATH)
+    _fast = module
     return lib
 
 
@@ -714,6 +724,10 @@ def sd_norm_rotary(q, q_out, k, k_out, positions, turns, q_weight=None, k_weight
     """q, q_out [N, Hq, D] and k, k_out [N, Hk, D] (or both None), D contiguous; an
     output may be its input.  positions int32 [axes, N], or [N] for one axis; axes:
     the pairs of each (None: one axis); weights [D] or None (not normed)."""
+    if stream is None and _fast is not None:
+        r = _fast.norm_rotary(q, q_out, k, k_out, positions, turns, q_weight, k_weight, eps, axes, axes_order, layout, magnitude)
+        if r is not None:          # (None: look at the arguments here, and say what is wrong with them)
+            return _check(r)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     if positions is None:
@@ -751,6 +765,11 @@ def sd_norm_rotary_append_paged(q, k, v, q_out, positions, turns, cu_q, kv_len, 
     """As sd_rotary_append_paged with norms and axes (sd_norm_rotary); positions None:
     every axis takes the cache position.  With k_scale and v_scale (fp32 [pages, Hkv,
     page_size]) the pages are float8_e4m3fn."""
+    if stream is None and _fast is not None:
+        r = _fast.append(q, k, v, q_out, positions, turns, cu_q, kv_len, page_table, k_pages, v_pages, k_scale, v_scale, q_weight,
+                         k_weight, eps, axes, axes_order, layout, magnitude)
+        if r is not None:          # (None: look at the arguments here, and say what is wrong with them)
+            return _check(r)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     dev = _one_device((k, v, turns, cu_q, kv_len, page_table, k_pages, v_pages) +
@@ -796,6 +815,10 @@ def sd_paged_attention_e4m3(q, k_pages, v_pages, k_scale, v_scale, page_table, c
                             ws, causal=True, stream=None):
     """As sd_paged_attention over float8_e4m3fn pages with k_scale and v_scale, fp32
     [pages, Hkv, page_size]; ws of sd_paged_attention_workspace_size."""
+    if stream is None and _fast is not None:
+        r = _fast.attend(q, k_pages, v_pages, k_scale, v_scale, page_table, None, cu_q, kv_len, max_q, max_kv, out, scale, ws, causal)
+        if r is not None:          # (None: look at the arguments here, and say what is wrong with them)
+            return _check(r)
     if k_scale is None or v_scale is None:
         raise ValueError("k_scale and v_scale are contiguous fp32 [pages, Hkv, page_size]")
     dev = _one_device((q, k_pages, v_pages, k_scale, v_scale, page_table, cu_q, kv_len, out, ws))
@@ -812,6 +835,11 @@ def sd_paged_tree_attention(q, k_pages, v_pages, page_table, tree_mask, cu_q, kv
     """Attention of drafted trees over a paged cache of q's dtype, or float8_e4m3fn with
     scales: tree_mask int64 [N], bit k of a node's word: it sees its tree's node k;
     max_q <= 64; the rest as sd_paged_attention."""
+    if stream is None and _fast is not None:
+        r = _fast.attend(q, k_pages, v_pages, k_scale, v_scale, page_table, tree_mask, cu_q, kv_len, max_q, max_kv, out, scale, ws,
+                         False)
+        if r is not None:          # (None: look at the arguments here, and say what is wrong with them)
+            return _check(r)
     dev = _one_device((q, k_pages, v_pages, page_table, tree_mask, cu_q, kv_len, out, ws) + _present(k_scale, v_scale))
     cache, B, Hkv, dim = _paged_cache(k_pages, v_pages, page_table, cu_q, kv_len)
     N, Hq, D, qt, qh = _query_rows(q, out, dim)
@@ -827,6 +855,10 @@ def sd_compact_tree_paged(k_pages, v_pages, page_table, ctx_len, path, n_accepte
                           stream=None):
     """As sd_compact_tree_kv in a paged cache (float8_e4m3fn pages with their scales, or
     bf16 / fp32): page_table int32 [B, columns], ctx_len and n_accepted int32 [B], path int32 [B, T]."""
+    if stream is None and _fast is not None:
+        r = _fast.compact(k_pages, v_pages, page_table, ctx_len, path, n_accepted, k_scale, v_scale)
+        if r is not None:          # (None: look at the arguments here, and say what is wrong with them)
+            return _check(r)
     dev = _one_device((k_pages, v_pages, page_table, ctx_len, path, n_accepted) + _present(k_scale, v_scale))
     cache, B, Hkv, D = _paged_cache(k_pages, v_pages, page_table, None, ctx_len)
     _i32_cuda(path, n_accepted)
