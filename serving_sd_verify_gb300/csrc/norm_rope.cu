@@ -102,9 +102,15 @@ norm_rope_row_kernel(const __grid_constant__ NormRopeParams p, const long rows, 
 // past the turned ones.  The next rows' loads are in flight while a row's sums meet by
 // shuffles among its lanes.  Arithmetic comes two elements an instruction: what bounds
 // the kernel besides memory is the instructions it issues.
+// Measured (bf16, three axes): 25,119 tokens of 32 heads of 128 69.5 us (5.9 TB/s of 6.8),
+// of 28 with 8 written as e4m3 81.4 us (5.4 TB/s), 2,048 tokens of 80 into a bf16 cache
+// 17.4 us (4.8 TB/s).  A lane group with angles of its own for four heads took 97, 171 and
+// 26 us, two rows in flight a lane 99, 126 and 26 (registers for five CTAs an SM only), one
+// warp a token with loads ahead in registers or in a ring of cp.async 76 to 101 and 92;
+// seven CTAs an SM are as many as fit without spills (six: 74.3, 87.4 and 22.6).
 constexpr int kVecThreads = 128;
 constexpr int kRows = 1;             // of a lane in flight
-constexpr int kTokens = 4;           // of a CTA at most
+constexpr int kTokens = 8;           // of a CTA at most
 constexpr int kVecPairs = 256;       // of a row at most: 32 chunks of 8
 
 // the two elements of each 32-bit word of a vector, or its words two and two
@@ -156,9 +162,13 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
             row += step;
             h += step;
             if (h >= heads) {
-                const int q = (int)((unsigned)h / (unsigned)heads);
-                t += q;
-                h -= q * heads;
+                h -= heads;
+                ++t;
+                if (h >= heads) {
+                    const int q = (int)((unsigned)h / (unsigned)heads);
+                    t += q;
+                    h -= q * heads;
+                }
             }
         }
     }
@@ -176,7 +186,7 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
         for (int i = 0; i < kRows; ++i) a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     __device__ __forceinline__ void run(const NormRopeParams &p, const VecShared &sh, int n0, int log_p, int rot_chunks, int c,
-                                        unsigned mine, bool live, bool two, int oa, int ob) {
+                                        bool live, bool two, int oa, int ob) {
         const T *w = static_cast<const T *>(kRole == 0 ? p.wq : kRole == 1 ? p.wk : nullptr);
         float2 ga[H], gb[H];
         if (kRole < 2) {
@@ -187,7 +197,10 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
             unpack2(wb, gb);
         }
         const bool turned = kRole < 2 && c < rot_chunks;
-        while (rt[0] >= 0) {
+        // whole warps go through the loop, rows or not: sums over some of a warp's lanes under a mask of their
+        // own would cost a synchronisation each (25,119 x 32 heads 77.7 us)
+        const int width = 1 << log_p;
+        while (__any_sync(0xffffffffu, rt[0] >= 0)) {
             uint4 ca[kRows], cb[kRows];
             int ct[kRows], ch[kRows];
 #pragma unroll
@@ -195,9 +208,9 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
             load(live, two, oa, ob);
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                if (ct[i] < 0) break;
-                const int *at = sh.place[ct[i]];
-                if (kCache && (kRole ? at[0] < 0 : at[0] == -2)) continue;
+                const int tok = max(ct[i], 0);
+                const int *at = sh.place[tok];
+                const bool write = ct[i] >= 0 && !(kCache && (kRole ? at[0] < 0 : at[0] == -2));
                 float2 fa[H], fb[H];
                 unpack2(ca[i], fa);
                 unpack2(cb[i], fb);
@@ -209,8 +222,9 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
 #pragma unroll
                         for (int e = 0; e < H; ++e) s2 = __ffma2_rn(fb[e], fb[e], s2);
                     float sum = s2.x + s2.y;
-#pragma unroll 1
-                    for (int o = 1; o < 1 << log_p; o <<= 1) sum += __shfl_xor_sync(mine, sum, o);
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1)
+                        if (o < width) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     const float inv = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
                     const float2 i2 = make_float2(inv, inv);
 #pragma unroll
@@ -220,7 +234,7 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
                         for (int e = 0; e < H; ++e) fb[e] = __fmul2_rn(__fmul2_rn(fb[e], i2), gb[e]);
                 }
                 if (turned) {
-                    const float4 *angle = sh.angles[ct[i]] + c;
+                    const float4 *angle = sh.angles[tok] + c;
                     if constexpr (kInter) {            // element pairs (a, b) side by side
 #pragma unroll
                         for (int e = 0; e < H; e += 2) {
@@ -247,8 +261,9 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
                     if (two)
 #pragma unroll
                         for (int e = 0; e < H; ++e) amax = fmaxf(amax, fmaxf(fabsf(fb[e].x), fabsf(fb[e].y)));
-#pragma unroll 1
-                    for (int o = 1; o < 1 << log_p; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(mine, amax, o));
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1)
+                        if (o < width) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                     const float mul = e4m3_inverse(amax);
                     uint8_t *codes = static_cast<uint8_t *>(kRole == 1 ? p.k_pages : p.v_pages) + (long)at[1] * p.pages.b +
                                      (long)at[2] * p.pages.s + (long)ch[i] * p.pages.h;
@@ -260,19 +275,19 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
                         if constexpr (V == 8) *reinterpret_cast<uint2 *>(codes + o) = make_uint2(q[0], q[1]);
                         else *reinterpret_cast<uint32_t *>(codes + o) = q[0];
                     };
-                    if (live) put(oa, fa);
-                    if (two) put(ob, fb);
-                    if (c == 0)
+                    if (live && write) put(oa, fa);
+                    if (two && write) put(ob, fb);
+                    if (c == 0 && write)
                         (kRole == 1 ? p.k_scale : p.v_scale)[((long)at[1] * p.Hk + ch[i]) * p.page_size + at[2]] = e4m3_scale(amax);
                 } else {
-                    const long n = n0 + ct[i];
+                    const long n = n0 + tok;
                     T *y = kRole == 0  ? static_cast<T *>(p.q_out) + n * p.qo_tok + ch[i] * p.qo_head
                            : !kCache ? static_cast<T *>(p.k_out) + n * p.ko_tok + ch[i] * p.ko_head
                                      : static_cast<T *>(kRole == 1 ? p.k_pages : p.v_pages) + (long)at[1] * p.pages.b +
                                            (long)at[2] * p.pages.s + (long)ch[i] * p.pages.h;
                     // (values bit for bit)
-                    if (live) *reinterpret_cast<uint4 *>(y + oa) = kRole == 2 ? ca[i] : pack2(fa);
-                    if (two) *reinterpret_cast<uint4 *>(y + ob) = kRole == 2 ? cb[i] : pack2(fb);
+                    if (live && write) *reinterpret_cast<uint4 *>(y + oa) = kRole == 2 ? ca[i] : pack2(fa);
+                    if (two && write) *reinterpret_cast<uint4 *>(y + ob) = kRole == 2 ? cb[i] : pack2(fb);
                 }
             }
         }
@@ -280,7 +295,7 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
 };
 
 template <typename T, bool kInter, int kCache>       // kCache: 0 no cache, 1 pages of T, 2 of codes
-__global__ void __launch_bounds__(kVecThreads, 8)
+__global__ void __launch_bounds__(kVecThreads, 7)
 norm_rope_vec_kernel(const __grid_constant__ NormRopeParams p, const int log_p, const int rot_chunks, const int chunks,
                      const int tokens, const int checks) {
     constexpr int V = kVec<T>, NP = kInter ? V / 2 : V;
@@ -294,7 +309,6 @@ norm_rope_vec_kernel(const __grid_constant__ NormRopeParams p, const int log_p, 
     }
     const int n0 = ((int)blockIdx.x - checks) * tokens, nt = min(tokens, p.N - n0);
     const int lane = tid & 31, c = lane & ((1 << log_p) - 1);
-    const unsigned mine = (log_p == 5 ? 0xffffffffu : (1u << (1 << log_p)) - 1u) << (lane - c);      // the row's lanes
     const bool turned = c < rot_chunks, live = c < chunks;
     // a chunk's elements: [oa, oa + V) and, of pairs in the half layout, [ob, ob + V)
     const int oa = turned ? c * V : p.rot + (c - rot_chunks) * V;
@@ -324,16 +338,16 @@ norm_rope_vec_kernel(const __grid_constant__ NormRopeParams p, const int log_p, 
         to[2] = cs.y;
     }
     __syncthreads();
-    q.run(p, sh, n0, log_p, rot_chunks, c, mine, live, two, oa, ob);
+    q.run(p, sh, n0, log_p, rot_chunks, c, live, two, oa, ob);
     if (p.Hk) {
         Rows<T, kInter, kCache, 1> k(p, n0, nt, first, step);
         k.load(live, two, oa, ob);
-        k.run(p, sh, n0, log_p, rot_chunks, c, mine, live, two, oa, ob);
+        k.run(p, sh, n0, log_p, rot_chunks, c, live, two, oa, ob);
     }
     if (kCache) {
         Rows<T, kInter, kCache, 2> v(p, n0, nt, first, step);
         v.load(live, two, oa, ob);
-        v.run(p, sh, n0, log_p, rot_chunks, c, mine, live, two, oa, ob);
+        v.run(p, sh, n0, log_p, rot_chunks, c, live, two, oa, ob);
     }
 }
 
@@ -361,7 +375,7 @@ cudaError_t launch_vec(NormRopeParams p, int chunks, cudaStream_t st) {
     p.inv_dim = 1.f / (float)p.D;
     const int checks = kCache ? (p.B + kVecThreads - 1) / kVecThreads : 0;      // CTAs that look over the sequences
     // several tokens to a CTA, as long as every SM gets six CTAs (2,048 tokens of 80 heads into a bf16 cache:
-    // 19.6 us with two, 21.0 with one, 24.3 with four)
+    // 17.4 us with two, 19.7 with one; 25,119 of 36 into one of 8 bits: 81.4 with eight, 83.2 with four, 95.6 with two)
     const int tokens = std::max(1, std::min(kTokens, p.N / (6 * std::max(1, device_sm_count()))));
     const long blocks = checks + ((long)p.N + tokens - 1) / tokens;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
