@@ -1106,7 +1106,7 @@ sd_status pack_axes(NormRopeParams &p, const sd_rope_axes *axes) {
     return SD_OK;
 }
 
-// what the calls with norms and axes share; `n_axes` positions per token where p.positions is given
+// what the calls with norms and axes share; a row of positions per axis where p.positions is given
 sd_status check_norm(NormRopeParams &p, sd_rope_layout layout, const sd_rope_axes *axes) {
     RopeParams r = {};               // the limits are the plain rotary calls'
     r.dt = p.dt; r.N = p.N; r.D = p.D; r.rot = p.rot; r.Hq = p.Hq; r.Hk = p.Hk; r.magnitude = p.magnitude;

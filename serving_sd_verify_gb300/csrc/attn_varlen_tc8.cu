@@ -21,13 +21,28 @@
 // l takes P before any rounding.
 //
 // Warps as in attn_varlen_tc.cu, except that the softmax warps split and write Q
-// (thread = row, which keeps its power of two) and warp 2 reads the scales ahead and
-// hands them over in a ring of kScaleSlots tiles.
+// (thread = row, which keeps its power of two), warp 2 reads the scales ahead and
+// hands them over in a ring of kScaleSlots tiles, and warp 3 works out the units for
+// all of them.
 // Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [384,384+D).  A
 // tile's scores come in two parts of 64 keys, whose weights go over the first 32 of
 // their 64 columns: while a stream's softmax has one part, the tensor pipe adds the
 // other's weights to O and makes the next tile's scores there, so that a warp does not
-// wait for its own products (2,048 over 32,768: of 5,400 clocks a pair of tiles 2,300).
+// wait for its own products (2,048 over 32,768: 5,400 clocks a pair of tiles, 2,300 of
+// them the pipe's; in one part 6,000).  Where a call's rows fit 32 of a tile's 128
+// (decoding), Q's tile holds them four times and warp w of a stream takes keys
+// [32 w, 32 w + 32) of a tile for all of them (64 sequences of one token: 119 -> 90 us).
+//
+// Measured.  2,048 tokens over 32,768 (64 / 8 heads): 2.07 ms, 1.03 PFLOP/s, against
+// 1.49 in bf16; one token over 25,119 (28 / 4) 20.7 us for 26.5 MB; 64 sequences of one
+// over 1,000 to 9,000, pages of 16, 87 us for 249 MB; 8 trees of 60 nodes 155 us.
+// What bounds it: the one warp that issues the products -- a part of 64 keys costs it
+// 715 clocks of products (a product 64 columns wide reads Q's 128 rows again) and 450
+// of waits and commits -- and in calls of few rows a tile's chain of scores, softmax and
+// second product (2,320 clocks) and a unit's start and end (9,000).  A second
+// issuing warp: 2.2 to 4.2 ms; four softmax warpgroups: 2.5 to 3.6 (104 registers a
+// thread spill); exponents and the e4m3 conversions (one warp instruction a clock an
+// SM) stay below both.
 //
 // Every wait is bounded; one that gives up sets the fault word, and the CTA
 // drains its copies and MMAs before it returns.
@@ -1134,7 +1149,10 @@ cudaError_t launch_tc8(const VarlenParams &p, int grid, cudaStream_t st) {
         const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)box_rows, 1, 1}, one[4] = {1, 1, 1, 1};
         if (fn(&m[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(i ? p.v : p.k), dims, strides, box, one,
                CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+               // a row's own bytes: 256 would fetch the next heads' with them, for CTAs that come much later (64
+               // sequences of one token: 315 MB from memory against 249)
+               D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
     cudaError_t e = configure8<D, kRows, kTree>();

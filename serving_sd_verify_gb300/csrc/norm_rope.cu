@@ -107,7 +107,9 @@ norm_rope_row_kernel(const __grid_constant__ NormRopeParams p, const long rows, 
 // 17.4 us (4.8 TB/s).  A lane group with angles of its own for four heads took 97, 171 and
 // 26 us, two rows in flight a lane 99, 126 and 26 (registers for five CTAs an SM only), one
 // warp a token with loads ahead in registers or in a ring of cp.async 76 to 101 and 92;
-// seven CTAs an SM are as many as fit without spills (six: 74.3, 87.4 and 22.6).
+// seven CTAs an SM are as many as fit without spills in the loop (six: 74.3, 87.4 and
+// 22.6, eight: 72.6, 84.1 and 18.4 with four tokens a CTA, which seven do in 69.9, 83.2
+// and 17.4).
 constexpr int kVecThreads = 128;
 constexpr int kRows = 1;             // of a lane in flight
 constexpr int kTokens = 8;           // of a CTA at most
