@@ -639,7 +639,7 @@ sd_status sd_norm_rotary(const void *q, int64_t q_tok, int64_t q_head, void *q_o
  * head -- of K and of V has an fp32 scale: the value is code * scale.
  *   k, v   device fp32 [n_pages, Hkv, page_size] contiguous, 16-byte aligned
  * A row x is written with m = max(max |x|, 2^-100) as scale = m / 448 (448 is the
- * largest e4m3 value) and codes x (448 / m), in fp32 and to nearest: an element is
+ * largest e4m3 value) and codes x 448 / m, the quotient rounded to nearest: an element is
  * off by 2^-4 of itself at most, and by 2^-10 scale where it is small.
  * Rows are taken to be finite.
  * ------------------------------------------------------------------------ */

@@ -43,10 +43,32 @@ __device__ __forceinline__ float4 from_e4m3x4(uint32_t codes) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// a row's scale by its largest magnitude, and what its elements are multiplied by
+// a row's scale by its largest magnitude m, and its elements u as u 448 / m
 constexpr float kE4m3Max = 448.f, kE4m3Tiny = 0x1p-100f;
 __device__ __forceinline__ float e4m3_scale(float amax) { return __fdiv_rn(fmaxf(amax, kE4m3Tiny), kE4m3Max); }
-__device__ __forceinline__ float e4m3_inverse(float amax) { return __fdiv_rn(kE4m3Max, fmaxf(amax, kE4m3Tiny)); }
+// u 448 / m to the nearest fp32 value.  For bf16 rows u 448 / m often is the middle of two codes, and a product
+// with 448 / m, rounded before, then falls to either side by chance (1 code in 1,000).  So the product q is
+// corrected by what it leaves (Markstein's correction of a quotient): q + (7/8 u - q (m / 512)) (512 / m), which
+// cannot overflow, and whose bracket rounds at 2^-28 of u.
+struct RowCodes {
+    float mul, part, inv;            // 448 / m, m / 512, 512 / m
+    __device__ __forceinline__ explicit RowCodes(float amax) {
+        const float m = fmaxf(amax, kE4m3Tiny);
+        mul = __fdiv_rn(kE4m3Max, m);
+        part = m * 0x1p-9f;
+        inv = mul * (512.f / 448.f);
+    }
+    __device__ __forceinline__ float operator()(float u) const {
+        const float q = __fmul_rn(u, mul);
+        return fmaf(fmaf(u, -0.125f, fmaf(-q, part, u)), inv, q);
+    }
+    __device__ __forceinline__ float2 operator()(float2 u) const {
+        const float2 q = __fmul2_rn(u, make_float2(mul, mul));
+        const float2 left = __ffma2_rn(u, make_float2(-0.125f, -0.125f),
+                                       __ffma2_rn(make_float2(-q.x, -q.y), make_float2(part, part), u));
+        return __ffma2_rn(left, make_float2(inv, inv), q);
+    }
+};
 
 }  // namespace
 

@@ -5,7 +5,7 @@
 // For a row x of D elements (one head of a token), weight w:
 //   u = w x / sqrt(mean(x^2) + eps);  (u_a, u_b) -> (u_a c - u_b s, u_b c + u_a s)
 // with c, s of positions[axis(i)] * w_i for pair i; a cached row then as codes
-// u (448 / max |u|).  All in fp32 registers, each row read once.
+// u 448 / max |u|.  All in fp32 registers, each row read once.
 #include "e4m3.cuh"
 #include "rope.cuh"
 
@@ -89,8 +89,8 @@ norm_rope_row_kernel(const __grid_constant__ NormRopeParams p, const long rows, 
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     uint8_t *codes = static_cast<uint8_t *>(role == 1 ? p.k_pages : p.v_pages) + at;
-    const float mul = e4m3_inverse(amax);
-    visit([&](int i, float v) { codes[i] = (uint8_t)e4m3x2(v * mul, 0.f); });
+    const RowCodes code(amax);
+    visit([&](int i, float v) { codes[i] = (uint8_t)e4m3x2(code(v), 0.f); });
     if (lane == 0)
         (role == 1 ? p.k_scale : p.v_scale)[((long)page * p.Hk + h) * p.page_size + slot] = e4m3_scale(amax);
 }
@@ -103,7 +103,7 @@ norm_rope_row_kernel(const __grid_constant__ NormRopeParams p, const long rows, 
 // shuffles among its lanes.  Arithmetic comes two elements an instruction: what bounds
 // the kernel besides memory is the instructions it issues.
 // Measured (bf16, three axes): 25,119 tokens of 32 heads of 128 69.5 us (5.9 TB/s of 6.8),
-// of 28 with 8 written as e4m3 81.4 us (5.4 TB/s), 2,048 tokens of 80 into a bf16 cache
+// of 28 with 8 written as e4m3 80.2 us (5.5 TB/s), 2,048 tokens of 80 into a bf16 cache
 // 17.4 us (4.8 TB/s).  A lane group with angles of its own for four heads took 97, 171 and
 // 26 us, two rows in flight a lane 99, 126 and 26 (registers for five CTAs an SM only), one
 // warp a token with loads ahead in registers or in a ring of cp.async 76 to 101 and 92;
@@ -266,14 +266,16 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1)
                         if (o < width) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    const float mul = e4m3_inverse(amax);
+                    const RowCodes code(amax);
                     uint8_t *codes = static_cast<uint8_t *>(kRole == 1 ? p.k_pages : p.v_pages) + (long)at[1] * p.pages.b +
                                      (long)at[2] * p.pages.s + (long)ch[i] * p.pages.h;
                     auto put = [&](int o, const float2 (&f)[H]) {
                         uint32_t q[V / 4];
 #pragma unroll
-                        for (int e = 0; e < V / 4; ++e)
-                            q[e] = e4m3x4(f[2 * e].x * mul, f[2 * e].y * mul, f[2 * e + 1].x * mul, f[2 * e + 1].y * mul);
+                        for (int e = 0; e < V / 4; ++e) {
+                            const float2 x = code(f[2 * e]), y = code(f[2 * e + 1]);
+                            q[e] = e4m3x4(x.x, x.y, y.x, y.y);
+                        }
                         if constexpr (V == 8) *reinterpret_cast<uint2 *>(codes + o) = make_uint2(q[0], q[1]);
                         else *reinterpret_cast<uint32_t *>(codes + o) = q[0];
                     };

@@ -48,8 +48,8 @@ def check_rows(got, want, off, dtype):
 def quantise(x):
     """Codes and scales of fp32 rows, by the definition."""
     top = x.abs().amax(-1, keepdim=True).clamp_min(TINY)
-    mul = torch.full_like(top, TOP) / top        # one division (a number over a tensor is a reciprocal and a product)
-    return (x * mul).clamp(-TOP, TOP).to(torch.float8_e4m3fn), (top / TOP)[..., 0]
+    codes = (x.double() * TOP / top.double()).float()          # (exact ties among bf16 rows' quotients stay ties)
+    return codes.clamp(-TOP, TOP).to(torch.float8_e4m3fn), (top / TOP)[..., 0]
 
 
 def check_codes(codes, scale, want, off):
