@@ -669,8 +669,9 @@ sd_status sd_norm_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_he
  * bf16 over pages of a multiple of 8 slots runs on the tensor cores, in e4m3: q as
  * the sum of two e4m3 terms (exact for elements above 2^-9 of their row's
  * largest, off by 2^-18 of that largest below), a weight times its value's scale as
- * two terms (off by 2^-9 of itself, or by 2^-16 of the row's largest weight times
- * the largest scale so far where that is more), fp32 sums.
+ * two terms (off by 2^-9 of itself, or by 2^-13 of the largest such product of the
+ * row where that is more), fp32 sums.  What a row does not see takes no part in it,
+ * whatever its size.
  * Scales of slots at and past kv_len[b] may hold anything; those inside a sequence
  * are finite and not negative. */
 sd_status sd_paged_attention_e4m3(const void *q, int64_t q_tok, int64_t q_head, const sd_paged_cache *cache,

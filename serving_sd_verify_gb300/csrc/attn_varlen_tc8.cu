@@ -6,18 +6,23 @@
 // ever widened, so a tile of 128 keys is 16 KB to copy and to read instead of 32.
 // With k_n, v_n the scales of key n, and for a unit (up to 256 query rows, as in
 // attn_varlen_tc.cu, whose tiles, streams and joins these are):
-//   S = (Q1 + Q2) K^T,  x_n = S_n k_n c,  m = max x,  P_n = exp2(x_n - m)
-//   l = sum P_n,  W_n = P_n v_n / v,  O = (W1 + W2) V,  out = O v / l
+//   S = (Q1 + Q2) K^T,  x_n = S_n k_n c,  m = max(x_n + log2 v_n) of the keys that the row sees
+//   P_n = 32 exp2(x_n - m),  l = sum P_n,  W_n = P_n v_n,  O = (W1 + W2) V,  out = O / l
 //   Q: a row times a power of two that brings its largest element to [128, 256), as
 //     a first e4m3 term and, exactly, what that leaves: a bf16 element has 8 bits and
 //     each term holds 4, so the two are the element itself where it is above 2^-10
 //     of the row's largest, and off by 2^-18 of the largest where not.  c is that
 //     power's inverse times scale log2(e).
-//   v: the largest v_n of the stream's tiles so far; the weights of values that are
-//     small against others' are small.  Where it grows, O is rescaled as where m does.
-//   W: 64 W_n in two e4m3 terms, the second what the first leaves: off by 2^-9 of
-//     itself, or by 2^-16 of the reference where it is small.  m moves where
-//     the maximum grows by more than 2^2 (2^16 in bf16), so 64 W_n stays below 448.
+//   m: of what the keys contribute, their values' scales among it: a row's weights are
+//     written against nothing but what the row itself sees, and neither a value that it
+//     does not see, however large, nor one that it sees of small values, however large
+//     its score, takes precision from the others.  It moves where a weight would pass
+//     what two terms hold (max x and the part's largest scale tell that none does, mostly),
+//     to max x and that scale where all the part's keys are seen and their scales are alike,
+//     else to the keys' own (a third reading of each key's scales, which always done
+//     made 2,048 over 32,768 2.77 ms; weights made first and looked over behind: 2.7 to 2.9).
+//   W: in two e4m3 terms, the second what the first leaves: off by 2^-9 of
+//     itself, or by 2^-10 where it is small.
 // l takes P before any rounding.
 //
 // Warps as in attn_varlen_tc.cu, except that the softmax warps split and write Q
@@ -33,9 +38,9 @@
 // (decoding), Q's tile holds them four times and warp w of a stream takes keys
 // [32 w, 32 w + 32) of a tile for all of them (64 sequences of one token: 119 -> 90 us).
 //
-// Measured.  2,048 tokens over 32,768 (64 / 8 heads): 2.07 ms, 1.03 PFLOP/s, against
-// 1.49 in bf16; one token over 25,119 (28 / 4) 20.7 us for 26.5 MB; 64 sequences of one
-// over 1,000 to 9,000, pages of 16, 87 us for 249 MB; 8 trees of 60 nodes 155 us.
+// Measured.  2,048 tokens over 32,768 (64 / 8 heads): 2.17 ms, 0.98 PFLOP/s, against
+// 1.49 in bf16; one token over 25,119 (28 / 4) 20.6 us for 26.5 MB; 64 sequences of one
+// over 1,000 to 9,000, pages of 16, 86 us for 249 MB; 8 trees of 60 nodes 164 us.
 // What bounds it: the one warp that issues the products -- a part of 64 keys costs it
 // 715 clocks of products (a product 64 columns wide reads Q's 128 rows again) and 450
 // of waits and commits -- and in calls of few rows a tile's chain of scores, softmax and
@@ -53,21 +58,23 @@ namespace sdv {
 
 namespace {
 
-constexpr float kRescale8 = 2.0f;           // log2 units
-constexpr float kWeightScale = 64.0f;       // 64 * 2^kRescale8 <= 448
+// In log2 units: the largest weight when m has been chosen; what a weight may be (448, e4m3's largest, and what the
+// second term still holds to 2^-9 of it); what P may be (so that 2^26 of them, with rows of zeros beside others, stay
+// finite); by how much scales that are alike differ.
+constexpr float kWeightLog = 5.0f, kWeightTop = 8.9f, kSumTop = 90.0f, kAlike = 1.5f;
 constexpr int kScaleSlots = 4;
 
-// a tile's scales: K's, kWeightScale times V's against `ref`, which was `ratio` times that before this tile
+// a tile's scales, V's logarithms, and the largest and the smallest of those of each 32 keys
 struct Scales {
-    float k[128], v[128];
-    float ratio, ref;
-    float pad[2];
+    float k[128], v[128], log_v[128];
+    float2 range[4];
 };
-
-struct Misc8 : Misc {
-    float vref[2];
-};
-static_assert(sizeof(Misc8) <= 512, "the misc area");
+// log2 of a scale, of no less than 2^-80: a row of zeros has a scale of 2^-109, and its P should stay finite
+__device__ __forceinline__ float log_scale(float v) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(v, 0x1p-80f)));
+    return y;
+}
 
 // The CTA's units, worked out by warp 3 ahead of everyone (each role's own walk would be on its way at
 // every unit, and four copies of its code in the instruction cache).  Softmax warps read theirs here
@@ -184,6 +191,20 @@ __device__ __forceinline__ float put_query(const __nv_bfloat16 *q, uint8_t *tile
     return e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ec - 7) << 23);
 }
 
+// A row's m: what is added to x; whether one of a part's weights may pass what e4m3 holds, by the largest x and the
+// largest of the part's scales (or the row has no m yet); and the move to `top`, the largest of what the part's keys
+// contribute, where one does.  Returns what the row's sums have to be multiplied by.
+__device__ __forceinline__ float weight_unit(float m) { return m == -INFINITY ? 0.f : kWeightLog - m; }
+__device__ __forceinline__ bool may_pass(float xmax, float neg_m, float log_top, float m) {
+    return (m == -INFINITY && xmax > -INFINITY) || xmax + neg_m > fminf(kWeightTop - log_top, kSumTop) - 0.02f;   // (roundings aside)
+}
+__device__ __forceinline__ float move_unit(bool row_ok, float xmax, float top, float &m) {
+    if (!row_ok || !(top > m + (kWeightTop - kWeightLog) || xmax > m + (kSumTop - kWeightLog))) return 1.f;
+    const float alpha = ex2(m - top);
+    m = top;
+    return alpha;
+}
+
 // kRows: what one unit holds.  kPairs: up to 256 rows.  kSmall: no sequence has more
 // rows of a kv head than one tile holds, and the second row tile's room is ring
 // slots.  kQuad: none has more than 32 (decoding).  Four copies of the rows then lie
@@ -235,7 +256,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
     };
     Scales *scales = reinterpret_cast<Scales *>(sbase + L::kOffScale);
     float *xrow = reinterpret_cast<float *>(sbase + L::kOffMl);      // [2][128]: one value per stream and row
-    Misc8 *misc = reinterpret_cast<Misc8 *>(sbase + L::kOffMisc);
+    Misc *misc = reinterpret_cast<Misc *>(sbase + L::kOffMisc);
     volatile int *abort_flag = &misc->abort_flag;
 
     if (tid == 0) {
@@ -512,8 +533,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 __syncwarp();
             } else if (warp == 2) {
                 // ---------------------------------------------------------- scales
-                // a tile's K scales, and its V scales against the largest of the stream's so far: four keys a lane,
-                // pages looked up two tiles ahead and scales read one ahead
+                // a tile's scales: four keys a lane, pages looked up two tiles ahead and scales read one ahead
                 unsigned done = 0;
                 bool ok = true;
                 while (next_unit()) {
@@ -521,7 +541,6 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     done_unit();
                     const int n = u.t1 - u.t0;
                     if (n <= 0 || !ok) continue;
-                    const bool pair = !kSmall && u.ntok > tpt;
                     const int32_t *trow = p.table + (long)u.b * p.table_stride;
                     auto page_of = [&](int j) {
                         const int key = (u.t0 + j) * 128 + 4 * lane;
@@ -538,7 +557,6 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             vs = __ldg(reinterpret_cast<const float4 *>(p.v_scale + at));
                         }
                     };
-                    float ref = 0.f, other = 0.f;          // of this tile's stream, and of the one in turn with it
                     int pg = page_of(1);
                     fetch(0, page_of(0));
                     for (int j = 0; j < n; ++j, ++done) {
@@ -552,25 +570,25 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             if (left < 2) k4.y = v4.y = 0.f;
                             if (left < 1) k4.x = v4.x = 0.f;
                         }
-                        float top = fmaxf(max3(v4.x, v4.y, v4.z), v4.w);
+                        const float4 lv = make_float4(log_scale(v4.x), log_scale(v4.y), log_scale(v4.z), log_scale(v4.w));
+                        float top = fmaxf(max3(lv.x, lv.y, lv.z), lv.w), low = fminf(fminf(lv.x, lv.y), fminf(lv.z, lv.w));
 #pragma unroll
-                        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const float grown = fmaxf(ref, top);
-                        const float ratio = ref == grown ? 1.f : __fdiv_rn(ref, grown);
-                        ref = grown;
+                        for (int o = 4; o; o >>= 1) {
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+                        }
                         const unsigned slot = done % kScaleSlots;
                         if (done >= kScaleSlots)
                             ok = wait_bar(scempty_bar(slot), (done / kScaleSlots - 1) & 1u, abort_flag, p.fault);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         Scales &to = scales[slot];
-                        auto share = [&](float v) { return ref > 0.f ? kWeightScale * __fdiv_rn(v, ref) : 0.f; };
                         reinterpret_cast<float4 *>(to.k)[lane] = k4;
-                        reinterpret_cast<float4 *>(to.v)[lane] = make_float4(share(v4.x), share(v4.y), share(v4.z), share(v4.w));
-                        if (lane == 0) { to.ratio = ratio; to.ref = ref; }
+                        reinterpret_cast<float4 *>(to.v)[lane] = v4;
+                        reinterpret_cast<float4 *>(to.log_v)[lane] = lv;
+                        if ((lane & 7) == 0) to.range[lane >> 3] = make_float2(top, low);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(scfull_bar(slot));
-                        if (!pair) { const float t = ref; ref = other; other = t; }
                     }
                 }
             } else if (warp == 3) {
@@ -626,7 +644,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 const uint64_t word = kTree && row_ok ? vl_tree_word(p, u, tl) : 0;
                 // rows this warp has to do anything for
                 const bool warp_live = __any_sync(0xffffffffu, row_ok);
-                float m_used = -INFINITY, l = 0.f, vref = 0.f, qk = 0.f;
+                float m_used = -INFINITY, l = 0.f, qk = 0.f;
                 // Q in two e4m3 terms.  The tile's last readers are done: a stream's own products have been
                 // waited for, and where both write one tile behind a pair of them, they meet first.
                 if (!pair && was_pair) named_sync(2, 256);
@@ -668,8 +686,6 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     const unsigned tile = before + j, sc = tile % kScaleSlots;
                     ok = __all_sync(0xffffffffu, wait_bar(scfull_bar(sc), (tile / kScaleSlots) & 1u, abort_flag, p.fault)) && ok;
                     const Scales &ts = scales[sc];
-                    const float ratio = ts.ratio;
-                    vref = ts.ref;
                     if constexpr (kQuad) {
                         uint32_t s[32];
                         tmem_ld32_async(s_col + 32u * quarter, s);
@@ -691,7 +707,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             s[e + 2] = __float_as_uint(__uint_as_float(s[e + 2]) * f.z);
                             s[e + 3] = __float_as_uint(__uint_as_float(s[e + 3]) * f.w);
                         }
-                        if (!__all_sync(0xffffffffu, seen == 0xffffffffu || !row_ok)) {
+                        const bool edge = !__all_sync(0xffffffffu, seen == 0xffffffffu || !row_ok);
+                        if (edge) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (!(seen >> e & 1)) s[e] = 0xff800000u;
@@ -702,28 +719,38 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         for (int e = 4; e < 16; e += 2) m = max3(m, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
 #pragma unroll
                         for (int e = 16; e < 30; e += 2) m2 = max3(m2, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                        const float tmax = qk * max3(m, m2, __uint_as_float(s[30]));
-                        const bool need = row_ok && tmax > m_used + kRescale8;
-                        float alpha = 1.f;
-                        if (need) {
-                            alpha = ex2(m_used - tmax);
-                            m_used = tmax;
-                        }
-                        if (j > j0 && __any_sync(0xffffffffu, need || ratio != 1.f)) {
-                            const float f = alpha * ratio;
-                            uint32_t o[D / 32][32];
+                        const float xmax = qk * max3(m, m2, __uint_as_float(s[30]));
+                        float neg_m = weight_unit(m_used);
+                        const float2 range = ts.range[quarter];
+                        if (__any_sync(0xffffffffu, row_ok && may_pass(xmax, neg_m, range.x, m_used))) {
+                            float top = xmax + range.x;
+                            if (edge || range.x > range.y + kAlike) {
+                                float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) tmem_ld32_async(o_col + 32u * c, o[c]);
-                            tmem_ld_wait();
+                                for (int g = 0; g < 8; ++g) {
+                                    const float4 f = reinterpret_cast<const float4 *>(ts.log_v)[8 * quarter + g];
+                                    t[0] = max3(t[0], fmaf(__uint_as_float(s[4 * g]), qk, f.x), fmaf(__uint_as_float(s[4 * g + 1]), qk, f.y));
+                                    t[1] = max3(t[1], fmaf(__uint_as_float(s[4 * g + 2]), qk, f.z), fmaf(__uint_as_float(s[4 * g + 3]), qk, f.w));
+                                }
+                                top = fmaxf(t[0], t[1]);
+                            }
+                            const float alpha = move_unit(row_ok, xmax, top, m_used);
+                            neg_m = weight_unit(m_used);
+                            l *= alpha;
+                            if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                                uint32_t o[D / 32][32];
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                tmem_ld_bind(o[c]);
+                                for (int c = 0; c < D / 32; ++c) tmem_ld32_async(o_col + 32u * c, o[c]);
+                                tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[c][e] = __float_as_uint(__uint_as_float(o[c][e]) * f);
-                                tmem_st32(o_col + 32u * c, o[c]);
+                                for (int c = 0; c < D / 32; ++c) {
+                                    tmem_ld_bind(o[c]);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[c][e] = __float_as_uint(__uint_as_float(o[c][e]) * alpha);
+                                    tmem_st32(o_col + 32u * c, o[c]);
+                                }
                             }
                         }
-                        const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
                         float ls[2] = {0.f, 0.f};
                         uint32_t hi[8], lo[8];
                         const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
@@ -748,7 +775,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         }
                         tmem_st8(s_col + 8u * quarter, hi);
                         tmem_st8(s_col + 32u + 8u * quarter, lo);
-                        l = l * alpha + (ls[0] + ls[1]);
+                        l += ls[0] + ls[1];
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
@@ -794,7 +821,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                     const int vis = lim - from;         // this row sees the first `vis` of the keys
                                     if (vis < 64) seen = vis <= 0 ? 0ull : (1ull << vis) - 1;
                                 }
-                                if (!__all_sync(0xffffffffu, seen == ~0ull || !row_ok)) {
+                                const bool edge = !__all_sync(0xffffffffu, seen == ~0ull || !row_ok);
+                                if (edge) {
 #pragma unroll
                                     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -810,31 +838,44 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                     for (int e = 3; e < 15; e += 2) m = max3(m, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                                     m4[i] = fmaxf(m, __uint_as_float(x[15]));
                                 }
-                                const float tmax = qk * fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-                                const bool need = row_ok && tmax > m_used + kRescale8;    // true at first while m_used = -inf
-                                float alpha = 1.f;
-                                if (need) {
-                                    alpha = ex2(m_used - tmax);         // 0 while nothing is held
-                                    m_used = tmax;
-                                }
-                                const float f = h ? alpha : alpha * ratio;
-                                if ((j > j0 || h) && __any_sync(0xffffffffu, f != 1.f)) {
-                                    // the part before this one has to be in O: the others are, their products went
-                                    // out before this part's scores and complete in order
-                                    ok = __all_sync(0xffffffffu, wait_bar(oadd_bar(w), (added - 1) & 1u, abort_flag, p.fault)) && ok;
-                                    tc_fence_after();
-#pragma unroll 1
-                                    for (int c = 0; c < D / 32; ++c) {
-                                        uint32_t o[32];
-                                        tmem_ld32_async(o_col + 32u * c, o);
-                                        tmem_ld_wait();
-                                        tmem_ld_bind(o);
+                                const float xmax = qk * fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+                                float neg_m = weight_unit(m_used);
+                                const float4 range = reinterpret_cast<const float4 *>(ts.range)[h];
+                                const float log_top = fmaxf(range.x, range.z);
+                                if (__any_sync(0xffffffffu, row_ok && may_pass(xmax, neg_m, log_top, m_used))) {
+                                    float top = xmax + log_top;
+                                    if (edge || log_top > fminf(range.y, range.w) + kAlike) {
+                                        const float4 *lv = reinterpret_cast<const float4 *>(ts.log_v) + 16 * h;
+                                        float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                        tmem_st32(o_col + 32u * c, o);
+                                        for (int g = 0; g < 16; ++g) {
+                                            const uint32_t *x = s[g >> 3] + 4 * (g & 7);
+                                            const float4 y = lv[g];
+                                            t[0] = max3(t[0], fmaf(__uint_as_float(x[0]), qk, y.x), fmaf(__uint_as_float(x[1]), qk, y.y));
+                                            t[1] = max3(t[1], fmaf(__uint_as_float(x[2]), qk, y.z), fmaf(__uint_as_float(x[3]), qk, y.w));
+                                        }
+                                        top = fmaxf(t[0], t[1]);
+                                    }
+                                    const float alpha = move_unit(row_ok, xmax, top, m_used);
+                                    neg_m = weight_unit(m_used);
+                                    l *= alpha;
+                                    if ((j > j0 || h) && __any_sync(0xffffffffu, alpha != 1.f)) {
+                                        // the part before this one has to be in O: the others are, their products went
+                                        // out before this part's scores and complete in order
+                                        ok = __all_sync(0xffffffffu, wait_bar(oadd_bar(w), (added - 1) & 1u, abort_flag, p.fault)) && ok;
+                                        tc_fence_after();
+#pragma unroll 1
+                                        for (int c = 0; c < D / 32; ++c) {
+                                            uint32_t o[32];
+                                            tmem_ld32_async(o_col + 32u * c, o);
+                                            tmem_ld_wait();
+                                            tmem_ld_bind(o);
+#pragma unroll
+                                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                            tmem_st32(o_col + 32u * c, o);
+                                        }
                                     }
                                 }
-                                const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
                                 const float2 qk2 = make_float2(qk, qk), nm2 = make_float2(neg_m, neg_m);
                                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                                 // the weights go over scores that have been read: the first terms in the part's
@@ -850,7 +891,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                     ls[0] = __fadd2_rn(ls[0], p0);
                                     ls[1] = __fadd2_rn(ls[1], p1);
                                     const float2 w0 = __fmul2_rn(p0, make_float2(y.x, y.y)), w1 = __fmul2_rn(p1, make_float2(y.z, y.w));
-                                    // (in f16, 2^-12 off; the first term's rest is exact there)
+                                    // (in f16, 2^-11 off at most; the first term's rest is exact there)
                                     const __half2 v0 = __floats2half2_rn(w0.x, w0.y), v1 = __floats2half2_rn(w1.x, w1.y);
                                     __half2 h0, h1;
                                     hi[g] = e4m3x4(v0, v1);
@@ -859,7 +900,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                 }
                                 tmem_st16(at, hi);
                                 tmem_st16(at + 16u, lo);
-                                l = l * alpha + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
+                                l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
                                 tmem_st_wait();
                             }
                             tc_fence_before();
@@ -900,12 +941,11 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 }
                 ring += 2 * max(n, 0);
                 before += max(n, 0);
-                float a0 = vref / kWeightScale, a1 = 0.f;
+                float a0 = 1.f, a1 = 0.f;
                 if (!pair) {
                     // join the two streams of the one row tile: they exchange the row's maximum, then
                     // its sum, and each takes half of the columns of both accumulators
                     xrow[128 * w + r] = m_used;
-                    if (r == 0) misc->vref[w] = vref / kWeightScale;
                     named_sync(1, 256);
                     const float mo = xrow[128 * (w ^ 1) + r];
                     float m = fmaxf(m_used, mo);
@@ -917,8 +957,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     const float own = ex2(m_used - ref), other = ex2(mo - ref);
                     l *= own;
                     m_used = m;
-                    a0 = (w == 0 ? own : other) * misc->vref[0];
-                    a1 = (w == 0 ? other : own) * misc->vref[1];
+                    a0 = w == 0 ? own : other;
+                    a1 = w == 0 ? other : own;
                     named_sync(2, 256);
                     xrow[128 * w + r] = l;
                     named_sync(1, 256);
