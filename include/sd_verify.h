@@ -668,9 +668,10 @@ sd_status sd_norm_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_he
  * sd_paged_attention's.
  * bf16 over pages of a multiple of 8 slots runs on the tensor cores, in e4m3: q as
  * the sum of two e4m3 terms (exact for elements above 2^-9 of their row's
- * largest, off by 2^-18 of that largest below), a weight times its value's scale as
- * two terms (off by 2^-9 of itself, or by 2^-13 of the largest such product of the
- * row where that is more), fp32 sums.  What a row does not see takes no part in it,
+ * largest, off by 2^-18 of that largest below), a weight times its value's scale in
+ * f16 and that as three e5m2 terms (off by 2^-9 of itself; where it is small it may be
+ * dropped, which takes 2^-8 of their sum from a row's weights at most, for max_kv up to
+ * 2^21, however they lie), fp32 sums.  What a row does not see takes no part in it,
  * whatever its size.
  * Scales of slots at and past kv_len[b] may hold anything; those inside a sequence
  * are finite and not negative. */

@@ -7,7 +7,7 @@
 // With k_n, v_n the scales of key n, and for a unit (up to 256 query rows, as in
 // attn_varlen_tc.cu, whose tiles, streams and joins these are):
 //   S = (Q1 + Q2) K^T,  x_n = S_n k_n c,  m = max(x_n + log2 v_n) of the keys that the row sees
-//   P_n = 32 exp2(x_n - m),  l = sum P_n,  W_n = P_n v_n,  O = (W1 + W2) V,  out = O / l
+//   P_n = 2^u exp2(x_n - m),  l = sum P_n,  W_n = P_n v_n,  O = (W1 + W2 + W3) V,  out = O / l
 //   Q: a row times a power of two that brings its largest element to [128, 256), as
 //     a first e4m3 term and, exactly, what that leaves: a bf16 element has 8 bits and
 //     each term holds 4, so the two are the element itself where it is above 2^-10
@@ -21,8 +21,14 @@
 //     to max x and that scale where all the part's keys are seen and their scales are alike,
 //     else to the keys' own (a third reading of each key's scales, which always done
 //     made 2,048 over 32,768 2.77 ms; weights made first and looked over behind: 2.7 to 2.9).
-//   W: in two e4m3 terms, the second what the first leaves: off by 2^-9 of
-//     itself, or by 2^-10 where it is small.
+//   W: in f16, and that in three e5m2 terms of 3 bits each (an e5m2 code is the upper
+//     byte of an f16 value): off by 2^-9 of itself, or by 2^-17 where it is small.  With u
+//     of 9 that is 2^-24 of the row's largest, so that a long rest far below one large
+//     weight is kept: the 65,536 keys that it holds for lose 2^-8 of the sum of the weights
+//     together at most, and for longer caches u grows with them.  (Two e4m3 terms end
+//     at 2^-10 and 2^-14 of the largest: with one key 12 nats above 32,768 others a third
+//     of the output went; one in e4m3 and one in e5m2 with m moved down where the
+//     small ones had lost too much: 2.69 ms and twice the error.)
 // l takes P before any rounding.
 //
 // Warps as in attn_varlen_tc.cu, except that the softmax warps split and write Q
@@ -30,24 +36,24 @@
 // hands them over in a ring of kScaleSlots tiles, and warp 3 works out the units for
 // all of them.
 // Tensor memory: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 [384,384+D).  A
-// tile's scores come in two parts of 64 keys, whose weights go over the first 32 of
+// tile's scores come in two parts of 64 keys, whose weights go over the first 48 of
 // their 64 columns: while a stream's softmax has one part, the tensor pipe adds the
 // other's weights to O and makes the next tile's scores there, so that a warp does not
-// wait for its own products (2,048 over 32,768: 5,400 clocks a pair of tiles, 2,300 of
-// them the pipe's; in one part 6,000).  Where a call's rows fit 32 of a tile's 128
+// wait for its own products (with two terms, 2,048 over 32,768: 5,400 clocks a pair of
+// tiles, in one part 6,000).  Where a call's rows fit 32 of a tile's 128
 // (decoding), Q's tile holds them four times and warp w of a stream takes keys
 // [32 w, 32 w + 32) of a tile for all of them (64 sequences of one token: 119 -> 90 us).
 //
-// Measured.  2,048 tokens over 32,768 (64 / 8 heads): 2.17 ms, 0.98 PFLOP/s, against
-// 1.49 in bf16; one token over 25,119 (28 / 4) 20.6 us for 26.5 MB; 64 sequences of one
-// over 1,000 to 9,000, pages of 16, 86 us for 249 MB; 8 trees of 60 nodes 164 us.
+// Measured.  2,048 tokens over 32,768 (64 / 8 heads): 2.43 ms, 0.88 PFLOP/s, against
+// 1.49 in bf16; one token over 25,119 (28 / 4) 22.2 us for 26.5 MB; 64 sequences of one
+// over 1,000 to 9,000, pages of 16, 86 us for 249 MB; 8 trees of 60 nodes 159 us.  With
+// two e4m3 terms a weight 2.17 ms, 20.6, 86 and 164 us, and a tail that gets lost.
 // What bounds it: the one warp that issues the products -- a part of 64 keys costs it
-// 715 clocks of products (a product 64 columns wide reads Q's 128 rows again) and 450
-// of waits and commits -- and in calls of few rows a tile's chain of scores, softmax and
-// second product (2,320 clocks) and a unit's start and end (9,000).  A second
-// issuing warp: 2.2 to 4.2 ms; four softmax warpgroups: 2.5 to 3.6 (104 registers a
-// thread spill); exponents and the e4m3 conversions (one warp instruction a clock an
-// SM) stay below both.
+// 8 products for the scores (64 columns wide, each reads Q's 128 rows again) and 6 for O,
+// and waits and commits -- and the chain of a part's scores, softmax and second
+// product; in calls of few rows also a unit's start and end (9,000 clocks).  With
+// two e4m3 terms were measured: a second issuing warp, 2.2 to 4.2 ms; four softmax
+// warpgroups, 2.5 to 3.6 (104 registers a thread spill).
 //
 // Every wait is bounded; one that gives up sets the fault word, and the CTA
 // drains its copies and MMAs before it returns.
@@ -58,10 +64,10 @@ namespace sdv {
 
 namespace {
 
-// In log2 units: the largest weight when m has been chosen; what a weight may be (448, e4m3's largest, and what the
-// second term still holds to 2^-9 of it); what P may be (so that 2^26 of them, with rows of zeros beside others, stay
-// finite); by how much scales that are alike differ.
-constexpr float kWeightLog = 5.0f, kWeightTop = 8.9f, kSumTop = 90.0f, kAlike = 1.5f;
+// In log2 units: the largest weight when m has been chosen, for up to 2^16 keys, and for any number; what a weight
+// may be (f16 and e5m2 end at 2^16 and 2^15.8); what P may be (so that 2^26 of them, with rows of zeros beside others,
+// stay finite); by how much scales that are alike differ.
+constexpr float kWeightLog = 9.0f, kWeightLogMost = 14.0f, kWeightTop = 15.7f, kSumTop = 90.0f, kAlike = 1.5f;
 constexpr int kScaleSlots = 4;
 
 // a tile's scales, V's logarithms, and the largest and the smallest of those of each 32 keys
@@ -123,9 +129,10 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
-// instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D, A K-major
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool b_mn_major) {
-    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// instruction descriptor, kind::f8f6f4: A e4m3 or e5m2, K-major; B e4m3; fp32 D
+__host__ __device__ constexpr uint32_t idesc_8(int M, int N, bool a_e5m2, bool b_mn_major) {
+    return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ void umma8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -191,15 +198,32 @@ __device__ __forceinline__ float put_query(const __nv_bfloat16 *q, uint8_t *tile
     return e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ec - 7) << 23);
 }
 
-// A row's m: what is added to x; whether one of a part's weights may pass what e4m3 holds, by the largest x and the
+// Two pairs of weights in f16 as e5m2 codes: the first two terms are cut off, what they leave is exact, and the
+// third is rounded.
+__device__ __forceinline__ void three_terms(__half2 a, __half2 b, uint32_t &t1, uint32_t &t2, uint32_t &t3) {
+    auto bits = [](const __half2 &x) { return *reinterpret_cast<const uint32_t *>(&x); };
+    auto upper = [&](__half2 x) {
+        const uint32_t u = bits(x) & 0xff00ff00u;
+        return *reinterpret_cast<const __half2 *>(&u);
+    };
+    t1 = __byte_perm(bits(a), bits(b), 0x7531);
+    a = __hsub2(a, upper(a));
+    b = __hsub2(b, upper(b));
+    t2 = __byte_perm(bits(a), bits(b), 0x7531);
+    a = __hsub2(a, upper(a));
+    b = __hsub2(b, upper(b));
+    t3 = __byte_perm(bits(a) + 0x00800080u, bits(b) + 0x00800080u, 0x7531);
+}
+
+// A row's m: what is added to x; whether one of a part's weights may pass what it may be, by the largest x and the
 // largest of the part's scales (or the row has no m yet); and the move to `top`, the largest of what the part's keys
 // contribute, where one does.  Returns what the row's sums have to be multiplied by.
-__device__ __forceinline__ float weight_unit(float m) { return m == -INFINITY ? 0.f : kWeightLog - m; }
+__device__ __forceinline__ float weight_unit(float log_w, float m) { return m == -INFINITY ? 0.f : log_w - m; }
 __device__ __forceinline__ bool may_pass(float xmax, float neg_m, float log_top, float m) {
     return (m == -INFINITY && xmax > -INFINITY) || xmax + neg_m > fminf(kWeightTop - log_top, kSumTop) - 0.02f;   // (roundings aside)
 }
-__device__ __forceinline__ float move_unit(bool row_ok, float xmax, float top, float &m) {
-    if (!row_ok || !(top > m + (kWeightTop - kWeightLog) || xmax > m + (kSumTop - kWeightLog))) return 1.f;
+__device__ __forceinline__ float move_unit(bool row_ok, float xmax, float top, float log_w, float &m) {
+    if (!row_ok || !(top > m + (kWeightTop - log_w) || xmax > m + (kSumTop - log_w))) return 1.f;
     const float alpha = ex2(m - top);
     m = top;
     return alpha;
@@ -387,10 +411,9 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                 {
                     const bool el = elect_one();
                     RingPos rp;
-                    uint32_t qphase = 0, pphase[2] = {0, 0}, fphase[2] = {0, 0};
-                    bool used[2] = {false, false};
+                    uint32_t qphase = 0, pphase = 0, fphase = 0, used = 0;        // (bit i: of stream i)
                     bool ok = true;
-                    const uint32_t idS = idesc_e4m3(128, 128 / kSubs, false), idO = idesc_e4m3(128, D, true);
+                    const uint32_t idS = idesc_8(128, 128 / kSubs, false, false), idO = idesc_8(128, D, true, true);
                     // the next tile of the ring: its slot
                     auto take = [&]() {
                         ok = ok && wait_bar(full_bar(rp.slot), rp.phase, abort_flag, p.fault);
@@ -420,7 +443,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                     // W_i V for part h of the V tile in `slot`
                     auto issue_pv = [&](int i, int slot, bool first, int steps, int h) {
                         const uint64_t vd = kd0 + (uint64_t)(slot * (L::kTile / 16) + h * (64 * D / 16));
-                        ok = ok && wait_bar(pfull_bar(i, h), pphase[i], abort_flag, p.fault);
+                        ok = ok && wait_bar(pfull_bar(i, h), pphase >> i & 1u, abort_flag, p.fault);
                         if (!ok) return;
                         tc_fence_after();
                         if (el) {
@@ -428,22 +451,22 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             for (int kk = 0; kk < 4 / kSubs; ++kk) {
                                 if (kSmall && kk + 2 * h >= steps) continue;
 #pragma unroll
-                                for (int term = 0; term < 2; ++term)
+                                for (int term = 0; term < 3; ++term)
                                     umma8_ts(tmem + 256u + 128u * i, tmem + 128u * i + 64u * h + 32u / kSubs * term + 8u * kk,
                                              vd + kk * (32 * D / 16), idO, (!first || kk + term > 0) ? 1u : 0u);
                             }
                             if (kSubs > 1) umma_commit(oadd_bar(i));
                         }
-                        if (h == kSubs - 1) pphase[i] ^= 1u;
+                        if (h == kSubs - 1) pphase ^= 1u << i;
                     };
                     // O_i free for a new unit
                     auto claim = [&](int i) {
-                        if (used[i]) {
-                            ok = ok && wait_bar(ofree_bar(i), fphase[i], abort_flag, p.fault);
+                        if (used >> i & 1u) {
+                            ok = ok && wait_bar(ofree_bar(i), fphase >> i & 1u, abort_flag, p.fault);
                             tc_fence_after();
-                            fphase[i] ^= 1u;
+                            fphase ^= 1u << i;
                         }
-                        used[i] = true;
+                        used |= 1u << i;
                     };
                     while (next_unit()) {
                         const VlUnit u = units[uslot].u;
@@ -490,7 +513,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                         kt[0] = kt[1] = take();
                         if (!ok) continue;
 #pragma unroll
-                        for (int h = 0; h < kSubs; ++h) {
+                        for (int h = 0; h < 2; ++h) {
                             issue_s(0, 0, kt[0], h);
                             if (pair) issue_s(1, 1, kt[0], h);
                         }
@@ -499,31 +522,41 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             kt[1] = take();
                             if (!ok) continue;
 #pragma unroll
-                            for (int h = 0; h < kSubs; ++h) issue_s(1, 0, kt[1], h);
+                            for (int h = 0; h < 2; ++h) issue_s(1, 0, kt[1], h);
                             if (el) umma_commit(empty_bar(kt[1]));
                         }
                         const int step = pair ? 1 : 2;
                         for (int jj = 0; ok && jj < n; jj += step) {
 #pragma unroll
-                            for (int h = 0; h < kSubs; ++h)
-#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                // (both unrolled, this warp's registers are too few for it: 2.80 ms against 2.47)
+#pragma unroll 1
                                 for (int i = 0; i < 2; ++i) {
                                     const int j = pair ? jj : jj + i;
                                     if (!ok || j >= n) continue;
-                                    const bool fetch = h == 0 && (!pair || i == 0), last = h == kSubs - 1 && (!pair || i == 1);
-                                    if (fetch) vt[i] = take();
-                                    const int v = vt[pair ? 0 : i];
+                                    const bool odd = !pair && i;
+                                    const bool fetch = h == 0 && (!pair || i == 0), last = h == 1 && (!pair || i == 1);
+                                    if (fetch) {
+                                        const int t = take();
+                                        if (odd) vt[1] = t;
+                                        else vt[0] = t;
+                                    }
+                                    const int v = odd ? vt[1] : vt[0];
                                     if (jj == 0 && h == 0) claim(i);
                                     issue_pv(i, v, jj == 0 && h == 0, steps(j), h);
                                     if (!ok) continue;
                                     if (last && el) umma_commit(empty_bar(v));
                                     if (j + step < n) {
-                                        if (fetch) kt[i] = take();
+                                        if (fetch) {
+                                            const int t = take();
+                                            if (odd) kt[1] = t;
+                                            else kt[0] = t;
+                                        }
                                         if (!ok) continue;
-                                        const int k = kt[pair ? 0 : i];
+                                        const int k = odd ? kt[1] : kt[0];
                                         issue_s(i, pair ? i : 0, k, h);
                                         if (last && el) umma_commit(empty_bar(k));
-                                    } else if (h == kSubs - 1) {
+                                    } else if (h == 1) {
                                         if (el) umma_commit(ofull_bar(i));
                                     }
                                 }
@@ -627,6 +660,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
             const int quarter = warp & 3;
             const int ur = kQuad ? lane : r;           // row of the unit's tile
             const int tr = ur / G;                     // and its token
+            // u: one more for every doubling of what a sequence may hold past 2^16
+            const float log_w = fminf(kWeightLogMost, kWeightLog + (float)max(0, 16 - __clz(p.max_kv - 1)));
             uint32_t sphase = 0, ophase0 = 0, ophase1 = 0;
             bool have_ends = false;
             unsigned ring = 0;                         // tiles that went through the ring before this unit
@@ -720,7 +755,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
 #pragma unroll
                         for (int e = 16; e < 30; e += 2) m2 = max3(m2, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                         const float xmax = qk * max3(m, m2, __uint_as_float(s[30]));
-                        float neg_m = weight_unit(m_used);
+                        float neg_m = weight_unit(log_w, m_used);
                         const float2 range = ts.range[quarter];
                         if (__any_sync(0xffffffffu, row_ok && may_pass(xmax, neg_m, range.x, m_used))) {
                             float top = xmax + range.x;
@@ -734,8 +769,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                 }
                                 top = fmaxf(t[0], t[1]);
                             }
-                            const float alpha = move_unit(row_ok, xmax, top, m_used);
-                            neg_m = weight_unit(m_used);
+                            const float alpha = move_unit(row_ok, xmax, top, log_w, m_used);
+                            neg_m = weight_unit(log_w, m_used);
                             l *= alpha;
                             if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                                 uint32_t o[D / 32][32];
@@ -752,12 +787,13 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             }
                         }
                         float ls[2] = {0.f, 0.f};
-                        uint32_t hi[8], lo[8];
+                        uint32_t t1[8], t2[8], t3[8];
                         const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
                         for (int c = 0; c < 4; ++c)
                             if (c != quarter) {
                                 tmem_st8(s_col + 8u * c, none);
                                 tmem_st8(s_col + 32u + 8u * c, none);
+                                tmem_st8(s_col + 64u + 8u * c, none);
                             }
 #pragma unroll
                         for (int g = 0; g < 8; ++g) {
@@ -768,13 +804,11 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                             ls[0] += x[0] + x[2];
                             ls[1] += x[1] + x[3];
                             const __half2 v0 = __floats2half2_rn(x[0] * f.x, x[1] * f.y), v1 = __floats2half2_rn(x[2] * f.z, x[3] * f.w);
-                            __half2 h0, h1;
-                            hi[g] = e4m3x4(v0, v1);
-                            halves_of_e4m3x4(hi[g], h0, h1);
-                            lo[g] = e4m3x4(__hsub2(v0, h0), __hsub2(v1, h1));
+                            three_terms(v0, v1, t1[g], t2[g], t3[g]);
                         }
-                        tmem_st8(s_col + 8u * quarter, hi);
-                        tmem_st8(s_col + 32u + 8u * quarter, lo);
+                        tmem_st8(s_col + 8u * quarter, t1);
+                        tmem_st8(s_col + 32u + 8u * quarter, t2);
+                        tmem_st8(s_col + 64u + 8u * quarter, t3);
                         l += ls[0] + ls[1];
                         tmem_st_wait();
                         tc_fence_before();
@@ -839,7 +873,7 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                     m4[i] = fmaxf(m, __uint_as_float(x[15]));
                                 }
                                 const float xmax = qk * fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-                                float neg_m = weight_unit(m_used);
+                                float neg_m = weight_unit(log_w, m_used);
                                 const float4 range = reinterpret_cast<const float4 *>(ts.range)[h];
                                 const float log_top = fmaxf(range.x, range.z);
                                 if (__any_sync(0xffffffffu, row_ok && may_pass(xmax, neg_m, log_top, m_used))) {
@@ -856,8 +890,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                         }
                                         top = fmaxf(t[0], t[1]);
                                     }
-                                    const float alpha = move_unit(row_ok, xmax, top, m_used);
-                                    neg_m = weight_unit(m_used);
+                                    const float alpha = move_unit(row_ok, xmax, top, log_w, m_used);
+                                    neg_m = weight_unit(log_w, m_used);
                                     l *= alpha;
                                     if ((j > j0 || h) && __any_sync(0xffffffffu, alpha != 1.f)) {
                                         // the part before this one has to be in O: the others are, their products went
@@ -879,8 +913,8 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                 const float2 qk2 = make_float2(qk, qk), nm2 = make_float2(neg_m, neg_m);
                                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                                 // the weights go over scores that have been read: the first terms in the part's
-                                // columns 0-15, the second in 16-31
-                                uint32_t hi[16], lo[16];
+                                // columns 0-15, the second in 16-31, the third in 32-47
+                                uint32_t t1[16], t2[16], t3[16];
 #pragma unroll
                                 for (int g = 0; g < 16; ++g) {
                                     const uint32_t *x = s[g >> 3] + 4 * (g & 7);
@@ -891,15 +925,11 @@ attn_varlen_tc8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_
                                     ls[0] = __fadd2_rn(ls[0], p0);
                                     ls[1] = __fadd2_rn(ls[1], p1);
                                     const float2 w0 = __fmul2_rn(p0, make_float2(y.x, y.y)), w1 = __fmul2_rn(p1, make_float2(y.z, y.w));
-                                    // (in f16, 2^-11 off at most; the first term's rest is exact there)
-                                    const __half2 v0 = __floats2half2_rn(w0.x, w0.y), v1 = __floats2half2_rn(w1.x, w1.y);
-                                    __half2 h0, h1;
-                                    hi[g] = e4m3x4(v0, v1);
-                                    halves_of_e4m3x4(hi[g], h0, h1);
-                                    lo[g] = e4m3x4(__hsub2(v0, h0), __hsub2(v1, h1));
+                                    three_terms(__floats2half2_rn(w0.x, w0.y), __floats2half2_rn(w1.x, w1.y), t1[g], t2[g], t3[g]);
                                 }
-                                tmem_st16(at, hi);
-                                tmem_st16(at + 16u, lo);
+                                tmem_st16(at, t1);
+                                tmem_st16(at + 16u, t2);
+                                tmem_st16(at + 32u, t3);
                                 l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
                                 tmem_st_wait();
                             }

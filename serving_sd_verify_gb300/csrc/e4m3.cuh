@@ -21,21 +21,10 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
         " mov.b32 %0, {l, h};\n}\n" : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
 }
-// of four values as two pairs in f16
-__device__ __forceinline__ uint32_t e4m3x4(__half2 a, __half2 b) {
-    uint32_t r;
-    asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n"
-        " mov.b32 %0, {l, h};\n}\n" : "=r"(r) : "r"(*reinterpret_cast<uint32_t *>(&a)), "r"(*reinterpret_cast<uint32_t *>(&b)));
-    return r;
-}
 // and back, exact
-__device__ __forceinline__ void halves_of_e4m3x4(uint32_t codes, __half2 &a, __half2 &b) {
-    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
-        : "=r"(*reinterpret_cast<uint32_t *>(&a)), "=r"(*reinterpret_cast<uint32_t *>(&b)) : "r"(codes));
-}
 __device__ __forceinline__ float2 from_e4m3x2(uint16_t codes) {
     uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));     // exact
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 __device__ __forceinline__ float4 from_e4m3x4(uint32_t codes) {

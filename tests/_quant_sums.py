@@ -82,19 +82,19 @@ class Sequence:
         self.S, self.m = S, len(k)
         self.cache, self.table, self.k, self.v, self.vs = pages_of(k, v, page, torch.Generator().manual_seed(seed))
 
-    def run(self, q, tree, causal=True, masks=None):
-        S, m = self.S, self.m
+    def run(self, q, tree, causal=True, masks=None, max_kv=None):
+        S, m, most = self.S, self.m, max_kv or self.m
         n, Hq, D = q.shape
         Hkv = self.k.shape[1]
         i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
         out = torch.empty(n, Hq, D, dtype=q.dtype, device="cuda")
-        ws = S.workspace(S.sd_paged_attention_workspace_size(n, 1, n, Hq, Hkv, D, m))
+        ws = S.workspace(S.sd_paged_attention_workspace_size(n, 1, n, Hq, Hkv, D, most))
         kp, vp, ks, vs = self.cache
         if tree:
-            S.sd_paged_tree_attention(q.cuda(), kp, vp, self.table, torch.tensor(masks).cuda(), i32(0, n), i32(m), n, m, out, D ** -0.5,
+            S.sd_paged_tree_attention(q.cuda(), kp, vp, self.table, torch.tensor(masks).cuda(), i32(0, n), i32(m), n, most, out, D ** -0.5,
                                       ws, ks, vs)
         else:
-            S.sd_paged_attention_e4m3(q.cuda(), kp, vp, ks, vs, self.table, i32(0, n), i32(m), n, m, out, D ** -0.5, ws, causal=causal)
+            S.sd_paged_attention_e4m3(q.cuda(), kp, vp, ks, vs, self.table, i32(0, n), i32(m), n, most, out, D ** -0.5, ws, causal=causal)
         torch.cuda.synchronize()
         assert S.sd_last_attention_path()[0] == 2 and S.sd_fault_word() == 0
         return out
