@@ -181,7 +181,14 @@ bool weight(const at::Tensor *w, int64_t D, ScalarType type) {
     return !w || (w->dim() == 1 && w->size(0) == D && w->scalar_type() == type && (D <= 1 || w->stride(0) == 1));
 }
 
-PyObject *answer(sd_status s) { return PyLong_FromLong((long)s); }
+// Calls a C entry (none throws) without the interpreter's lock: a launch waits where the queue is full, and what it
+// waits for may need the lock.
+template <typename F, typename... A> PyObject *answer(F entry, A... args) {
+    PyThreadState *state = PyEval_SaveThread();
+    const sd_status s = entry(args...);
+    PyEval_RestoreThread(state);
+    return PyLong_FromLong((long)s);
+}
 
 // q q_out k k_out positions turns q_weight k_weight eps axes order layout magnitude
 PyObject *norm_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -199,10 +206,10 @@ PyObject *norm_rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
            N <= INT32_MAX && Hq <= INT32_MAX && Hk <= INT32_MAX && D <= INT32_MAX);
     x.current();
     if (!x.ok) Py_RETURN_NONE;
-    return answer(norm_rotary_fn(q->data_ptr(), q->stride(0), q->stride(1), qo->data_ptr(), qo->stride(0), qo->stride(1), ptr(k),
+    return answer(norm_rotary_fn, q->data_ptr(), q->stride(0), q->stride(1), qo->data_ptr(), qo->stride(0), qo->stride(1), ptr(k),
                                  k ? k->stride(0) : 0, k ? k->stride(1) : 0, ptr(ko), ko ? ko->stride(0) : 0, ko ? ko->stride(1) : 0,
                                  ptr(wq), ptr(wk), (float)eps, r.positions, r.stride, r.use, r.turns, (float)m, (int)N, (int)Hq, (int)Hk,
-                                 (int)D, r.rot, r.layout, (sd_dtype)dtype_of(*q), x.stream()));
+                                 (int)D, r.rot, r.layout, (sd_dtype)dtype_of(*q), x.stream());
 }
 
 // q k v q_out positions turns cu_q kv_len page_table k_pages v_pages k_scale v_scale q_weight k_weight eps axes order layout magnitude
@@ -226,10 +233,10 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
            Hq <= INT32_MAX);
     x.current();
     if (!x.ok) Py_RETURN_NONE;
-    return answer(append_fn(ptr(q), q ? q->stride(0) : 0, q ? q->stride(1) : 0, k->data_ptr(), v->data_ptr(), k->stride(0), k->stride(1),
+    return answer(append_fn, ptr(q), q ? q->stride(0) : 0, q ? q->stride(1) : 0, k->data_ptr(), v->data_ptr(), k->stride(0), k->stride(1),
                             ptr(qo), ptr(wq), ptr(wk), (float)eps, r.positions, r.stride, r.use, r.turns, (float)m, r.rot, r.layout,
                             static_cast<const int32_t *>(cu->data_ptr()), static_cast<const int32_t *>(kv->data_ptr()), &c.c,
-                            c.scaled ? &c.s : nullptr, (int)N, c.B, (int)Hq, (int)Hkv, (int)D, (sd_dtype)dtype_of(*k), x.stream()));
+                            c.scaled ? &c.s : nullptr, (int)N, c.B, (int)Hq, (int)Hkv, (int)D, (sd_dtype)dtype_of(*k), x.stream());
 }
 
 // q k_pages v_pages k_scale v_scale page_table tree_mask cu_q kv_len max_q max_kv out scale ws causal (tree_mask None: no tree)
@@ -253,12 +260,12 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!x.ok) Py_RETURN_NONE;
     const int32_t *cup = static_cast<const int32_t *>(cu->data_ptr()), *kvp = static_cast<const int32_t *>(kv->data_ptr());
     if (mask)
-        return answer(tree_fn(q->data_ptr(), q->stride(0), q->stride(1), &c.c, c.scaled ? &c.s : nullptr,
+        return answer(tree_fn, q->data_ptr(), q->stride(0), q->stride(1), &c.c, c.scaled ? &c.s : nullptr,
                               static_cast<const uint64_t *>(mask->data_ptr()), cup, kvp, max_q, max_kv, out->data_ptr(), (int)N, c.B,
-                              (int)Hq, c.Hkv, (int)D, (sd_dtype)dtype_of(*q), (float)scale, ws->data_ptr(), ws->nbytes(), x.stream()));
-    return answer(attention_fn(q->data_ptr(), q->stride(0), q->stride(1), &c.c, &c.s, cup, kvp, max_q, max_kv, out->data_ptr(), (int)N,
+                              (int)Hq, c.Hkv, (int)D, (sd_dtype)dtype_of(*q), (float)scale, ws->data_ptr(), ws->nbytes(), x.stream());
+    return answer(attention_fn, q->data_ptr(), q->stride(0), q->stride(1), &c.c, &c.s, cup, kvp, max_q, max_kv, out->data_ptr(), (int)N,
                                c.B, (int)Hq, c.Hkv, (int)D, (sd_dtype)dtype_of(*q), (float)scale, causal ? 1 : 0, ws->data_ptr(),
-                               ws->nbytes(), x.stream()));
+                               ws->nbytes(), x.stream());
 }
 
 // k_pages v_pages page_table ctx_len path n_accepted k_scale v_scale
@@ -275,9 +282,9 @@ PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
            path->scalar_type() == ScalarType::Int && path->is_contiguous());
     x.current();
     if (!x.ok) Py_RETURN_NONE;
-    return answer(compact_fn(&c.c, c.scaled ? &c.s : nullptr, static_cast<const int32_t *>(ctx->data_ptr()),
+    return answer(compact_fn, &c.c, c.scaled ? &c.s : nullptr, static_cast<const int32_t *>(ctx->data_ptr()),
                              static_cast<const int32_t *>(path->data_ptr()), static_cast<const int32_t *>(acc->data_ptr()), c.B,
-                             (int)path->size(1), c.Hkv, c.D, (sd_dtype)dt, x.stream()));
+                             (int)path->size(1), c.Hkv, c.D, (sd_dtype)dt, x.stream());
 }
 
 // bind(path of libsdverify.so): finds the entry points in the library that is already loaded
