@@ -3,7 +3,8 @@
 Each .cu under csrc/ is compiled in parallel to an object in _build/, then
 linked with the static CUDA runtime into serving_sd_verify_gb300/libsdverify.so.
 Beside them g++ compiles csrc/fast_calls.cpp, the Python binding's short way
-into the library, against the installed torch to _fast_calls.so.
+into the library, against the installed torch; the file's name carries torch's and
+Python's versions, so that another of either gets one of its own.
 The library links no libcuda: the one driver entry point it needs (tensor-map
 encoding) is fetched at run time through the runtime's driver-entry-point
 query, so the .so also loads on machines without a GPU driver.
@@ -22,7 +23,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsdverify.so")
-FAST = os.path.join(PKG, "_fast_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-I", os.path.join(ROOT, "include")]
@@ -39,16 +39,25 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return sources() + [os.path.join(CSRC, "fast_calls.cpp")] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        [os.path.join(ROOT, "include", "sd_verify.h"), os.path.abspath(__file__)]
+def fast_path() -> str:
+    """The short way's file for the torch and the Python at hand."""
+    import torch
+    abi = "cxx11" if torch._C._GLIBCXX_USE_CXX11_ABI else "cxx98"
+    return os.path.join(PKG, f"_fast_calls.torch{torch.__version__}-{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _newer(out: str, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps)
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(FAST)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(FAST))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
+                  [os.path.join(ROOT, "include", "sd_verify.h"), os.path.abspath(__file__)])
+
+
+def fast_up_to_date() -> bool:
+    return _newer(fast_path(), [os.path.join(CSRC, "fast_calls.cpp"), os.path.join(ROOT, "include", "sd_verify.h"),
+                                os.path.abspath(__file__)])
 
 
 def _build_fast() -> None:
@@ -58,19 +67,24 @@ def _build_fast() -> None:
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     lib = os.path.join(root, "lib")
-    tmp = FAST + f".tmp{os.getpid()}"
+    out = fast_path()
+    tmp = out + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(a for d in inc for a in ("-isystem", d)), os.path.join(CSRC, "fast_calls.cpp"), "-o", tmp, "-L" + lib,
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib, "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for fast_calls.cpp:\n{r.stderr}")
-    os.replace(tmp, FAST)
+    os.replace(tmp, out)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile and link; returns the path of the shared library."""
-    if not force and up_to_date():
+    stale = force or not up_to_date()
+    stale_fast = force or not fast_up_to_date()
+    if not stale:
+        if stale_fast:
+            _build_fast()
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -87,9 +101,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        fast = ex.submit(_build_fast)
+        fast = ex.submit(_build_fast) if stale_fast else None
         objs = list(ex.map(compile_one, sources()))
-        fast.result()
+        if fast:
+            fast.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

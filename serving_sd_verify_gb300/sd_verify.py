@@ -17,9 +17,11 @@ import warnings
 
 import torch
 
+from serving_sd_verify_gb300 import build
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsdverify.so")
-FAST_PATH = os.path.join(_HERE, "_fast_calls.so")
+FAST_PATH = build.fast_path()
 
 SD_OK, SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED, SD_ERR_WORKSPACE, SD_ERR_CUDA = range(5)
 SD_BF16, SD_FP32 = 0, 1
