@@ -4,7 +4,9 @@ Each .cu under csrc/ is compiled in parallel to an object in _build/, then
 linked with the static CUDA runtime into serving_sd_verify_gb300/libsdverify.so.
 Beside them g++ compiles csrc/fast_calls.cpp, the Python binding's short way
 into the library, against the installed torch; the file's name carries torch's and
-Python's versions, so that another of either gets one of its own.
+Python's versions, so that another of either gets one of its own.  Where that
+cannot be built (no g++, no headers, a torch without CUDA) a warning says so, and
+the binding does without it.
 The library links no libcuda: the one driver entry point it needs (tensor-map
 encoding) is fetched at run time through the runtime's driver-entry-point
 query, so the .so also loads on machines without a GPU driver.
@@ -16,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -78,13 +81,23 @@ def _build_fast() -> None:
     os.replace(tmp, out)
 
 
+def _try_build_fast() -> None:
+    try:
+        _build_fast()
+    except (ImportError, AttributeError, OSError, RuntimeError) as e:
+        warnings.warn(f"the binding's short way was not built: {e}", RuntimeWarning)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile and link; returns the path of the shared library."""
     stale = force or not up_to_date()
-    stale_fast = force or not fast_up_to_date()
+    try:
+        stale_fast = force or not fast_up_to_date()
+    except (ImportError, AttributeError):
+        stale_fast = True              # (no torch: said below)
     if not stale:
         if stale_fast:
-            _build_fast()
+            _try_build_fast()
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -101,7 +114,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        fast = ex.submit(_build_fast) if stale_fast else None
+        fast = ex.submit(_try_build_fast) if stale_fast else None
         objs = list(ex.map(compile_one, sources()))
         if fast:
             fast.result()

@@ -1,4 +1,4 @@
-"""Building: the binding's short way belongs to one torch and one Python."""
+"""Building: the binding's short way belongs to one torch and one Python, and the library is built without it."""
 import os
 import sysconfig
 
@@ -22,6 +22,16 @@ def test_another_torch_or_python_is_another_file(monkeypatch):
     monkeypatch.undo()
     monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-other.so")
     assert build.fast_path() not in (here, there) and not build.fast_up_to_date()
+
+
+@pytest.mark.parametrize("how", [ImportError("no torch"), FileNotFoundError("g++"), RuntimeError("cannot find -lc10_cuda")])
+def test_the_library_is_built_without_it(monkeypatch, tmp_path, how):
+    def fails():
+        raise how
+    monkeypatch.setattr(build, "fast_path", lambda: str(tmp_path / "missing.so"))
+    monkeypatch.setattr(build, "_build_fast", fails)
+    with pytest.warns(RuntimeWarning, match="short way"):
+        assert build.build() == build.LIB
 
 
 def test_it_alone_is_built_where_it_alone_is_missing(monkeypatch, tmp_path, recwarn):
