@@ -178,11 +178,11 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
         x = static_cast<const T *>(kRole == 0 ? p.q : kRole == 1 ? p.k : p.v) + (long)n0 * (kRole == 0 ? p.q_tok : p.k_tok);
         x_tok = kRole == 0 ? p.q_tok : p.k_tok;
         x_head = kRole == 0 ? p.q_head : p.k_head;
-        heads = kRole == 0 ? p.Hq : p.Hk;
-        rows = nt * heads;
+        heads = kRole ? p.Hk : kCache ? max(1, p.Hq) : p.Hq;      // (an append may have no queries: no rows, but a walk that divides)
+        rows = nt * (kRole == 0 ? p.Hq : p.Hk);
         step = step_;
         row = first;
-        t = heads ? (int)((unsigned)row / (unsigned)heads) : 0;
+        t = (int)((unsigned)row / (unsigned)heads);
         h = row - t * heads;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
