@@ -111,7 +111,6 @@ norm_rope_row_kernel(const __grid_constant__ NormRopeParams p, const long rows, 
 // 22.6, eight: 72.6, 84.1 and 18.4 with four tokens a CTA, which seven do in 69.9, 83.2
 // and 17.4).
 constexpr int kVecThreads = 128;
-constexpr int kRows = 1;             // of a lane in flight
 constexpr int kTokens = 8;           // of a CTA at most
 constexpr int kVecPairs = 256;       // of a row at most: 32 chunks of 8
 
@@ -148,29 +147,26 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
     long x_tok, x_head;
     int heads, rows, step;
     int row, t, h;                   // the next to load
-    uint4 a[kRows], b[kRows];
-    int rt[kRows], rh[kRows];
+    uint4 a, b;                      // the loaded one: its vectors, its token (-1 behind the last row) and head
+    int rt, rh;
 
     __device__ __forceinline__ void load(bool live, bool two, int oa, int ob) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            rt[i] = row < rows ? t : -1;
-            rh[i] = h;
-            if (row < rows) {
-                const T *src = x + t * x_tok + h * x_head;
-                if (live) a[i] = *reinterpret_cast<const uint4 *>(src + oa);
-                if (two) b[i] = *reinterpret_cast<const uint4 *>(src + ob);
-            }
-            row += step;
-            h += step;
+        rt = row < rows ? t : -1;
+        rh = h;
+        if (row < rows) {
+            const T *src = x + t * x_tok + h * x_head;
+            if (live) a = *reinterpret_cast<const uint4 *>(src + oa);
+            if (two) b = *reinterpret_cast<const uint4 *>(src + ob);
+        }
+        row += step;
+        h += step;
+        if (h >= heads) {
+            h -= heads;
+            ++t;
             if (h >= heads) {
-                h -= heads;
-                ++t;
-                if (h >= heads) {
-                    const int q = (int)((unsigned)h / (unsigned)heads);
-                    t += q;
-                    h -= q * heads;
-                }
+                const int q = (int)((unsigned)h / (unsigned)heads);
+                t += q;
+                h -= q * heads;
             }
         }
     }
@@ -184,8 +180,7 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
         row = first;
         t = (int)((unsigned)row / (unsigned)heads);
         h = row - t * heads;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+        a = b = make_uint4(0u, 0u, 0u, 0u);
     }
     __device__ __forceinline__ void run(const NormRopeParams &p, const VecShared &sh, int n0, int log_p, int rot_chunks, int c,
                                         bool live, bool two, int oa, int ob) {
@@ -202,97 +197,92 @@ template <typename T, bool kInter, int kCache, int kRole> struct Rows {
         // whole warps go through the loop, rows or not: sums over some of a warp's lanes under a mask of their
         // own would cost a synchronisation each (25,119 x 32 heads 77.7 us)
         const int width = 1 << log_p;
-        while (__any_sync(0xffffffffu, rt[0] >= 0)) {
-            uint4 ca[kRows], cb[kRows];
-            int ct[kRows], ch[kRows];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) { ca[i] = a[i]; cb[i] = b[i]; ct[i] = rt[i]; ch[i] = rh[i]; }
+        while (__any_sync(0xffffffffu, rt >= 0)) {
+            const uint4 ca = a, cb = b;
+            const int ct = rt, ch = rh;
             load(live, two, oa, ob);
+            const int tok = max(ct, 0);
+            const int *at = sh.place[tok];
+            const bool write = ct >= 0 && !(kCache && (kRole ? at[0] < 0 : at[0] == -2));
+            float2 fa[H], fb[H];
+            unpack2(ca, fa);
+            unpack2(cb, fb);
+            if (kRole < 2 && w) {
+                float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int tok = max(ct[i], 0);
-                const int *at = sh.place[tok];
-                const bool write = ct[i] >= 0 && !(kCache && (kRole ? at[0] < 0 : at[0] == -2));
-                float2 fa[H], fb[H];
-                unpack2(ca[i], fa);
-                unpack2(cb[i], fb);
-                if (kRole < 2 && w) {
-                    float2 s2 = make_float2(0.f, 0.f);
+                for (int e = 0; e < H; ++e) s2 = __ffma2_rn(fa[e], fa[e], s2);
+                if (!kInter)
 #pragma unroll
-                    for (int e = 0; e < H; ++e) s2 = __ffma2_rn(fa[e], fa[e], s2);
-                    if (!kInter)
+                    for (int e = 0; e < H; ++e) s2 = __ffma2_rn(fb[e], fb[e], s2);
+                float sum = s2.x + s2.y;
 #pragma unroll
-                        for (int e = 0; e < H; ++e) s2 = __ffma2_rn(fb[e], fb[e], s2);
-                    float sum = s2.x + s2.y;
+                for (int o = 1; o < 32; o <<= 1)
+                    if (o < width) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const float inv = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
+                const float2 i2 = make_float2(inv, inv);
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1)
-                        if (o < width) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    const float inv = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
-                    const float2 i2 = make_float2(inv, inv);
+                for (int e = 0; e < H; ++e) fa[e] = __fmul2_rn(__fmul2_rn(fa[e], i2), ga[e]);
+                if (!kInter)
 #pragma unroll
-                    for (int e = 0; e < H; ++e) fa[e] = __fmul2_rn(__fmul2_rn(fa[e], i2), ga[e]);
-                    if (!kInter)
+                    for (int e = 0; e < H; ++e) fb[e] = __fmul2_rn(__fmul2_rn(fb[e], i2), gb[e]);
+            }
+            if (turned) {
+                const float4 *angle = sh.angles[tok] + c;
+                if constexpr (kInter) {            // element pairs (a, b) side by side
 #pragma unroll
-                        for (int e = 0; e < H; ++e) fb[e] = __fmul2_rn(__fmul2_rn(fb[e], i2), gb[e]);
-                }
-                if (turned) {
-                    const float4 *angle = sh.angles[tok] + c;
-                    if constexpr (kInter) {            // element pairs (a, b) side by side
+                    for (int e = 0; e < H; e += 2) {
+                        const float4 cs = angle[(e >> 1) * rot_chunks];
+                        const float2 u = fa[e], v = fa[e + 1];
+                        fa[e] = make_float2(u.x * cs.x - u.y * cs.z, u.y * cs.x + u.x * cs.z);
+                        fa[e + 1] = make_float2(v.x * cs.y - v.y * cs.w, v.y * cs.y + v.x * cs.w);
+                    }
+                } else {
 #pragma unroll
-                        for (int e = 0; e < H; e += 2) {
-                            const float4 cs = angle[(e >> 1) * rot_chunks];
-                            const float2 u = fa[e], v = fa[e + 1];
-                            fa[e] = make_float2(u.x * cs.x - u.y * cs.z, u.y * cs.x + u.x * cs.z);
-                            fa[e + 1] = make_float2(v.x * cs.y - v.y * cs.w, v.y * cs.y + v.x * cs.w);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < H; ++e) {
-                            const float4 cs = angle[e * rot_chunks];
-                            const float2 co = make_float2(cs.x, cs.y), si = make_float2(cs.z, cs.w), u = fa[e], v = fb[e];
-                            fa[e] = __ffma2_rn(u, co, neg2(__fmul2_rn(v, si)));
-                            fb[e] = __ffma2_rn(u, si, __fmul2_rn(v, co));
-                        }
+                    for (int e = 0; e < H; ++e) {
+                        const float4 cs = angle[e * rot_chunks];
+                        const float2 co = make_float2(cs.x, cs.y), si = make_float2(cs.z, cs.w), u = fa[e], v = fb[e];
+                        fa[e] = __ffma2_rn(u, co, neg2(__fmul2_rn(v, si)));
+                        fb[e] = __ffma2_rn(u, si, __fmul2_rn(v, co));
                     }
                 }
-                if constexpr (kCache == 2 && kRole > 0) {
-                    float amax = 0.f;
-                    if (live)
+            }
+            if constexpr (kCache == 2 && kRole > 0) {
+                float amax = 0.f;
+                if (live)
 #pragma unroll
-                        for (int e = 0; e < H; ++e) amax = fmaxf(amax, fmaxf(fabsf(fa[e].x), fabsf(fa[e].y)));
-                    if (two)
+                    for (int e = 0; e < H; ++e) amax = fmaxf(amax, fmaxf(fabsf(fa[e].x), fabsf(fa[e].y)));
+                if (two)
 #pragma unroll
-                        for (int e = 0; e < H; ++e) amax = fmaxf(amax, fmaxf(fabsf(fb[e].x), fabsf(fb[e].y)));
+                    for (int e = 0; e < H; ++e) amax = fmaxf(amax, fmaxf(fabsf(fb[e].x), fabsf(fb[e].y)));
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1)
-                        if (o < width) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    const RowCodes code(amax);
-                    uint8_t *codes = static_cast<uint8_t *>(kRole == 1 ? p.k_pages : p.v_pages) + (long)at[1] * p.pages.b +
-                                     (long)at[2] * p.pages.s + (long)ch[i] * p.pages.h;
-                    auto put = [&](int o, const float2 (&f)[H]) {
-                        uint32_t q[V / 4];
+                for (int o = 1; o < 32; o <<= 1)
+                    if (o < width) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                const RowCodes code(amax);
+                uint8_t *codes = static_cast<uint8_t *>(kRole == 1 ? p.k_pages : p.v_pages) + (long)at[1] * p.pages.b +
+                                 (long)at[2] * p.pages.s + (long)ch * p.pages.h;
+                auto put = [&](int o, const float2 (&f)[H]) {
+                    uint32_t q[V / 4];
 #pragma unroll
-                        for (int e = 0; e < V / 4; ++e) {
-                            const float2 x = code(f[2 * e]), y = code(f[2 * e + 1]);
-                            q[e] = e4m3x4(x.x, x.y, y.x, y.y);
-                        }
-                        if constexpr (V == 8) *reinterpret_cast<uint2 *>(codes + o) = make_uint2(q[0], q[1]);
-                        else *reinterpret_cast<uint32_t *>(codes + o) = q[0];
-                    };
-                    if (live && write) put(oa, fa);
-                    if (two && write) put(ob, fb);
-                    if (c == 0 && write)
-                        (kRole == 1 ? p.k_scale : p.v_scale)[((long)at[1] * p.Hk + ch[i]) * p.page_size + at[2]] = e4m3_scale(amax);
-                } else {
-                    const long n = n0 + tok;
-                    T *y = kRole == 0  ? static_cast<T *>(p.q_out) + n * p.qo_tok + ch[i] * p.qo_head
-                           : !kCache ? static_cast<T *>(p.k_out) + n * p.ko_tok + ch[i] * p.ko_head
-                                     : static_cast<T *>(kRole == 1 ? p.k_pages : p.v_pages) + (long)at[1] * p.pages.b +
-                                           (long)at[2] * p.pages.s + (long)ch[i] * p.pages.h;
-                    // (values bit for bit)
-                    if (live && write) *reinterpret_cast<uint4 *>(y + oa) = kRole == 2 ? ca[i] : pack2(fa);
-                    if (two && write) *reinterpret_cast<uint4 *>(y + ob) = kRole == 2 ? cb[i] : pack2(fb);
-                }
+                    for (int e = 0; e < V / 4; ++e) {
+                        const float2 x = code(f[2 * e]), y = code(f[2 * e + 1]);
+                        q[e] = e4m3x4(x.x, x.y, y.x, y.y);
+                    }
+                    if constexpr (V == 8) *reinterpret_cast<uint2 *>(codes + o) = make_uint2(q[0], q[1]);
+                    else *reinterpret_cast<uint32_t *>(codes + o) = q[0];
+                };
+                if (live && write) put(oa, fa);
+                if (two && write) put(ob, fb);
+                if (c == 0 && write)
+                    (kRole == 1 ? p.k_scale : p.v_scale)[((long)at[1] * p.Hk + ch) * p.page_size + at[2]] = e4m3_scale(amax);
+            } else {
+                const long n = n0 + tok;
+                T *y = kRole == 0  ? static_cast<T *>(p.q_out) + n * p.qo_tok + ch * p.qo_head
+                       : !kCache ? static_cast<T *>(p.k_out) + n * p.ko_tok + ch * p.ko_head
+                                 : static_cast<T *>(kRole == 1 ? p.k_pages : p.v_pages) + (long)at[1] * p.pages.b +
+                                       (long)at[2] * p.pages.s + (long)ch * p.pages.h;
+                // (values bit for bit)
+                if (live && write) *reinterpret_cast<uint4 *>(y + oa) = kRole == 2 ? ca : pack2(fa);
+                if (two && write) *reinterpret_cast<uint4 *>(y + ob) = kRole == 2 ? cb : pack2(fb);
             }
         }
     }
