@@ -613,7 +613,8 @@ sd_status sd_prompt_attention(const void *q, int64_t q_tok, int64_t q_head, cons
  *   q_weight, k_weight  device [D] of the inputs' type, aligned to it, or NULL
  *   eps        >= 0, finite
  *   the rest as for sd_rotary
- * The squares are summed in fp32 (elements up to about 1e18).  Rows of non-finite
+ * The squares are summed in fp32 (elements up to about 1e18, and with eps = 0 from
+ * about 1e-18 on).  Rows of non-finite
  * values, and with eps = 0 rows of zeros, give NaN as the formula does; no other
  * row is touched by them.
  * ------------------------------------------------------------------------ */
@@ -668,7 +669,7 @@ sd_status sd_norm_rotary_append_paged(const void *q, int64_t q_tok, int64_t q_he
  * sd_paged_attention's.
  * bf16 over pages of a multiple of 8 slots runs on the tensor cores, in e4m3: q as
  * the sum of two e4m3 terms (exact for elements above 2^-9 of their row's
- * largest, off by 2^-18 of that largest below), a weight times its value's scale in
+ * largest, off by 2^-17 of that largest below), a weight times its value's scale in
  * f16 and that as three e5m2 terms (off by 2^-9 of itself; where it is small it may be
  * dropped, which takes 2^-8 of their sum from a row's weights at most, for max_kv up to
  * 2^21, however they lie), fp32 sums.  What a row does not see takes no part in it,

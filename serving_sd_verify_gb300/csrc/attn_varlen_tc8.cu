@@ -10,17 +10,18 @@
 //   P_n = 2^u exp2(x_n - m),  l = sum P_n,  W_n = P_n v_n,  O = (W1 + W2 + W3) V,  out = O / l
 //   Q: a row times a power of two that brings its largest element to [128, 256), as
 //     a first e4m3 term and, exactly, what that leaves: a bf16 element has 8 bits and
-//     each term holds 4, so the two are the element itself where it is above 2^-10
-//     of the row's largest, and off by 2^-18 of the largest where not.  c is that
+//     each term holds 4, so the two are the element itself where it is above 2^-9
+//     of the row's largest, and off by 2^-17 of the largest where not.  c is that
 //     power's inverse times scale log2(e).
 //   m: of what the keys contribute, their values' scales among it: a row's weights are
 //     written against nothing but what the row itself sees, and neither a value that it
 //     does not see, however large, nor one that it sees of small values, however large
 //     its score, takes precision from the others.  It moves where a weight would pass
-//     what two terms hold (max x and the part's largest scale tell that none does, mostly),
+//     what the terms hold (max x and the part's largest scale tell that none does, mostly),
 //     to max x and that scale where all the part's keys are seen and their scales are alike,
-//     else to the keys' own (a third reading of each key's scales, which always done
-//     made 2,048 over 32,768 2.77 ms; weights made first and looked over behind: 2.7 to 2.9).
+//     else to the keys' own (with two e4m3 terms, 2,048 over 32,768 2.17 ms; the keys' own
+//     always, a third reading of each key's scales, 2.77; weights made first and looked
+//     over behind 2.7 to 2.9).
 //   W: in f16, and that in three e5m2 terms of 3 bits each (an e5m2 code is the upper
 //     byte of an f16 value): off by 2^-9 of itself, or by 2^-17 where it is small.  With u
 //     of 9 that is 2^-24 of the row's largest, so that a long rest far below one large
@@ -28,7 +29,7 @@
 //     together at most, and for longer caches u grows with them.  (Two e4m3 terms end
 //     at 2^-10 and 2^-14 of the largest: with one key 12 nats above 32,768 others a third
 //     of the output went; one in e4m3 and one in e5m2 with m moved down where the
-//     small ones had lost too much: 2.69 ms and twice the error.)
+//     small ones had lost too much: 2.69 ms, error 2.1e-3 for 1.73e-3.)
 // l takes P before any rounding.
 //
 // Warps as in attn_varlen_tc.cu, except that the softmax warps split and write Q

@@ -102,7 +102,7 @@ norm_rope_row_kernel(const __grid_constant__ NormRopeParams p, const long rows, 
 // past the turned ones.  The next rows' loads are in flight while a row's sums meet by
 // shuffles among its lanes.  Arithmetic comes two elements an instruction: what bounds
 // the kernel besides memory is the instructions it issues.
-// Measured (bf16, three axes): 25,119 tokens of 32 heads of 128 69.5 us (5.9 TB/s of 6.8),
+// Measured (bf16, three axes): 25,119 tokens of 32 heads of 128 69.3 us (5.9 TB/s of 6.8),
 // of 28 with 8 written as e4m3 80.2 us (5.5 TB/s), 2,048 tokens of 80 into a bf16 cache
 // 17.4 us (4.8 TB/s).  A lane group with angles of its own for four heads took 97, 171 and
 // 26 us, two rows in flight a lane 99, 126 and 26 (registers for five CTAs an SM only), one
