@@ -42,11 +42,15 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _cxx11_abi() -> int:
+    import torch
+    return int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))
+
+
 def fast_path() -> str:
     """The short way's file for the torch and the Python at hand."""
     import torch
-    abi = "cxx11" if torch._C._GLIBCXX_USE_CXX11_ABI else "cxx98"
-    return os.path.join(PKG, f"_fast_calls.torch{torch.__version__}-{abi}{sysconfig.get_config_var('EXT_SUFFIX')}")
+    return os.path.join(PKG, f"_fast_calls.torch{torch.__version__}-abi{_cxx11_abi()}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _newer(out: str, deps) -> bool:
@@ -72,7 +76,7 @@ def _build_fast() -> None:
     lib = os.path.join(root, "lib")
     out = fast_path()
     tmp = out + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={_cxx11_abi()}",
            *(a for d in inc for a in ("-isystem", d)), os.path.join(CSRC, "fast_calls.cpp"), "-o", tmp, "-L" + lib,
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib, "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
